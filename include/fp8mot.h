@@ -104,6 +104,23 @@ typedef enum {
   FP8MOT_ACC_FP8_MFMA = 1
 } fp8mot_acc;
 
+/* Element type of the float tensors that come in two: the bias and residual
+ * of fp8_linear_act and the layer norm's inputs. */
+typedef enum {
+  FP8MOT_ELEM_BF16 = 0, /* uint16_t bit patterns */
+  FP8MOT_ELEM_F32 = 1   /* float */
+} fp8mot_elem;
+
+/* Activation of fp8_linear_act, evaluated in FP32.  At z = -Inf gelu,
+ * gelu_tanh and silu give the NaN of -Inf * 0; a NaN stays a NaN. */
+typedef enum {
+  FP8MOT_ACT_NONE = 0,      /* z */
+  FP8MOT_ACT_RELU = 1,      /* max(z, 0) */
+  FP8MOT_ACT_GELU = 2,      /* z * Phi(z), Phi the normal distribution function */
+  FP8MOT_ACT_GELU_TANH = 3, /* z * (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+  FP8MOT_ACT_SILU = 4       /* z / (1 + exp(-z)) */
+} fp8mot_act;
+
 /* Observer mode of fp8_observe. */
 typedef enum {
   FP8MOT_OBS_MAX = 0,       /* running max of the per-call amax */
@@ -294,6 +311,111 @@ int fp8_quant_per_row(const uint16_t* x, uint8_t* q, float* d_scales,
 int fp8_linear_rowwise(const uint8_t* qx, const uint8_t* qw, void* y, int64_t M,
                        int64_t N, int64_t K, const float* d_sx, const float* d_sw,
                        int out_kind, int accum, hipStream_t stream);
+
+/* ------------------------------------------------------------------ */
+/* Linear epilogue: bias, activation, residual                         */
+/* ------------------------------------------------------------------ */
+
+/* Bytes of workspace fp8_linear_act needs: 0 for most shapes, FP32 partial
+ * sums where K is split over workgroups (few outputs, long K).  Depends on
+ * (M, N, K) only.  Returns 0 for negative sizes. */
+size_t fp8_linear_act_workspace(int64_t M, int64_t N, int64_t K);
+
+/* FP8 Linear with bias, activation and residual in its epilogue:
+ *   acc[m,n] = sum_k e4m3_value(qx[m,k]) * e4m3_value(qw[n,k])
+ *   z        = fp32(acc * alpha) + bias[n],  alpha = fp32(s_x * s_w)
+ *   v        = act(z) + residual[m,n]
+ *   y[m,n]   = bf16_rne(v) | e4m3(v / *d_sy) | v    per out_kind
+ * each step one FP32 operation; NULL bias or residual leaves its addition
+ * out.  The bias of a projection, the activation of an ungated MLP and the
+ * residual stream's addition after o and down are what a decoder layer does
+ * to a projection's output; here no pass over [M, N] is spent on them.
+ *  - row_scales 0: d_sx, d_sw one scale each, as fp8_linear; row_scales 1:
+ *    d_sx [M] and d_sw [N], alpha[m,n] = fp32(d_sx[m] * d_sw[n]), as
+ *    fp8_linear_rowwise.
+ *  - bias: [N] of bias_elem (fp8mot_elem); residual: [M, N] of residual_elem.
+ *  - pre: NULL, or BF16 [M, N] that receives bf16_rne(z), which the backward
+ *    pass needs.
+ *  - y may be the residual itself where the element types agree (the sum is
+ *    then added in place); no other overlap of y or pre with an input or
+ *    with each other.
+ *  - accum as fp8_linear.  Calls of few rows (M <= 64) are bound by the
+ *    weight's bytes and always sum as FP8MOT_ACC_EXACT does.
+ *  - ws: 16-byte aligned device workspace of at least
+ *    fp8_linear_act_workspace(M, N, K) bytes (may be NULL where that is 0).
+ *    Calls that may overlap need workspaces of their own.
+ * K == 0 gives act(bias) + residual.  The order of the FP32 sum depends on
+ * (M, N, K, accum) only; it is not fp8_linear's.  qx, qw, y, bias, residual,
+ * pre 16-byte aligned; row scales too.  M, N, K as in fp8_linear. */
+int fp8_linear_act(const uint8_t* qx, const uint8_t* qw, void* y, int64_t M, int64_t N,
+                   int64_t K, const float* d_sx, const float* d_sw, int row_scales,
+                   const void* bias, int bias_elem, int act, const void* residual,
+                   int residual_elem, uint16_t* pre, int out_kind, const float* d_sy,
+                   int accum, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Bytes of workspace fp8_linear_act_backward needs for dbias (column sums
+ * over slabs of rows).  Returns 0 for negative sizes. */
+size_t fp8_linear_act_backward_workspace(int64_t M, int64_t N);
+
+/* Backward pass of fp8_linear_act's epilogue: for the gradient dy of y,
+ *   dz[m,n]  = bf16_rne(dy * act'(pre)),   dbias[n] = sum_m dy * act'(pre)
+ * (the residual's gradient is dy itself).  The sum takes the FP32 products,
+ * before their rounding to BF16, in an order that depends on (M, N) only.
+ * dz goes on to the input's gradient through the frozen weight:
+ * fp8_quant_per_row and fp8_linear_rowwise on the transposed codes.
+ * dy, pre, dz: BF16 [M, N]; dbias: FP32 [N]; all 16-byte aligned.  dz or
+ * dbias may be NULL (not computed), and with FP8MOT_ACT_NONE pre too.  dz may
+ * be dy or pre itself.  relu's slope at 0 is 0.  M == 0 writes dbias = 0.
+ * ws: 16-byte aligned, at least fp8_linear_act_backward_workspace(M, N)
+ * bytes; unused where dbias is NULL. */
+int fp8_linear_act_backward(const uint16_t* dy, const uint16_t* pre, int act, uint16_t* dz,
+                            float* dbias, int64_t M, int64_t N, void* ws, size_t ws_bytes,
+                            hipStream_t stream);
+
+/* ------------------------------------------------------------------ */
+/* Layer norm                                                          */
+/* ------------------------------------------------------------------ */
+
+/* Layer norm of each row of x, with direct FP8 emission for the projections
+ * that read it (one quantized tensor for a group that shares its input scale,
+ * as silu_mul_2in_fp8 emits the down projection's input):
+ *   mean = sum_i x[i] / H,   var = sum_i (x[i] - mean)^2 / H
+ *   rstd = 1 / sqrt(var + eps)
+ *   v    = (x[i] - mean) * rstd * weight[i] + bias[i]       (FP32)
+ *   y[i] = bf16_rne(v) | e4m3(v / *d_sy) | v    per out_kind
+ * x: [rows, H] of x_elem (fp8mot_elem); weight, bias: [H] of wb_elem, either
+ * may be NULL (ones, zeros); y: [rows, H]; mean, rstd: FP32 [rows] for the
+ * backward pass, or NULL.  eps finite and >= 0.  y may be x itself where the
+ * element types agree; no other overlap.  Any H >= 0; x, y, weight, bias
+ * 16-byte aligned.  A row that holds a NaN or an infinity becomes NaN. */
+int fp8_layer_norm(const void* x, int x_elem, const void* weight, const void* bias,
+                   int wb_elem, void* y, int out_kind, const float* d_sy, float* mean,
+                   float* rstd, int64_t rows, int64_t H, float eps, hipStream_t stream);
+
+/* Bytes of workspace fp8_layer_norm_backward needs for dweight and dbias
+ * (column sums over slabs of rows).  Returns 0 for negative sizes. */
+size_t fp8_layer_norm_backward_workspace(int64_t rows, int64_t H);
+
+/* Backward pass of fp8_layer_norm, for the gradient dy of y (an FP8 y passes
+ * its gradient straight through):
+ *   xh = (x - mean) * rstd,   g = dy * weight
+ *   dx = rstd * (g - sum_i g / H - xh * sum_i(g * xh) / H) + dres
+ *   dweight[i] = sum_rows dy * xh,   dbias[i] = sum_rows dy
+ * mean, rstd: what fp8_layer_norm wrote.  dres: NULL, or the gradient that
+ * reaches x past the norm (the residual stream's), added before dx is
+ * rounded.  dy: of dy_elem; x, dres, dx: of x_elem; weight: [H] of w_elem or
+ * NULL (ones); dweight, dbias: FP32 [H], either may be NULL (not computed).
+ * dx may be dy or dres itself where the element types agree, or x; no other
+ * overlap.  rows == 0 writes dweight = dbias = 0.  The sums over rows take an
+ * order that depends on (rows, H) only.  All tensors 16-byte aligned but
+ * mean and rstd.  ws: 16-byte aligned, at least
+ * fp8_layer_norm_backward_workspace(rows, H) bytes; unused where dweight and
+ * dbias are NULL. */
+int fp8_layer_norm_backward(const void* dy, int dy_elem, const void* x, int x_elem,
+                            const void* weight, int w_elem, const float* mean,
+                            const float* rstd, const void* dres, void* dx, float* dweight,
+                            float* dbias, int64_t rows, int64_t H, void* ws, size_t ws_bytes,
+                            hipStream_t stream);
 
 /* ------------------------------------------------------------------ */
 /* Fused-topology comparison (what the split path avoids)              */

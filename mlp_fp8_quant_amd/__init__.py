@@ -6,11 +6,15 @@ PyTorch binding with the same names.  The library is loaded on first use and
 its absence is an error -- there is no CPU path.
 """
 
-from .api import (ACC_EXACT, ACC_FP8_MFMA, CONV_BF16, CONV_E4M3_INT,  # noqa: F401
+from .api import (ACC_EXACT, ACC_FP8_MFMA, ACT_GELU, ACT_GELU_TANH, ACT_NONE,  # noqa: F401
+                  ACT_RELU, ACT_SILU, CONV_BF16, CONV_E4M3_INT,
                   CONV_E4M3_PACKED, OBS_MAX,
                   OBS_MOVING_AVG, OUT_BF16, OUT_F32,
                   OUT_FP8, Fp8motError, debug_quant_launches,
-                  convert_f32, fp8_check_shared_scale, fp8_gate_up_swiglu, fp8_linear,
+                  convert_f32, fp8_check_shared_scale, fp8_gate_up_swiglu, fp8_layer_norm,
+                  fp8_layer_norm_backward, fp8_layer_norm_backward_workspace, fp8_linear,
+                  fp8_linear_act, fp8_linear_act_backward,
+                  fp8_linear_act_backward_workspace, fp8_linear_act_workspace,
                   fp8_linear_into, fp8_linear_rowwise, fp8_quant_per_row,
                   fp8_requantize_onto_max,
                   fp8_observe,

@@ -30,6 +30,22 @@ SIGNATURES = {
     "fp8_quant_per_row": (c_int, [c_void_p, c_void_p, c_void_p, c_i64, c_i64, c_void_p]),
     "fp8_linear_rowwise": (c_int, [c_void_p, c_void_p, c_void_p, c_i64, c_i64, c_i64,
                                    c_void_p, c_void_p, c_int, c_int, c_void_p]),
+    "fp8_linear_act_workspace": (c_size_t, [c_i64, c_i64, c_i64]),
+    "fp8_linear_act": (c_int, [c_void_p, c_void_p, c_void_p, c_i64, c_i64, c_i64,
+                               c_void_p, c_void_p, c_int, c_void_p, c_int, c_int,
+                               c_void_p, c_int, c_void_p, c_int, c_void_p, c_int,
+                               c_void_p, c_size_t, c_void_p]),
+    "fp8_linear_act_backward_workspace": (c_size_t, [c_i64, c_i64]),
+    "fp8_linear_act_backward": (c_int, [c_void_p, c_void_p, c_int, c_void_p, c_void_p,
+                                        c_i64, c_i64, c_void_p, c_size_t, c_void_p]),
+    "fp8_layer_norm": (c_int, [c_void_p, c_int, c_void_p, c_void_p, c_int, c_void_p, c_int,
+                               c_void_p, c_void_p, c_void_p, c_i64, c_i64, c_float,
+                               c_void_p]),
+    "fp8_layer_norm_backward_workspace": (c_size_t, [c_i64, c_i64]),
+    "fp8_layer_norm_backward": (c_int, [c_void_p, c_int, c_void_p, c_int, c_void_p, c_int,
+                                        c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                        c_void_p, c_i64, c_i64, c_void_p, c_size_t,
+                                        c_void_p]),
     "fp8_linear_ldc": (c_int, [c_void_p, c_void_p, c_void_p, c_i64, c_i64, c_i64, c_i64,
                                c_void_p, c_void_p, c_int, c_void_p, c_int, c_void_p]),
     "fp8_requantize_onto_max": (c_int, [c_void_p, c_void_p, c_i64, c_void_p, c_void_p,

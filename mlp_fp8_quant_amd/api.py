@@ -21,8 +21,10 @@ from ._lib import Fp8motError  # noqa: F401
 
 OUT_BF16, OUT_FP8, OUT_F32 = 0, 1, 2
 ACC_EXACT, ACC_FP8_MFMA = 0, 1
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
 OBS_MAX, OBS_MOVING_AVG = 0, 1
 CONV_E4M3_PACKED, CONV_E4M3_INT, CONV_BF16 = 0, 1, 2
+_ELEM = {torch.bfloat16: 0, torch.float32: 1}     # FP8MOT_ELEM_*
 _OUT_DTYPE = {OUT_BF16: torch.bfloat16, OUT_FP8: torch.uint8, OUT_F32: torch.float32}
 
 
@@ -165,6 +167,212 @@ def fp8_linear_rowwise(qx, qw, sx, sw, out_kind=OUT_BF16, out=None, accum=ACC_EX
     _lib.call("fp8_linear_rowwise", _ptr(qx), _ptr(qw), _ptr(out), M, N, K,
               _ptr(sx), _ptr(sw), out_kind, accum, _stream(qx))
     return out
+
+
+def _need_float(t, name, device=None, dtype=None):
+    """A BF16 or FP32 tensor (``dtype`` where only one of them fits); returns
+    its FP8MOT_ELEM code (0 for None)."""
+    if t is None:
+        return 0
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _ELEM or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must be {dtype or 'torch.bfloat16 or torch.float32'}, got {t.dtype}")
+    _need(t, name, t.dtype, device)
+    return _ELEM[t.dtype]
+
+
+def _out_dtype(out_kind):
+    dtype = _OUT_DTYPE.get(out_kind)
+    if dtype is None:
+        raise ValueError("out_kind must be OUT_BF16, OUT_FP8 or OUT_F32")
+    return dtype
+
+
+def _opt_workspace(nbytes, device, ws):
+    # like _workspace, but a call that needs none gets none
+    return None if ws is None and nbytes == 0 else _workspace(nbytes, device, ws)
+
+
+def fp8_linear_act_workspace(M, N, K):
+    return int(_lib.lib().fp8_linear_act_workspace(M, N, K))
+
+
+def fp8_linear_act(qx, qw, sx, sw, bias=None, act=ACT_NONE, residual=None, out_kind=OUT_BF16,
+                   sy=None, rowwise=False, pre=False, out=None, accum=ACC_EXACT, workspace=None):
+    """y = act((qx . qw^T) * scale + bias) + residual in one pass, with
+    qx [..., K] and qw [N, K] E4M3 and y [..., N] BF16, FP32 or (at the scale
+    ``sy``) E4M3 codes.
+
+    ``act``: ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH or ACT_SILU.  ``bias``
+    [N] and ``residual`` [..., N] are BF16 or FP32; ``out`` may be the residual
+    itself where the types agree.  ``rowwise``: sx holds one scale per row of
+    qx and sw one per row of qw (as fp8_linear_rowwise); else one scale each.
+    ``pre``: True, or a BF16 tensor [..., N], keeps the activation's argument
+    for fp8_linear_act_backward and makes the call return (y, pre)."""
+    _need(qx, "qx", torch.uint8)
+    dev = qx.device
+    _need(qw, "qw", torch.uint8, dev)
+    if qw.dim() != 2 or qx.dim() < 1 or qx.shape[-1] != qw.shape[1]:
+        raise ValueError("shapes: qx [..., K], qw [N, K]")
+    N, K = qw.shape
+    M = math.prod(qx.shape[:-1])
+    if rowwise:
+        _need(sx, "sx", torch.float32, dev)
+        _need(sw, "sw", torch.float32, dev)
+        if sx.numel() != M or sw.numel() != N:
+            raise ValueError("sx must hold one scale per row of qx and sw one per row of qw")
+    else:
+        _scale(sx, "sx", dev)
+        _scale(sw, "sw", dev)
+    dtype = _out_dtype(out_kind)
+    if out_kind == OUT_FP8:
+        _scale(sy, "sy", dev)
+    bias_elem = _need_float(bias, "bias", dev)
+    if bias is not None and bias.numel() != N:
+        raise ValueError("bias must hold N elements")
+    res_elem = _need_float(residual, "residual", dev)
+    if residual is not None and residual.numel() != M * N:
+        raise ValueError("residual must hold M * N elements")
+    shape = (*qx.shape[:-1], N)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    _need(out, "out", dtype, dev)
+    if out.numel() != M * N:
+        raise ValueError("out must hold M * N elements")
+    keep = None
+    if pre is not False and pre is not None:
+        keep = torch.empty(shape, dtype=torch.bfloat16, device=dev) if pre is True else pre
+        _need(keep, "pre", torch.bfloat16, dev)
+        if keep.numel() != M * N:
+            raise ValueError("pre must hold M * N elements")
+    nb = fp8_linear_act_workspace(M, N, K)
+    ws = _opt_workspace(nb, dev, workspace)
+    _lib.call("fp8_linear_act", _ptr(qx), _ptr(qw), _ptr(out), M, N, K, _ptr(sx), _ptr(sw),
+              int(bool(rowwise)), _ptr(bias), bias_elem, act, _ptr(residual), res_elem,
+              _ptr(keep), out_kind, _ptr(sy) if out_kind == OUT_FP8 else None, accum,
+              _ptr(ws), ws.numel() if ws is not None else 0, _stream(qx))
+    return out if keep is None else (out, keep)
+
+
+def fp8_linear_act_backward_workspace(M, N):
+    return int(_lib.lib().fp8_linear_act_backward_workspace(M, N))
+
+
+def fp8_linear_act_backward(dy, pre, act=ACT_NONE, dz=None, dbias=None, workspace=None):
+    """Backward pass of fp8_linear_act's epilogue: (dz, dbias) with
+    dz = dy * act'(pre) (BF16, shaped as dy [..., N]) and dbias its sum over
+    rows (FP32 [N], summed before the rounding of dz).  ``pre`` is what
+    fp8_linear_act kept (None allowed for ACT_NONE); ``dz`` may be dy or pre
+    itself."""
+    _need(dy, "dy", torch.bfloat16)
+    dev = dy.device
+    if dy.dim() == 0:
+        raise ValueError("dy must have a last (N) dimension")
+    N = dy.shape[-1]
+    M = math.prod(dy.shape[:-1])
+    if pre is not None:
+        _need(pre, "pre", torch.bfloat16, dev)
+        if pre.numel() != M * N:
+            raise ValueError("pre must have as many elements as dy")
+    if dz is None:
+        dz = torch.empty(dy.shape, dtype=torch.bfloat16, device=dev)
+    if dbias is None:
+        dbias = torch.empty(N, dtype=torch.float32, device=dev)
+    _need(dz, "dz", torch.bfloat16, dev)
+    _need(dbias, "dbias", torch.float32, dev)
+    if dz.numel() != M * N or dbias.numel() != N:
+        raise ValueError("dz must have as many elements as dy and dbias N")
+    ws = _opt_workspace(fp8_linear_act_backward_workspace(M, N), dev, workspace)
+    _lib.call("fp8_linear_act_backward", _ptr(dy), _ptr(pre), act, _ptr(dz), _ptr(dbias), M, N,
+              _ptr(ws), ws.numel() if ws is not None else 0, _stream(dy))
+    return dz, dbias
+
+
+def fp8_layer_norm(x, weight=None, bias=None, eps=1e-5, out_kind=OUT_BF16, sy=None, stats=False,
+                   out=None):
+    """Layer norm over the last dimension of x [..., H] (BF16 or FP32):
+    y = (x - mean) * rstd * weight + bias as BF16, FP32 or (at the scale
+    ``sy``) E4M3 codes for the Linears that read it.  weight and bias [H]:
+    both BF16 or both FP32, or None.  ``stats`` makes the call return
+    (y, mean, rstd), FP32 [...], for fp8_layer_norm_backward.  ``out`` may be
+    x itself where the types agree."""
+    x_elem = _need_float(x, "x")
+    if x is None or x.dim() == 0:
+        raise ValueError("x must be a tensor with a last (H) dimension")
+    dev = x.device
+    H = x.shape[-1]
+    rows = math.prod(x.shape[:-1])
+    wb_elem = _need_float(weight, "weight", dev)
+    b_elem = _need_float(bias, "bias", dev, weight.dtype if weight is not None else None)
+    for t, n in ((weight, "weight"), (bias, "bias")):
+        if t is not None and t.numel() != H:
+            raise ValueError(f"{n} must hold H elements")
+    dtype = _out_dtype(out_kind)
+    if out_kind == OUT_FP8:
+        _scale(sy, "sy", dev)
+    if out is None:
+        out = torch.empty(x.shape, dtype=dtype, device=dev)
+    _need(out, "out", dtype, dev)
+    if out.numel() != rows * H:
+        raise ValueError("out must have as many elements as x")
+    mean = rstd = None
+    if stats:
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    _lib.call("fp8_layer_norm", _ptr(x), x_elem, _ptr(weight), _ptr(bias),
+              wb_elem if weight is not None else b_elem, _ptr(out), out_kind,
+              _ptr(sy) if out_kind == OUT_FP8 else None, _ptr(mean), _ptr(rstd), rows, H,
+              float(eps), _stream(x))
+    return (out, mean, rstd) if stats else out
+
+
+def fp8_layer_norm_backward_workspace(rows, H):
+    return int(_lib.lib().fp8_layer_norm_backward_workspace(rows, H))
+
+
+def fp8_layer_norm_backward(dy, x, weight, mean, rstd, dres=None, dx=None, dweight=None,
+                            dbias=None, workspace=None):
+    """Backward pass of fp8_layer_norm: (dx, dweight, dbias) for the gradient
+    dy [..., H] (BF16 or FP32) of its output.  mean and rstd are what
+    fp8_layer_norm(stats=True) returned; ``dres`` (x's type) is the gradient
+    that reaches x past the norm and is added to dx before its rounding; dx
+    has x's type, dweight and dbias are FP32 [H]."""
+    x_elem = _need_float(x, "x")
+    if x is None or x.dim() == 0:
+        raise ValueError("x must be a tensor with a last (H) dimension")
+    dev = x.device
+    H = x.shape[-1]
+    rows = math.prod(x.shape[:-1])
+    if dy is None:
+        raise ValueError("dy must be a tensor")
+    dy_elem = _need_float(dy, "dy", dev)
+    w_elem = _need_float(weight, "weight", dev)
+    _need_float(dres, "dres", dev, x.dtype)
+    _need(mean, "mean", torch.float32, dev)
+    _need(rstd, "rstd", torch.float32, dev)
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    if dweight is None:
+        dweight = torch.empty(H, dtype=torch.float32, device=dev)
+    if dbias is None:
+        dbias = torch.empty(H, dtype=torch.float32, device=dev)
+    _need(dx, "dx", x.dtype, dev)
+    _need(dweight, "dweight", torch.float32, dev)
+    _need(dbias, "dbias", torch.float32, dev)
+    for t, n in ((dy, "dy"), (dres, "dres"), (dx, "dx")):
+        if t is not None and t.numel() != rows * H:
+            raise ValueError(f"{n} must have as many elements as x")
+    for t, n in ((weight, "weight"), (dweight, "dweight"), (dbias, "dbias")):
+        if t is not None and t.numel() != H:
+            raise ValueError(f"{n} must hold H elements")
+    if mean.numel() != rows or rstd.numel() != rows:
+        raise ValueError("mean and rstd must hold one value per row")
+    ws = _opt_workspace(fp8_layer_norm_backward_workspace(rows, H), dev, workspace)
+    _lib.call("fp8_layer_norm_backward", _ptr(dy), dy_elem, _ptr(x), x_elem, _ptr(weight), w_elem,
+              _ptr(mean), _ptr(rstd), _ptr(dres), _ptr(dx), _ptr(dweight), _ptr(dbias), rows, H,
+              _ptr(ws), ws.numel() if ws is not None else 0, _stream(x))
+    return dx, dweight, dbias
 
 
 def fp8_linear_into(qx, qw, sx, sw, out, col0=0, out_kind=OUT_BF16, sy=None,

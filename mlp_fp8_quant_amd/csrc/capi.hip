@@ -105,6 +105,15 @@ int check_linear(const uint8_t* qx, const uint8_t* qw, const void* y, int64_t M,
   return FP8MOT_OK;
 }
 
+// Argument checks of the Linear epilogue and the layer norm.
+bool elem_ok(int e) { return e == FP8MOT_ELEM_BF16 || e == FP8MOT_ELEM_F32; }
+bool act_ok(int a) { return a >= FP8MOT_ACT_NONE && a <= FP8MOT_ACT_SILU; }
+// rows, H at most INT32_MAX (32-bit workgroup counts); rows * H elements of
+// up to 4 bytes then stay below 2^64, and 2 H floats per slab below 2^63
+bool norm_sizes_ok(int64_t rows, int64_t H) {
+  return rows >= 0 && H >= 0 && rows <= INT32_MAX && H <= INT32_MAX;
+}
+
 }  // namespace
 
 extern "C" {
@@ -240,6 +249,119 @@ int fp8_requantize_onto_max(const uint8_t* qw, uint8_t* out, int64_t n,
   if (st != FP8MOT_OK) return st;
   return hip_status(launch_requant_onto_max(qw, out, n, d_s_member, d_s_group, group_size,
                                             ew_blocks(cus), stream));
+}
+
+size_t fp8_linear_act_workspace(int64_t M, int64_t N, int64_t K) {
+  if (M < 0 || N < 0 || K < 0) return 0;
+  return linear_act_workspace(M, N, K);
+}
+
+int fp8_linear_act(const uint8_t* qx, const uint8_t* qw, void* y, int64_t M, int64_t N,
+                   int64_t K, const float* d_sx, const float* d_sw, int row_scales,
+                   const void* bias, int bias_elem, int act, const void* residual,
+                   int residual_elem, uint16_t* pre, int out_kind, const float* d_sy,
+                   int accum, void* ws, size_t ws_bytes, hipStream_t stream) {
+  int st = check_linear(qx, qw, y, M, N, K, d_sx, d_sw, out_kind, d_sy, accum);
+  if (st != FP8MOT_OK) return st;
+  if ((row_scales != 0 && row_scales != 1) || !elem_ok(bias_elem) || !elem_ok(residual_elem) || !act_ok(act))
+    return FP8MOT_ERR_INVALID_ARG;
+  // the widest of y, residual and pre addresses a tile's rows like y
+  const int esz = residual != nullptr && residual_elem == FP8MOT_ELEM_F32 ? 4 : 2;
+  if (!gemm_sizes_ok(M, N, K, N, esz)) return FP8MOT_ERR_INVALID_ARG;
+  if (M == 0 || N == 0) return FP8MOT_OK;
+  if (!aligned16(bias) || !aligned16(residual) || !aligned16(pre)) return FP8MOT_ERR_MISALIGNED;
+  if (row_scales && (!aligned16(d_sx) || !aligned16(d_sw))) return FP8MOT_ERR_MISALIGNED;
+  const size_t need = linear_act_workspace(M, N, K);
+  if (need > 0 && (ws == nullptr || !aligned16(ws) || ws_bytes < need)) return FP8MOT_ERR_WORKSPACE;
+  int cus = 0;
+  st = current_device(&cus);
+  if (st != FP8MOT_OK) return st;
+  LinearActArgs g{};
+  g.qx = qx; g.qw = qw; g.y = y;
+  g.M = M; g.N = N; g.K = K;
+  g.sx = d_sx; g.sw = d_sw; g.row_scales = row_scales;
+  g.bias = bias; g.bias_f32 = bias_elem == FP8MOT_ELEM_F32;
+  g.act = act;
+  g.residual = residual; g.residual_f32 = residual_elem == FP8MOT_ELEM_F32;
+  g.pre = pre;
+  g.out_kind = out_kind; g.sy = d_sy;
+  return hip_status(launch_linear_act(g, accum, static_cast<float*>(ws), cus, stream));
+}
+
+size_t fp8_linear_act_backward_workspace(int64_t M, int64_t N) {
+  if (M < 0 || N < 0) return 0;
+  return (size_t)act_backward_slabs(M, N) * (size_t)N * sizeof(float);
+}
+
+int fp8_linear_act_backward(const uint16_t* dy, const uint16_t* pre, int act, uint16_t* dz,
+                            float* dbias, int64_t M, int64_t N, void* ws, size_t ws_bytes,
+                            hipStream_t stream) {
+  if (!act_ok(act) || M < 0 || N < 0 || M > INT32_MAX || N > INT32_MAX) return FP8MOT_ERR_INVALID_ARG;
+  if (N == 0) return FP8MOT_OK;
+  if (M > 0 && (dy == nullptr || (act != FP8MOT_ACT_NONE && pre == nullptr))) return FP8MOT_ERR_INVALID_ARG;
+  if (!aligned16(dy) || !aligned16(pre) || !aligned16(dz) || !aligned16(dbias)) return FP8MOT_ERR_MISALIGNED;
+  const size_t need = dbias != nullptr ? fp8_linear_act_backward_workspace(M, N) : 0;
+  if (need > 0 && (ws == nullptr || !aligned16(ws) || ws_bytes < need)) return FP8MOT_ERR_WORKSPACE;
+  if (dbias == nullptr && (dz == nullptr || M == 0)) return FP8MOT_OK;
+  int cus = 0;
+  int st = current_device(&cus);
+  if (st != FP8MOT_OK) return st;
+  return hip_status(launch_act_backward(dy, pre, act, dz, dbias, M, N, static_cast<float*>(ws), stream));
+}
+
+int fp8_layer_norm(const void* x, int x_elem, const void* weight, const void* bias,
+                   int wb_elem, void* y, int out_kind, const float* d_sy, float* mean,
+                   float* rstd, int64_t rows, int64_t H, float eps, hipStream_t stream) {
+  if (!elem_ok(x_elem) || !elem_ok(wb_elem) || out_kind < 0 || out_kind > 2) return FP8MOT_ERR_INVALID_ARG;
+  if (out_kind == FP8MOT_OUT_FP8 && d_sy == nullptr) return FP8MOT_ERR_UNSUPPORTED;
+  if (!norm_sizes_ok(rows, H) || !std::isfinite(eps) || eps < 0.0f) return FP8MOT_ERR_INVALID_ARG;
+  if (rows == 0 || H == 0) return FP8MOT_OK;
+  if (x == nullptr || y == nullptr) return FP8MOT_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(y) || !aligned16(weight) || !aligned16(bias)) return FP8MOT_ERR_MISALIGNED;
+  int cus = 0;
+  int st = current_device(&cus);
+  if (st != FP8MOT_OK) return st;
+  LayerNormArgs g{};
+  g.x = x; g.x_f32 = x_elem == FP8MOT_ELEM_F32;
+  g.w = weight; g.b = bias; g.wb_f32 = wb_elem == FP8MOT_ELEM_F32;
+  g.y = y; g.out_kind = out_kind; g.sy = d_sy;
+  g.mean = mean; g.rstd = rstd;
+  g.rows = rows; g.H = H; g.eps = eps;
+  return hip_status(launch_layer_norm(g, cus, stream));
+}
+
+size_t fp8_layer_norm_backward_workspace(int64_t rows, int64_t H) {
+  if (rows < 0 || H < 0) return 0;
+  return (size_t)layer_norm_backward_slabs(rows, H) * 2 * (size_t)H * sizeof(float);
+}
+
+int fp8_layer_norm_backward(const void* dy, int dy_elem, const void* x, int x_elem,
+                            const void* weight, int w_elem, const float* mean,
+                            const float* rstd, const void* dres, void* dx, float* dweight,
+                            float* dbias, int64_t rows, int64_t H, void* ws, size_t ws_bytes,
+                            hipStream_t stream) {
+  if (!elem_ok(dy_elem) || !elem_ok(x_elem) || !elem_ok(w_elem) || !norm_sizes_ok(rows, H))
+    return FP8MOT_ERR_INVALID_ARG;
+  if (H == 0) return FP8MOT_OK;
+  if (rows > 0 && (dy == nullptr || x == nullptr || mean == nullptr || rstd == nullptr || dx == nullptr))
+    return FP8MOT_ERR_INVALID_ARG;
+  if (!aligned16(dy) || !aligned16(x) || !aligned16(weight) || !aligned16(dres) || !aligned16(dx) ||
+      !aligned16(dweight) || !aligned16(dbias))
+    return FP8MOT_ERR_MISALIGNED;
+  const bool sums = dweight != nullptr || dbias != nullptr;
+  const size_t need = sums ? fp8_layer_norm_backward_workspace(rows, H) : 0;
+  if (need > 0 && (ws == nullptr || !aligned16(ws) || ws_bytes < need)) return FP8MOT_ERR_WORKSPACE;
+  if (rows == 0 && !sums) return FP8MOT_OK;
+  int cus = 0;
+  int st = current_device(&cus);
+  if (st != FP8MOT_OK) return st;
+  LayerNormBwdArgs g{};
+  g.dy = dy; g.dy_f32 = dy_elem == FP8MOT_ELEM_F32;
+  g.x = x; g.x_f32 = x_elem == FP8MOT_ELEM_F32;
+  g.w = weight; g.w_f32 = w_elem == FP8MOT_ELEM_F32;
+  g.mean = mean; g.rstd = rstd; g.dres = dres; g.dx = dx;
+  g.rows = rows; g.H = H;
+  return hip_status(launch_layer_norm_backward(g, dweight, dbias, static_cast<float*>(ws), cus, stream));
 }
 
 int fp8_quant_per_row(const uint16_t* x, uint8_t* q, float* d_scales,

@@ -110,4 +110,69 @@ hipError_t launch_gemm_swiglu(const uint8_t* qx, const uint8_t* wg, const uint8_
                               const float* sx, const float* sg, const float* su,
                               const float* sh, int accum, int num_cus, hipStream_t stream);
 
+// FP8 Linear with bias, activation and residual (fp8_linear_act).  N > 0, M > 0.
+struct LinearActArgs {
+  const uint8_t* qx;      // [M, K]
+  const uint8_t* qw;      // [N, K]
+  void* y;                // [M, N], kind out_kind (fp8mot_out)
+  int64_t M, N, K;
+  const float* sx;        // one scale, or with row_scales one per row of qx
+  const float* sw;        // one scale, or with row_scales one per row of qw
+  int row_scales;
+  const void* bias;       // [N] or NULL, FP32 if bias_f32, else BF16
+  int bias_f32;
+  int act;                // fp8mot_act
+  const void* residual;   // [M, N] or NULL, FP32 if residual_f32, else BF16; may be y
+  int residual_f32;
+  uint16_t* pre;          // [M, N] or NULL: BF16 of the activation's argument
+  int out_kind;
+  const float* sy;        // FP8 output scale
+};
+// ws: linear_act_workspace(M, N, K) bytes.
+size_t linear_act_workspace(int64_t M, int64_t N, int64_t K);
+hipError_t launch_linear_act(const LinearActArgs& g, int accum, float* ws, int num_cus, hipStream_t stream);
+
+// dz = dy act'(pre), dbias[n] = sum_m dz; part: [act_backward_slabs(M, N), N] floats.
+int64_t act_backward_slabs(int64_t M, int64_t N);
+hipError_t launch_act_backward(const uint16_t* dy, const uint16_t* pre, int act, uint16_t* dz,
+                               float* dbias, int64_t M, int64_t N, float* part, hipStream_t stream);
+
+// out[n] = sum over p of part[p, n], in order of p (slabs == 0: zeros).
+hipError_t launch_sum_slabs(const float* part, float* out, int64_t slabs, int64_t N, hipStream_t stream);
+
+// Layer norm of rows of H elements (fp8_layer_norm); H > 0, rows > 0.
+struct LayerNormArgs {
+  const void* x;          // [rows, H], FP32 if x_f32, else BF16
+  int x_f32;
+  const void* w;          // [H] or NULL
+  const void* b;          // [H] or NULL
+  int wb_f32;
+  void* y;                // [rows, H], kind out_kind (fp8mot_out)
+  int out_kind;
+  const float* sy;        // FP8 output scale
+  float* mean;            // [rows] or NULL
+  float* rstd;            // [rows] or NULL
+  int64_t rows, H;
+  float eps;
+};
+hipError_t launch_layer_norm(const LayerNormArgs& g, int num_cus, hipStream_t stream);
+
+struct LayerNormBwdArgs {
+  const void* dy;         // [rows, H]
+  int dy_f32;
+  const void* x;          // [rows, H]
+  int x_f32;              // element type of x, dres and dx
+  const void* w;          // [H] or NULL (all ones)
+  int w_f32;
+  const float* mean;      // [rows]
+  const float* rstd;      // [rows]
+  const void* dres;       // [rows, H] or NULL
+  void* dx;               // [rows, H]
+  int64_t rows, H;
+};
+// part: [layer_norm_backward_slabs(rows, H), 2 H] floats; dw, db: [H] or NULL.
+int64_t layer_norm_backward_slabs(int64_t rows, int64_t H);
+hipError_t launch_layer_norm_backward(const LayerNormBwdArgs& g, float* dw, float* db, float* part,
+                                      int num_cus, hipStream_t stream);
+
 }  // namespace fp8mot

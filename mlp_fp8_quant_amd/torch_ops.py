@@ -15,6 +15,7 @@ Scales are 1-element FP32 device tensors; weights are E4M3 codes (uint8).
 """
 
 import math
+from typing import Optional
 
 import torch
 
@@ -128,5 +129,86 @@ def _(qx, qw, sx, sw, accum=api.ACC_EXACT):
     return torch.empty((*qx.shape[:-1], qw.shape[0]), dtype=torch.bfloat16, device=qx.device)
 
 
+@torch.library.custom_op(f"{NS}::linear_act", mutates_args=())
+def linear_act(qx: torch.Tensor, qw: torch.Tensor, sx: torch.Tensor, sw: torch.Tensor,
+               bias: Optional[torch.Tensor] = None, act: int = api.ACT_NONE,
+               residual: Optional[torch.Tensor] = None, out_kind: int = api.OUT_BF16,
+               sy: Optional[torch.Tensor] = None, rowwise: bool = False,
+               accum: int = api.ACC_EXACT) -> torch.Tensor:
+    """act((qx . qw^T) * scale + bias) + residual as BF16, FP32 or E4M3 codes."""
+    return api.fp8_linear_act(qx, qw, sx, sw, bias, act, residual, out_kind, sy, rowwise,
+                              accum=accum)
+
+
+@linear_act.register_fake
+def _(qx, qw, sx, sw, bias=None, act=api.ACT_NONE, residual=None, out_kind=api.OUT_BF16, sy=None,
+      rowwise=False, accum=api.ACC_EXACT):
+    return torch.empty((*qx.shape[:-1], qw.shape[0]), dtype=api._out_dtype(out_kind),
+                       device=qx.device)
+
+
+@torch.library.custom_op(f"{NS}::linear_act_train", mutates_args=())
+def linear_act_train(qx: torch.Tensor, qw: torch.Tensor, sx: torch.Tensor, sw: torch.Tensor,
+                     bias: Optional[torch.Tensor] = None, act: int = api.ACT_NONE,
+                     residual: Optional[torch.Tensor] = None, out_kind: int = api.OUT_BF16,
+                     sy: Optional[torch.Tensor] = None, rowwise: bool = False,
+                     accum: int = api.ACC_EXACT) -> tuple[torch.Tensor, torch.Tensor]:
+    """linear_act with the activation's argument kept: (y, pre)."""
+    return api.fp8_linear_act(qx, qw, sx, sw, bias, act, residual, out_kind, sy, rowwise,
+                              pre=True, accum=accum)
+
+
+@linear_act_train.register_fake
+def _(qx, qw, sx, sw, bias=None, act=api.ACT_NONE, residual=None, out_kind=api.OUT_BF16, sy=None,
+      rowwise=False, accum=api.ACC_EXACT):
+    shape = (*qx.shape[:-1], qw.shape[0])
+    return (torch.empty(shape, dtype=api._out_dtype(out_kind), device=qx.device),
+            torch.empty(shape, dtype=torch.bfloat16, device=qx.device))
+
+
+@torch.library.custom_op(f"{NS}::linear_act_backward", mutates_args=())
+def linear_act_backward(dy: torch.Tensor, pre: Optional[torch.Tensor],
+                        act: int = api.ACT_NONE) -> tuple[torch.Tensor, torch.Tensor]:
+    """(dz, dbias) of linear_act's epilogue."""
+    return api.fp8_linear_act_backward(dy, pre, act)
+
+
+@linear_act_backward.register_fake
+def _(dy, pre, act=api.ACT_NONE):
+    return (torch.empty(dy.shape, dtype=torch.bfloat16, device=dy.device),
+            torch.empty(dy.shape[-1], dtype=torch.float32, device=dy.device))
+
+
+@torch.library.custom_op(f"{NS}::layer_norm", mutates_args=())
+def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+               bias: Optional[torch.Tensor] = None, eps: float = 1e-5,
+               out_kind: int = api.OUT_BF16, sy: Optional[torch.Tensor] = None
+               ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Layer norm over the last dimension: (y, mean, rstd)."""
+    return api.fp8_layer_norm(x, weight, bias, eps, out_kind, sy, stats=True)
+
+
+@layer_norm.register_fake
+def _(x, weight=None, bias=None, eps=1e-5, out_kind=api.OUT_BF16, sy=None):
+    stat = lambda: torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)  # noqa: E731
+    return (torch.empty(x.shape, dtype=api._out_dtype(out_kind), device=x.device), stat(), stat())
+
+
+@torch.library.custom_op(f"{NS}::layer_norm_backward", mutates_args=())
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor],
+                        mean: torch.Tensor, rstd: torch.Tensor,
+                        dres: Optional[torch.Tensor] = None
+                        ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(dx, dweight, dbias) of layer_norm."""
+    return api.fp8_layer_norm_backward(dy, x, weight, mean, rstd, dres)
+
+
+@layer_norm_backward.register_fake
+def _(dy, x, weight, mean, rstd, dres=None):
+    col = lambda: torch.empty(x.shape[-1], dtype=torch.float32, device=x.device)  # noqa: E731
+    return torch.empty(x.shape, dtype=x.dtype, device=x.device), col(), col()
+
+
 OPS = (quant_static, linear, silu_mul_2in, silu_mul, gated_mlp, qkv, quant_per_row,
-       linear_rowwise)
+       linear_rowwise, linear_act, linear_act_train, linear_act_backward, layer_norm,
+       layer_norm_backward)
