@@ -17,45 +17,49 @@ namespace fp8mot {
 
 enum Act { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
 
-// 1 / (1 + exp(-x)): exp overflows to +Inf for very negative x and its
-// reciprocal is 0.
-__device__ __forceinline__ float sigmoid_f32(float x) {
-  return __builtin_amdgcn_rcpf(__fadd_rn(1.0f, __expf(-x)));
+// 1 / (1 + 2^x), for sigma(y) = 1 / (1 + 2^(-y log2 e)): the power overflows
+// to +Inf for large x and its reciprocal is 0.
+__device__ __forceinline__ float rcp_1p_exp2(float x) {
+  return __builtin_amdgcn_rcpf(__fadd_rn(1.0f, __builtin_amdgcn_exp2f(x)));
 }
+constexpr float kLog2e = 1.44269504f;
+__device__ __forceinline__ float sigmoid_f32(float x) { return rcp_1p_exp2(__fmul_rn(x, -kLog2e)); }
 
 // Phi(z) = erfc(-z / sqrt 2) / 2 with Abramowitz and Stegun's formula 7.1.26,
 // erfc(x) ~ (a1 t + .. + a5 t^5) exp(-x^2), t = 1 / (1 + p x), x >= 0, within
-// 1.5e-7: one exponential, one reciprocal and six FMAs, where a library erf
-// evaluates two polynomial branches.  The factor exp(-x^2) keeps the tail's
-// relative accuracy, which 1 + erf would lose to cancellation.  *e receives
-// exp(-z^2 / 2).
+// 1.5e-7: one exponential, one reciprocal and a dozen operations, where a
+// library erf evaluates two polynomial branches.  The factor exp(-x^2) keeps
+// the tail's relative accuracy, which 1 + erf would lose to cancellation.
+// The constants below are the formula's with 1/sqrt 2, 1/2 and log2 e folded
+// in.  *e receives exp(-z^2 / 2).
 __device__ __forceinline__ float normal_cdf(float z, float* e) {
-  const float x = __fmul_rn(__builtin_fabsf(z), 0.70710678f);
-  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, x, 1.0f));
-  float p = __builtin_fmaf(t, 1.061405429f, -1.453152027f);
-  p = __builtin_fmaf(t, p, 1.421413741f);
-  p = __builtin_fmaf(t, p, -0.284496736f);
-  p = __builtin_fmaf(t, p, 0.254829592f);
-  *e = __expf(-__fmul_rn(x, x));
-  const float half = __fmul_rn(__fmul_rn(0.5f * t, p), *e);   // erfc(|z| / sqrt 2) / 2
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.23164190f, __builtin_fabsf(z), 1.0f));
+  float p = __builtin_fmaf(t, 0.530702715f, -0.726576014f);
+  p = __builtin_fmaf(t, p, 0.710706871f);
+  p = __builtin_fmaf(t, p, -0.142248368f);
+  p = __builtin_fmaf(t, p, 0.127414796f);
+  *e = __builtin_amdgcn_exp2f(__fmul_rn(z, __fmul_rn(z, -0.5f * kLog2e)));
+  const float half = __fmul_rn(__fmul_rn(t, p), *e);   // erfc(|z| / sqrt 2) / 2
   return z < 0.0f ? half : 1.0f - half;
 }
 
-// 2 c (z + a z^3) with z held to [-16, 16] (NaN stays), beyond which sigma of
-// it is 0 or 1 to the last bit: keeps z^3 and the slope's z^2 finite.
-__device__ __forceinline__ float clamp16(float z) {
-  return __builtin_elementwise_minimum(__builtin_elementwise_maximum(z, -16.0f), 16.0f);
-}
-__device__ __forceinline__ float gelu_tanh_arg(float zc) {
-  return __fmul_rn(1.5957691f * zc, __builtin_fmaf(0.044715f * zc, zc, 1.0f));
+// sigma(2 c (z + a z^3)) and the slope of its argument.  z is held to
+// [-16, 16], beyond which sigma is 0 or 1 to the last bit: that keeps z^3
+// and z^2 finite (a NaN z turns into a bound here and is a NaN again in the
+// product with z).
+__device__ __forceinline__ float gelu_tanh_sigma(float z, float* zc_out) {
+  const float zc = __builtin_amdgcn_fmed3f(z, -16.0f, 16.0f);
+  *zc_out = zc;
+  const float p = __builtin_fmaf(__fmul_rn(zc, zc), -1.5957691f * 0.044715f * kLog2e, -1.5957691f * kLog2e);
+  return rcp_1p_exp2(__fmul_rn(zc, p));
 }
 
 __device__ __forceinline__ float act_value(float z, int act) {
-  float e;
+  float e;   // not needed here
   switch (act) {
     case kActRelu: return __builtin_elementwise_maximum(z, 0.0f);   // NaN stays NaN
     case kActGelu: return __fmul_rn(z, normal_cdf(z, &e));
-    case kActGeluTanh: return __fmul_rn(z, sigmoid_f32(gelu_tanh_arg(clamp16(z))));
+    case kActGeluTanh: return __fmul_rn(z, gelu_tanh_sigma(z, &e));
     case kActSilu: return __fmul_rn(z, sigmoid_f32(z));
     default: return z;
   }
@@ -72,10 +76,11 @@ __device__ __forceinline__ float act_slope(float z, int act) {
       return __builtin_fmaf(z * 0.39894228f, e, p);
     }
     case kActGeluTanh: {
-      const float zc = clamp16(z);
-      const float p = sigmoid_f32(gelu_tanh_arg(zc));
-      const float du = 1.5957691f * __builtin_fmaf(0.134145f * zc, zc, 1.0f);
-      return __builtin_fmaf(__fmul_rn(zc * p, 1.0f - p), du, p);
+      float zc;
+      const float p = gelu_tanh_sigma(z, &zc);
+      const float du = __builtin_fmaf(zc * zc, 1.5957691f * 0.134145f, 1.5957691f);
+      const float s = __builtin_fmaf(__fmul_rn(zc * p, 1.0f - p), du, p);
+      return z == z ? s : z;
     }
     case kActSilu: {
       const float p = sigmoid_f32(z);

@@ -128,9 +128,25 @@ struct LinearActArgs {
   int out_kind;
   const float* sy;        // FP8 output scale
 };
+// How fp8_linear_act runs a shape; depends on the shape only, so that the
+// workspace and the order of the sums do.
+enum LinearTile {
+  // few outputs: blocks of 16 rows of X by blocks of 16 rows of W (Pair: two
+  // workgroups per CU)
+  kRows1x1, kRows1x2, kRows1x4, kRows2x1, kRows2x2, kRows2x4, kRows4x2, kRows4x4, kRows4x4Pair,
+  kTile256x256, kTile256x128, kTile128x128, kTile128x128K2
+};
+struct LinearPlan {
+  int tile;      // LinearTile
+  int splits;    // workgroups that share an output's K, joined by a second launch
+};
+LinearPlan linear_plan(int64_t M, int64_t N, int64_t K);
 // ws: linear_act_workspace(M, N, K) bytes.
 size_t linear_act_workspace(int64_t M, int64_t N, int64_t K);
 hipError_t launch_linear_act(const LinearActArgs& g, int accum, float* ws, int num_cus, hipStream_t stream);
+// The tiled kernels; with p.splits > 1 raw sums into part [splits, M, N].
+hipError_t launch_linear_tile(const LinearActArgs& g, const LinearPlan& p, int accum, float* part,
+                              int num_cus, hipStream_t stream);
 
 // dz = dy act'(pre), dbias[n] = sum_m dz; part: [act_backward_slabs(M, N), N] floats.
 int64_t act_backward_slabs(int64_t M, int64_t N);

@@ -11,109 +11,211 @@
 
 #include "act.h"
 #include "device_common.h"
+#include "gemm_parts.h"
 #include "kernels.h"
+#include "linear_epilogue.h"
 
 namespace fp8mot {
 
 namespace {
 
-typedef int v4i __attribute__((ext_vector_type(4)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef float v4f __attribute__((ext_vector_type(4)));
-
-// Eight E4M3 codes (two dwords) -> eight F16 values with the gfx950 packed
-// conversion at scale 1.0: every E4M3 value is exactly an F16 value, and the
-// NaN codes become an F16 NaN.
-__device__ __forceinline__ f16x8 decode8(int lo, int hi) {
-  return __builtin_bit_cast(
-      f16x8, (v4i){__builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((uint32_t)lo, 1.0f, false)),
-                   __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((uint32_t)lo, 1.0f, true)),
-                   __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((uint32_t)hi, 1.0f, false)),
-                   __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((uint32_t)hi, 1.0f, true))});
-}
-
-__device__ __forceinline__ float load_elem(const void* p, int f32, int64_t i) {
-  return f32 ? static_cast<const float*>(p)[i] : bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
-}
+using tile::decode8;
+using tile::f16x8;
+using tile::v4f;
+using tile::v4i;
 
 __device__ __forceinline__ uint16_t bf16_of(float v) { return (uint16_t)bf16x2_rne(v, v); }
 
-// One output element from its sum.
-__device__ __forceinline__ void finish(const LinearActArgs& g, int64_t m, int64_t n, float acc) {
-  const float alpha = g.row_scales ? __fmul_rn(g.sx[m], g.sw[n]) : __fmul_rn(*g.sx, *g.sw);
-  float z = __fmul_rn(acc, alpha);
-  if (g.bias != nullptr) z = __fadd_rn(z, load_elem(g.bias, g.bias_f32, n));
-  const int64_t i = m * g.N + n;
-  if (g.pre != nullptr) g.pre[i] = bf16_of(z);
-  float y = act_value(z, g.act);
-  if (g.residual != nullptr) y = __fadd_rn(y, load_elem(g.residual, g.residual_f32, i));
-  if (g.out_kind == 0) static_cast<uint16_t*>(g.y)[i] = bf16_of(y);
-  else if (g.out_kind == 1) static_cast<uint8_t*>(g.y)[i] = (uint8_t)e4m3_encode(y / *g.sy);   // IEEE division
-  else static_cast<float*>(g.y)[i] = y;
-}
+// Products of few rows.  A workgroup computes 16 * MB rows of X against 16 * NB
+// rows of W; its NW waves take the 128-K stages of K in turn, each through a
+// ring of D stages of its own in LDS that the buffer unit fills (rows of 128
+// codes, swizzled as in the tiled kernel), so no wave waits for another until
+// their sums are added in wave order at the end.  A lane reads 16-byte chunks
+// lane / 16 and lane / 16 + 4 of row lane % 16 of each 16-row block and feeds
+// bytes 0..7 of a chunk to one 16x16x32 F16 MFMA and bytes 8..15 to the next,
+// W as the first operand: accumulator register v of lane l is then column
+// n = 4 * (l / 16) + v of row m = l % 16.  Rows past M or N and K past its end
+// get offsets past the buffers and land as zeros.
+constexpr int kStageK = 128;
 
-// A workgroup computes 16 * MB rows of X against 16 rows of W, straight from
-// memory: its NW waves take the 64-K chunks in turn and their sums are added
-// through LDS in wave order.  A lane reads 16 bytes of one row of W and of
-// each 16-row block of X (row lane % 16, K position 16 * (lane / 16) of the
-// chunk) and feeds bytes 0..7 to one 16x16x32 F16 MFMA and bytes 8..15 to the
-// next, W as its first operand: accumulator register v of lane l is then
-// column n = 4 * (l / 16) + v of row m = l % 16.
-constexpr int kWaves = 8;
-
-template <int MB>
-__global__ __launch_bounds__(kWaves * 64) void linear_rows_kernel(LinearActArgs g) {
-  __shared__ v4f red[kWaves][MB][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+template <int MB, int NB, int NW, int D>
+__global__ __launch_bounds__(NW * 64, 1) void linear_rows_kernel(LinearActArgs g) {
+  constexpr int RB = MB + NB, COPIES = 2 * RB, STAGE = RB * 2048;
+  static_assert(NW * D * STAGE <= 160 * 1024 && NW * MB * NB * 1024 <= NW * D * STAGE, "LDS");
+  static_assert(D >= 2 && D <= 4 && D * COPIES < 64, "wait_copies");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[NW * D * STAGE];
+  constexpr int ITEMS = (MB * NB + NW - 1) / NW;   // 16x16 blocks joined by a wave
+  constexpr bool EARLY = ITEMS == 1;               // the epilogue's operands are read during the product
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int l15 = lane & 15, kq = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * 16;
-  const bool n_ok = n0 + l15 < g.N;
-  const uint8_t* wrow = g.qw + (n_ok ? n0 + l15 : 0) * g.K;
-  for (int64_t m0 = (int64_t)blockIdx.y * (16 * MB); m0 < g.M; m0 += (int64_t)gridDim.y * (16 * MB)) {
-  const uint8_t* xrow[MB];
-  bool m_ok[MB];
+  const int K = (int)g.K;
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * NB), m0 = (int64_t)blockIdx.y * (16 * MB);
+  uint8_t* const ring = smem + wave * (D * STAGE);
+
+  const bool vec = (g.N & 3) == 0;
+  const linear::Epilogue epi = linear::open_epilogue(g, m0);
+  linear::u4v res[ITEMS];
+  linear::Columns col[ITEMS];
+  // block b = wave + i * NW of the tile: row 16 (b / NB) + l15 from m0, columns from n
+  auto operands = [&](int i) {
+    const int b = wave + i * NW;
+    if (b >= MB * NB) return;
+    const int row = 16 * (b / NB) + l15, n = (int)n0 + 16 * (b % NB) + 4 * kq, nv = (int)g.N - n;
+    if (vec) {
+      if (g.residual != nullptr) linear::load_residual<1, true>(g, epi, row, 1, n, nv, &res[i]);
+      col[i] = linear::load_columns<true>(g, n, nv);
+    } else {
+      if (g.residual != nullptr) linear::load_residual<1, false>(g, epi, row, 1, n, nv, &res[i]);
+      col[i] = linear::load_columns<false>(g, n, nv);
+    }
+  };
+  if constexpr (EARLY) operands(0);
+
+  // copy q of a stage fills LDS rows 8q .. 8q + 7 (W's 16 NB rows, then X's):
+  // lane l brings row 8q + l/8, physical chunk l % 8
+  const tile::v4i wr = tile::make_rsrc_words(g.qw + n0 * K, (g.N - n0) * K);
+  const tile::v4i xr = tile::make_rsrc_words(g.qx + m0 * K, (g.M - m0) * K);
+  int off[COPIES];
 #pragma unroll
-  for (int b = 0; b < MB; ++b) {
-    const int64_t m = m0 + 16 * b + l15;
-    m_ok[b] = m < g.M;
-    xrow[b] = g.qx + (m_ok[b] ? m : 0) * g.K;
+  for (int q = 0; q < COPIES; ++q) {
+    const int r = 8 * q + (lane >> 3), rr = q < 2 * NB ? r : r - 16 * NB;
+    const int c = (lane & 7) ^ ((r >> 1) & 7);
+    off[q] = rr < (q < 2 * NB ? g.N - n0 : g.M - m0) ? rr * K + 16 * c : tile::kOOB;
   }
-  v4f acc[MB];
+  const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((tile::lds_ptr_t)ring);
+  auto issue = [&](int s, int slot) {
+    const int k0 = s * kStageK;
+    const uint32_t dst = lds0 + slot * STAGE;
+    if (k0 + kStageK <= K) {
 #pragma unroll
-  for (int b = 0; b < MB; ++b) acc[b] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
-  for (int64_t k0 = (int64_t)wave * 64; k0 < g.K; k0 += kWaves * 64) {
-    const int64_t k = k0 + 16 * kq;
-    const bool k_ok = k < g.K;   // K % 16 == 0: a chunk of 16 lies inside K or past it
-    const v4i zero = {0, 0, 0, 0};
-    const v4i w = n_ok && k_ok ? *reinterpret_cast<const v4i*>(wrow + k) : zero;
-    const f16x8 w0 = decode8(w[0], w[1]), w1 = decode8(w[2], w[3]);
+      for (int q = 0; q < COPIES; ++q) tile::copy_to_lds(q < 2 * NB ? wr : xr, dst + q * 1024, off[q], k0);
+    } else {   // K ends inside the stage
 #pragma unroll
-    for (int b = 0; b < MB; ++b) {
-      const v4i x = m_ok[b] && k_ok ? *reinterpret_cast<const v4i*>(xrow[b] + k) : zero;
-      acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w0, decode8(x[0], x[1]), acc[b], 0, 0, 0);
-      acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w1, decode8(x[2], x[3]), acc[b], 0, 0, 0);
+      for (int q = 0; q < COPIES; ++q) {
+        const int c = (lane & 7) ^ (((8 * q + (lane >> 3)) >> 1) & 7);
+        tile::copy_to_lds(q < 2 * NB ? wr : xr, dst + q * 1024,
+                          k0 + 16 * c < K && off[q] != tile::kOOB ? off[q] + k0 : tile::kOOB, 0);
+      }
+    }
+  };
+  // at most n copies of this wave in flight (vmcnt alone: gfx9 encoding)
+  auto wait_copies = [&](int n) {
+    if (D > 3 && n >= 3 * COPIES) __builtin_amdgcn_s_waitcnt(0x0F70 | ((3 * COPIES) & 15) | (((3 * COPIES) >> 4) << 14));
+    else if (D > 2 && n >= 2 * COPIES) __builtin_amdgcn_s_waitcnt(0x0F70 | ((2 * COPIES) & 15) | (((2 * COPIES) >> 4) << 14));
+    else if (n >= COPIES) __builtin_amdgcn_s_waitcnt(0x0F70 | (COPIES & 15) | ((COPIES >> 4) << 14));
+    else __builtin_amdgcn_s_waitcnt(0x0F70);
+  };
+  const int stages = (K + kStageK - 1) / kStageK;
+  const int mine = wave < stages ? (stages - wave + NW - 1) / NW : 0;   // stages wave, wave + NW, ..
+#pragma unroll
+  for (int i = 0; i < D; ++i)
+    if (i < mine) issue(wave + i * NW, i);
+
+  v4f acc[MB][NB];
+#pragma unroll
+  for (int b = 0; b < MB; ++b)
+#pragma unroll
+    for (int c = 0; c < NB; ++c) acc[b][c] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+  const int rd0 = l15 * 128 + ((kq ^ (l15 >> 1)) << 4), rd1 = l15 * 128 + (((kq + 4) ^ (l15 >> 1)) << 4);
+  int slot = 0;
+  for (int i = 0; i < mine; ++i) {
+    wait_copies(COPIES * (min(D, mine - i) - 1));
+    asm volatile("" ::: "memory");
+    const uint8_t* st = ring + slot * STAGE;
+    v4i f[RB][2];
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      f[r][0] = *reinterpret_cast<const v4i*>(st + r * 2048 + rd0);
+      f[r][1] = *reinterpret_cast<const v4i*>(st + r * 2048 + rd1);
+    }
+    if (i + D < mine) {
+      // the fragments have been read before the stage is refilled
+      __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+      asm volatile("" ::: "memory");
+      issue(wave + (i + D) * NW, slot);
+    }
+    slot = slot + 1 == D ? 0 : slot + 1;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      f16x8 w0[NB], w1[NB];
+#pragma unroll
+      for (int c = 0; c < NB; ++c) {
+        w0[c] = decode8(f[c][h][0], f[c][h][1]);
+        w1[c] = decode8(f[c][h][2], f[c][h][3]);
+      }
+#pragma unroll
+      for (int b = 0; b < MB; ++b) {
+        const f16x8 x0 = decode8(f[NB + b][h][0], f[NB + b][h][1]), x1 = decode8(f[NB + b][h][2], f[NB + b][h][3]);
+#pragma unroll
+        for (int c = 0; c < NB; ++c) {
+          acc[b][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w0[c], x0, acc[b][c], 0, 0, 0);
+          acc[b][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w1[c], x1, acc[b][c], 0, 0, 0);
+        }
+      }
     }
   }
-#pragma unroll
-  for (int b = 0; b < MB; ++b) red[wave][b][lane] = acc[b];
+
+  // join: the ring is free once every wave is here (its copies have landed)
   __syncthreads();
-  for (int t = threadIdx.x; t < MB * 64; t += kWaves * 64) {
-    const int b = t >> 6, l = t & 63;
-    v4f s = red[0][b][l];
+  v4f* red = reinterpret_cast<v4f*>(smem);
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) {
-      const v4f o = red[w][b][l];
+  for (int b = 0; b < MB; ++b)
+#pragma unroll
+    for (int c = 0; c < NB; ++c) red[(wave * (MB * NB) + b * NB + c) * 64 + lane] = acc[b][c];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const int b = wave + i * NW;
+    if (b >= MB * NB) break;
+    if constexpr (!EARLY) operands(i);
+    v4f s = red[b * 64 + lane];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) {
+      const v4f o = red[(w * (MB * NB) + b) * 64 + lane];
 #pragma unroll
       for (int v = 0; v < 4; ++v) s[v] = __fadd_rn(s[v], o[v]);
     }
-    const int64_t m = m0 + 16 * b + (l & 15), n = n0 + 4 * (l >> 4);
-    if (m < g.M) {
-#pragma unroll
-      for (int v = 0; v < 4; ++v)
-        if (n + v < g.N) finish(g, m, n + v, s[v]);
-    }
+    float z[1][4] = {{s[0], s[1], s[2], s[3]}};
+    const int row = 16 * (b / NB) + l15, n = (int)n0 + 16 * (b % NB) + 4 * kq, nv = (int)g.N - n;
+    if (vec) linear::finish<1, true>(g, epi, col[i], m0, row, 1, n, nv, &res[i], z, [] {});
+    else linear::finish<1, false>(g, epi, col[i], m0, row, 1, n, nv, &res[i], z, [] {});
   }
-  __syncthreads();   // red is reused by the next rows
+}
+
+template <int MB, int NB, int NW, int D>
+hipError_t launch_rows(const LinearActArgs& g, hipStream_t stream) {
+  hipLaunchKernelGGL((linear_rows_kernel<MB, NB, NW, D>),
+                     dim3((unsigned)((g.N + 16 * NB - 1) / (16 * NB)), (unsigned)((g.M + 16 * MB - 1) / (16 * MB))),
+                     dim3(NW * 64), 0, stream, g);
+  return hipGetLastError();
+}
+
+// Joins the splits of K: sums part [splits, M, N] in split order and runs the
+// epilogue, four consecutive columns per thread.  A workgroup's groups lie
+// within kJoinRows rows of each other, which the epilogue addresses from the
+// first of them.
+constexpr int kJoinRows = 16;
+
+template <bool VEC>
+__global__ __launch_bounds__(256) void linear_join_kernel(LinearActArgs g, const float* __restrict__ part,
+                                                          int splits) {
+  const int N = (int)g.N, per_row = (N + 3) / 4;
+  const int64_t m0 = (int64_t)blockIdx.y * kJoinRows;
+  const int rows = g.M - m0 < kJoinRows ? (int)(g.M - m0) : kJoinRows;
+  const linear::Epilogue e = linear::open_epilogue(g, m0);
+  for (int i = (int)blockIdx.x * 256 + (int)threadIdx.x; i < rows * per_row; i += (int)gridDim.x * 256) {
+    const int row = i / per_row, n = (i - row * per_row) * 4, nv = N - n;
+    linear::u4v r[1];
+    if (g.residual != nullptr) linear::load_residual<1, VEC>(g, e, row, 1, n, nv, r);
+    const linear::Columns col = linear::load_columns<VEC>(g, n, nv);
+    float z[1][4] = {{0.0f, 0.0f, 0.0f, 0.0f}}, o[4];
+    for (int p = 0; p < splits; ++p) {
+      linear::values4(linear::load4<VEC>(linear::rows_of(part + p * g.M * N, m0, g.M, N, 4), 1, row * N + n, nv), 1, o);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) z[0][c] = p == 0 ? o[c] : __fadd_rn(z[0][c], o[c]);
+    }
+    linear::finish<1, VEC>(g, e, col, m0, row, 1, n, nv, r, z, [] {});
   }
 }
 
@@ -142,23 +244,85 @@ __global__ __launch_bounds__(kThreads) void act_backward_kernel(
 
 }  // namespace
 
+// How a shape runs (MI355X, 256 CUs; us measured with bias and residual).
+//
+// Few outputs: the smallest tile of 16x16 blocks whose grid gives no CU more
+// than one workgroup, since a CU's share of the rows has to pass through its
+// own L1 at 40-50 bytes a clock whatever the tile: 1x4096x4096 5.2 with 16x16
+// blocks and 16 waves (16x32: 5.6), 64x4096x4096 7.3 with 32x32 (64x32 10.3,
+// 32x16 8.2), 256x4096x4096 16.6 with 64x64 (64x32 19.3; 128x128 tiles split
+// four ways over K 23.1).  Above that, up to two workgroups per CU (64x64,
+// two waves): 512x4096x4096 27.3 (128x128 tiles split in two 29.8).
+//
+// More outputs: the cheapest of the tiles and splits by an estimate of rounds
+// of workgroups times (rate * K + what a tile costs besides), plus the second
+// launch that joins splits of K.  The rates are fitted to sweeps: 256x256
+// tiles 4096x4096x12288 303 (256x128 333, 128x128 337), 128x128 with two K
+// groups 2048x2048x8192 66 (256x128 split in two 72) and 1024x4096x4096 38.6
+// (256x128 52), 256x128 split in three 3000x700x8000 50 (128x128, two K
+// groups, unsplit: 59), 128x128 two to a CU 3000x3000x1024 39.4 (256x256 41,
+// 256x128 45).
+LinearPlan linear_plan(int64_t M, int64_t N, int64_t K) {
+  constexpr int64_t kCus = 256;
+  auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+  const int64_t area = up(up(M, 16) * up(N, 16), kCus);   // blocks per CU
+  if (M <= 16) return {area <= 1 ? kRows1x1 : area <= 2 ? kRows1x2 : kRows1x4, 1};
+  if (area <= 2) return {kRows2x1, 1};
+  if (area <= 4) return {kRows2x2, 1};
+  if (M <= 32) return {kRows2x4, 1};
+  if (area <= 8) return {kRows4x2, 1};
+  if (area <= 16) return {kRows4x4, 1};
+  if (M <= 64) return {kRows4x4Pair, 1};
+  LinearPlan best{kTile256x256, 1};
+  auto tiles = [&](int bm, int bn) { return up(M, bm) * up(N, bn); };
+  double least = (double)up(tiles(256, 256), kCus) * (0.0235 * (double)K + 13.0);
+  auto offer = [&](LinearPlan p, double us) {
+    if (us < least) {
+      least = us;
+      best = p;
+    }
+  };
+  if (area <= 32) offer({kRows4x4Pair, 1}, 0.0038 * (double)K + 11.7);
+  const double pairs = (double)tiles(128, 128) / (2 * kCus);
+  if (pairs > 0.5) offer({kTile128x128, 1}, (pairs + 0.3) * (0.0150 * (double)K + 10.0));
+  const int64_t stages = up(K, 128);
+  for (int s = 1; s <= 4 && (s == 1 || stages >= 8 * s); ++s) {
+    const double k = (double)(up(stages, s) * 128);
+    const double join = s == 1 ? 0.0 : 4.0 + (double)s * (double)M * (double)N * 8.0 / 12e6;
+    offer({kTile256x128, s}, (double)up(tiles(256, 128) * s, kCus) * (0.0132 * k + 9.0) + join);
+    offer({kTile128x128K2, s}, (double)up(tiles(128, 128) * s, kCus) * (0.0072 * k + 8.0) + join);
+  }
+  return best;
+}
+
 size_t linear_act_workspace(int64_t M, int64_t N, int64_t K) {
-  (void)M;
-  (void)N;
-  (void)K;
-  return 0;
+  if (M == 0 || N == 0) return 0;
+  const LinearPlan p = linear_plan(M, N, K);
+  return p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)N * sizeof(float) : 0;
 }
 
 hipError_t launch_linear_act(const LinearActArgs& g, int accum, float* ws, int num_cus, hipStream_t stream) {
-  (void)accum;
-  (void)ws;
-  (void)num_cus;
-  const unsigned gx = (unsigned)((g.N + 15) / 16);
-  if (g.M <= 16)
-    hipLaunchKernelGGL((linear_rows_kernel<1>), dim3(gx, 1), dim3(kWaves * 64), 0, stream, g);
+  const LinearPlan p = linear_plan(g.M, g.N, g.K);
+  switch (p.tile) {
+    case kRows1x1: return launch_rows<1, 1, 16, 2>(g, stream);
+    case kRows1x2: return launch_rows<1, 2, 8, 2>(g, stream);
+    case kRows1x4: return launch_rows<1, 4, 4, 2>(g, stream);
+    case kRows2x1: return launch_rows<2, 1, 8, 2>(g, stream);
+    case kRows2x2: return launch_rows<2, 2, 8, 2>(g, stream);
+    case kRows2x4: return launch_rows<2, 4, 4, 2>(g, stream);
+    case kRows4x2: return launch_rows<4, 2, 4, 2>(g, stream);
+    case kRows4x4: return launch_rows<4, 4, 4, 2>(g, stream);
+    case kRows4x4Pair: return launch_rows<4, 4, 2, 2>(g, stream);
+    default: break;
+  }
+  const hipError_t e = launch_linear_tile(g, p, accum, ws, num_cus, stream);
+  if (e != hipSuccess || p.splits == 1) return e;
+  const int64_t blocks = (kJoinRows * ((g.N + 3) / 4) + 255) / 256;
+  const dim3 grid((unsigned)blocks, (unsigned)((g.M + kJoinRows - 1) / kJoinRows));
+  if ((g.N & 3) == 0)
+    hipLaunchKernelGGL(linear_join_kernel<true>, grid, dim3(256), 0, stream, g, ws, p.splits);
   else
-    hipLaunchKernelGGL((linear_rows_kernel<4>), dim3(gx, (unsigned)(g.M < 64 * 4096 ? (g.M + 63) / 64 : 4096)),
-                       dim3(kWaves * 64), 0, stream, g);
+    hipLaunchKernelGGL(linear_join_kernel<false>, grid, dim3(256), 0, stream, g, ws, p.splits);
   return hipGetLastError();
 }
 
