@@ -366,6 +366,7 @@ size_t fp8_linear_act_backward_workspace(int64_t M, int64_t N);
  * dy, pre, dz: BF16 [M, N]; dbias: FP32 [N]; all 16-byte aligned.  dz or
  * dbias may be NULL (not computed), and with FP8MOT_ACT_NONE pre too.  dz may
  * be dy or pre itself.  relu's slope at 0 is 0.  M == 0 writes dbias = 0.
+ * M up to INT32_MAX, N up to 2^28.
  * ws: 16-byte aligned, at least fp8_linear_act_backward_workspace(M, N)
  * bytes; unused where dbias is NULL. */
 int fp8_linear_act_backward(const uint16_t* dy, const uint16_t* pre, int act, uint16_t* dz,
@@ -386,8 +387,8 @@ int fp8_linear_act_backward(const uint16_t* dy, const uint16_t* pre, int act, ui
  * x: [rows, H] of x_elem (fp8mot_elem); weight, bias: [H] of wb_elem, either
  * may be NULL (ones, zeros); y: [rows, H]; mean, rstd: FP32 [rows] for the
  * backward pass, or NULL.  eps finite and >= 0.  y may be x itself where the
- * element types agree; no other overlap.  Any H >= 0; x, y, weight, bias
- * 16-byte aligned.  A row that holds a NaN or an infinity becomes NaN. */
+ * element types agree; no other overlap.  H up to 2^28, rows up to INT32_MAX;
+ * x, y, weight, bias 16-byte aligned.  A row that holds a NaN or an infinity becomes NaN. */
 int fp8_layer_norm(const void* x, int x_elem, const void* weight, const void* bias,
                    int wb_elem, void* y, int out_kind, const float* d_sy, float* mean,
                    float* rstd, int64_t rows, int64_t H, float eps, hipStream_t stream);
@@ -406,7 +407,7 @@ size_t fp8_layer_norm_backward_workspace(int64_t rows, int64_t H);
  * rounded.  dy: of dy_elem; x, dres, dx: of x_elem; weight: [H] of w_elem or
  * NULL (ones); dweight, dbias: FP32 [H], either may be NULL (not computed).
  * dx may be dy or dres itself where the element types agree, or x; no other
- * overlap.  rows == 0 writes dweight = dbias = 0.  The sums over rows take an
+ * overlap.  rows == 0 writes dweight = dbias = 0.  Sizes as fp8_layer_norm.  The sums over rows take an
  * order that depends on (rows, H) only.  All tensors 16-byte aligned but
  * mean and rstd.  ws: 16-byte aligned, at least
  * fp8_layer_norm_backward_workspace(rows, H) bytes; unused where dweight and

@@ -90,4 +90,54 @@ __device__ __forceinline__ float act_slope(float z, int act) {
   }
 }
 
+// The same over n values: the switch is outside the loops, so that only the
+// chosen one's instructions are fetched.
+template <int n>
+__device__ __forceinline__ void act_all(float* z, int act) {
+  switch (act) {
+    case kActRelu:
+#pragma unroll
+      for (int i = 0; i < n; ++i) z[i] = act_value(z[i], kActRelu);
+      break;
+    case kActGelu:
+#pragma unroll
+      for (int i = 0; i < n; ++i) z[i] = act_value(z[i], kActGelu);
+      break;
+    case kActGeluTanh:
+#pragma unroll
+      for (int i = 0; i < n; ++i) z[i] = act_value(z[i], kActGeluTanh);
+      break;
+    case kActSilu:
+#pragma unroll
+      for (int i = 0; i < n; ++i) z[i] = act_value(z[i], kActSilu);
+      break;
+    default: break;
+  }
+}
+
+template <int n>
+__device__ __forceinline__ void slope_all(float* z, int act) {
+  switch (act) {
+    case kActRelu:
+#pragma unroll
+      for (int i = 0; i < n; ++i) z[i] = act_slope(z[i], kActRelu);
+      break;
+    case kActGelu:
+#pragma unroll
+      for (int i = 0; i < n; ++i) z[i] = act_slope(z[i], kActGelu);
+      break;
+    case kActGeluTanh:
+#pragma unroll
+      for (int i = 0; i < n; ++i) z[i] = act_slope(z[i], kActGeluTanh);
+      break;
+    case kActSilu:
+#pragma unroll
+      for (int i = 0; i < n; ++i) z[i] = act_slope(z[i], kActSilu);
+      break;
+    default:
+#pragma unroll
+      for (int i = 0; i < n; ++i) z[i] = 1.0f;
+  }
+}
+
 }  // namespace fp8mot

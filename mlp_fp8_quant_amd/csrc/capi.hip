@@ -108,10 +108,11 @@ int check_linear(const uint8_t* qx, const uint8_t* qw, const void* y, int64_t M,
 // Argument checks of the Linear epilogue and the layer norm.
 bool elem_ok(int e) { return e == FP8MOT_ELEM_BF16 || e == FP8MOT_ELEM_F32; }
 bool act_ok(int a) { return a >= FP8MOT_ACT_NONE && a <= FP8MOT_ACT_SILU; }
-// rows, H at most INT32_MAX (32-bit workgroup counts); rows * H elements of
-// up to 4 bytes then stay below 2^64, and 2 H floats per slab below 2^63
-bool norm_sizes_ok(int64_t rows, int64_t H) {
-  return rows >= 0 && H >= 0 && rows <= INT32_MAX && H <= INT32_MAX;
+// rows at most INT32_MAX and at most 2^28 columns (32-bit counts of threads in
+// a launch); byte offsets are 64-bit
+constexpr int64_t kMaxColumns = int64_t(1) << 28;
+bool rows_ok(int64_t rows, int64_t cols) {
+  return rows >= 0 && cols >= 0 && rows <= INT32_MAX && cols <= kMaxColumns;
 }
 
 }  // namespace
@@ -296,7 +297,7 @@ size_t fp8_linear_act_backward_workspace(int64_t M, int64_t N) {
 int fp8_linear_act_backward(const uint16_t* dy, const uint16_t* pre, int act, uint16_t* dz,
                             float* dbias, int64_t M, int64_t N, void* ws, size_t ws_bytes,
                             hipStream_t stream) {
-  if (!act_ok(act) || M < 0 || N < 0 || M > INT32_MAX || N > INT32_MAX) return FP8MOT_ERR_INVALID_ARG;
+  if (!act_ok(act) || !rows_ok(M, N)) return FP8MOT_ERR_INVALID_ARG;
   if (N == 0) return FP8MOT_OK;
   if (M > 0 && (dy == nullptr || (act != FP8MOT_ACT_NONE && pre == nullptr))) return FP8MOT_ERR_INVALID_ARG;
   if (!aligned16(dy) || !aligned16(pre) || !aligned16(dz) || !aligned16(dbias)) return FP8MOT_ERR_MISALIGNED;
@@ -314,7 +315,7 @@ int fp8_layer_norm(const void* x, int x_elem, const void* weight, const void* bi
                    float* rstd, int64_t rows, int64_t H, float eps, hipStream_t stream) {
   if (!elem_ok(x_elem) || !elem_ok(wb_elem) || out_kind < 0 || out_kind > 2) return FP8MOT_ERR_INVALID_ARG;
   if (out_kind == FP8MOT_OUT_FP8 && d_sy == nullptr) return FP8MOT_ERR_UNSUPPORTED;
-  if (!norm_sizes_ok(rows, H) || !std::isfinite(eps) || eps < 0.0f) return FP8MOT_ERR_INVALID_ARG;
+  if (!rows_ok(rows, H) || !std::isfinite(eps) || eps < 0.0f) return FP8MOT_ERR_INVALID_ARG;
   if (rows == 0 || H == 0) return FP8MOT_OK;
   if (x == nullptr || y == nullptr) return FP8MOT_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(y) || !aligned16(weight) || !aligned16(bias)) return FP8MOT_ERR_MISALIGNED;
@@ -327,7 +328,7 @@ int fp8_layer_norm(const void* x, int x_elem, const void* weight, const void* bi
   g.y = y; g.out_kind = out_kind; g.sy = d_sy;
   g.mean = mean; g.rstd = rstd;
   g.rows = rows; g.H = H; g.eps = eps;
-  return hip_status(launch_layer_norm(g, cus, stream));
+  return hip_status(launch_layer_norm(g, stream));
 }
 
 size_t fp8_layer_norm_backward_workspace(int64_t rows, int64_t H) {
@@ -340,7 +341,7 @@ int fp8_layer_norm_backward(const void* dy, int dy_elem, const void* x, int x_el
                             const float* rstd, const void* dres, void* dx, float* dweight,
                             float* dbias, int64_t rows, int64_t H, void* ws, size_t ws_bytes,
                             hipStream_t stream) {
-  if (!elem_ok(dy_elem) || !elem_ok(x_elem) || !elem_ok(w_elem) || !norm_sizes_ok(rows, H))
+  if (!elem_ok(dy_elem) || !elem_ok(x_elem) || !elem_ok(w_elem) || !rows_ok(rows, H))
     return FP8MOT_ERR_INVALID_ARG;
   if (H == 0) return FP8MOT_OK;
   if (rows > 0 && (dy == nullptr || x == nullptr || mean == nullptr || rstd == nullptr || dx == nullptr))
@@ -361,7 +362,7 @@ int fp8_layer_norm_backward(const void* dy, int dy_elem, const void* x, int x_el
   g.w = weight; g.w_f32 = w_elem == FP8MOT_ELEM_F32;
   g.mean = mean; g.rstd = rstd; g.dres = dres; g.dx = dx;
   g.rows = rows; g.H = H;
-  return hip_status(launch_layer_norm_backward(g, dweight, dbias, static_cast<float*>(ws), cus, stream));
+  return hip_status(launch_layer_norm_backward(g, dweight, dbias, static_cast<float*>(ws), stream));
 }
 
 int fp8_quant_per_row(const uint16_t* x, uint8_t* q, float* d_scales,

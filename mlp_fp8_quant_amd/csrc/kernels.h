@@ -153,8 +153,10 @@ int64_t act_backward_slabs(int64_t M, int64_t N);
 hipError_t launch_act_backward(const uint16_t* dy, const uint16_t* pre, int act, uint16_t* dz,
                                float* dbias, int64_t M, int64_t N, float* part, hipStream_t stream);
 
-// out[n] = sum over p of part[p, n], in order of p (slabs == 0: zeros).
-hipError_t launch_sum_slabs(const float* part, float* out, int64_t slabs, int64_t N, hipStream_t stream);
+// Column sums of part [slabs, cols] into out_a [N] and, past column N, out_b
+// [cols - N], either of them NULL to leave it out (slabs == 0: zeros).
+hipError_t launch_sum_slabs(const float* part, float* out_a, float* out_b, int64_t slabs, int64_t N,
+                            int64_t cols, hipStream_t stream);
 
 // Layer norm of rows of H elements (fp8_layer_norm); H > 0, rows > 0.
 struct LayerNormArgs {
@@ -171,7 +173,7 @@ struct LayerNormArgs {
   int64_t rows, H;
   float eps;
 };
-hipError_t launch_layer_norm(const LayerNormArgs& g, int num_cus, hipStream_t stream);
+hipError_t launch_layer_norm(const LayerNormArgs& g, hipStream_t stream);
 
 struct LayerNormBwdArgs {
   const void* dy;         // [rows, H]
@@ -189,6 +191,6 @@ struct LayerNormBwdArgs {
 // part: [layer_norm_backward_slabs(rows, H), 2 H] floats; dw, db: [H] or NULL.
 int64_t layer_norm_backward_slabs(int64_t rows, int64_t H);
 hipError_t launch_layer_norm_backward(const LayerNormBwdArgs& g, float* dw, float* db, float* part,
-                                      int num_cus, hipStream_t stream);
+                                      hipStream_t stream);
 
 }  // namespace fp8mot

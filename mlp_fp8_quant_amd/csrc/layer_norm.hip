@@ -7,166 +7,463 @@
 //   dw = sum_rows dy xh,  db = sum_rows dy
 //
 // All sums are FP32; the variance is taken about the mean (not from the
-// squares' mean, which cancels where the mean is large).
+// squares' mean, which cancels where the mean is large).  Bound by memory: a
+// row is read once and kept in registers over its sums.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
 #include "device_common.h"
 #include "kernels.h"
+#include "rowwise.h"
 
 namespace fp8mot {
 
 namespace {
 
-constexpr int kThreads = 256;
+using namespace rows;
 
-__device__ __forceinline__ float load_elem(const void* p, int f32, int64_t i) {
-  return f32 ? static_cast<const float*>(p)[i] : bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
+// Sum over T threads (whole waves) of a workgroup that share a row, the same
+// in each.  red: T / 64 floats of LDS that no other sum in flight uses.
+template <int T>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+  v = wave_sum(v);
+  if constexpr (T > 64) {
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int w = 1; w < T / 64; ++w) v = __fadd_rn(v, red[w]);
+  }
+  return v;
 }
 
-__device__ __forceinline__ uint16_t bf16_of(float v) { return (uint16_t)bf16x2_rne(v, v); }
-
-// Sum over the workgroup, the same in every thread.
-__device__ __forceinline__ float block_sum(float v, float* red) {
+__device__ __forceinline__ void emit8(const LayerNormArgs& g, int64_t base, int64_t i, float rs, float* y) {
+  if (g.out_kind == 0) {
+    store8_bf16(static_cast<uint16_t*>(g.y) + base, i, g.H, y);
+  } else if (g.out_kind == 1) {
 #pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v = __fadd_rn(v, __shfl_xor(v, off, 64));
-  __syncthreads();   // red may still be read from the sum before
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float s = red[0];
-#pragma unroll
-  for (int w = 1; w < kThreads / 64; ++w) s = __fadd_rn(s, red[w]);
-  return s;
+    for (int k = 0; k < 8; ++k) y[k] = __fmul_rn(y[k], rs);
+    store8_fp8(static_cast<uint8_t*>(g.y) + base, i, g.H, y);
+  } else {
+    store8_f32(static_cast<float*>(g.y) + base, i, g.H, y);
+  }
 }
 
-// One workgroup per row, which it reads three times (from cache after the first).
-__global__ __launch_bounds__(kThreads) void layer_norm_kernel(LayerNormArgs g) {
-  __shared__ float red[kThreads / 64];
+__device__ __forceinline__ void norm8(const LayerNormArgs& g, int64_t i, float mean, float rstd, float* f) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] = __fmul_rn(__fadd_rn(f[k], -mean), rstd);
+  if (g.w != nullptr) {
+    float w[8];
+    load8_values(g.w, g.wb_f32, i, g.H, w);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = __fmul_rn(f[k], w[k]);
+  }
+  if (g.b != nullptr) {
+    float b[8];
+    load8_values(g.b, g.wb_f32, i, g.H, b);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = __fadd_rn(f[k], b[k]);
+  }
+}
+
+// T threads per row, U groups of eight elements per thread (group j * T + t of
+// the row): a row of up to 8 T U elements in registers.  Workgroups of 256
+// threads hold 256 / T rows where T < 256.
+template <bool F32, int T, int U>
+__global__ __launch_bounds__(T < 256 ? 256 : T) void layer_norm_kernel(LayerNormArgs g) {
+  __shared__ float red[2][T / 64];
+  constexpr int RPB = T < 256 ? 256 / T : 1;
+  const int t = T < 256 ? threadIdx.x % T : threadIdx.x;
   const float inv_h = 1.0f / (float)g.H;
-  for (int64_t r = blockIdx.x; r < g.rows; r += gridDim.x) {
-    const int64_t base = r * g.H;
-    float s = 0.0f;
-    for (int64_t i = threadIdx.x; i < g.H; i += kThreads) s = __fadd_rn(s, load_elem(g.x, g.x_f32, base + i));
-    const float mean = __fmul_rn(block_sum(s, red), inv_h);
-    float v = 0.0f;
-    for (int64_t i = threadIdx.x; i < g.H; i += kThreads) {
-      const float d = __fadd_rn(load_elem(g.x, g.x_f32, base + i), -mean);
+  // (the two sums' LDS takes turns, so a row's never meets the row before)
+  for (int64_t r = (int64_t)blockIdx.x * RPB + (T < 256 ? threadIdx.x / T : 0); r < g.rows;
+       r += (int64_t)gridDim.x * RPB) {
+  const int64_t base = r * g.H;
+  const void* xr = static_cast<const uint8_t*>(g.x) + base * (F32 ? 4 : 2);
+  Raw8<F32> x[U];
+#pragma unroll
+  for (int j = 0; j < U; ++j) x[j] = load8<F32>(xr, 8 * (int64_t)(j * T + t), g.H);
+  float s = 0.0f;
+#pragma unroll
+  for (int j = 0; j < U; ++j) {
+    float f[8];
+    values8<F32>(x[j], f);
+    // a tree per group: fewer roundings in a row than one after another
+    s = __fadd_rn(s, __fadd_rn(__fadd_rn(__fadd_rn(f[0], f[1]), __fadd_rn(f[2], f[3])),
+                               __fadd_rn(__fadd_rn(f[4], f[5]), __fadd_rn(f[6], f[7]))));
+  }
+  const float mean = __fmul_rn(row_sum<T>(s, red[0]), inv_h);
+  float v = 0.0f;
+#pragma unroll
+  for (int j = 0; j < U; ++j) {
+    float f[8];
+    values8<F32>(x[j], f);
+    const int64_t left = g.H - 8 * (int64_t)(j * T + t);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float d = k < left ? __fadd_rn(f[k], -mean) : 0.0f;
       v = __builtin_fmaf(d, d, v);
     }
-    const float var = __fmul_rn(block_sum(v, red), inv_h);
-    const float rstd = 1.0f / __fsqrt_rn(__fadd_rn(var, g.eps));
-    for (int64_t i = threadIdx.x; i < g.H; i += kThreads) {
-      float y = __fmul_rn(__fadd_rn(load_elem(g.x, g.x_f32, base + i), -mean), rstd);
-      if (g.w != nullptr) y = __fmul_rn(y, load_elem(g.w, g.wb_f32, i));
-      if (g.b != nullptr) y = __fadd_rn(y, load_elem(g.b, g.wb_f32, i));
-      if (g.out_kind == 0) static_cast<uint16_t*>(g.y)[base + i] = bf16_of(y);
-      else if (g.out_kind == 1) static_cast<uint8_t*>(g.y)[base + i] = (uint8_t)e4m3_encode(y / *g.sy);
-      else static_cast<float*>(g.y)[base + i] = y;
+  }
+  const float var = __fmul_rn(row_sum<T>(v, red[1]), inv_h);
+  const float rstd = 1.0f / __fsqrt_rn(__fadd_rn(var, g.eps));
+  if (t == 0) {
+    if (g.mean != nullptr) g.mean[r] = mean;
+    if (g.rstd != nullptr) g.rstd[r] = rstd;
+  }
+  const float rs = g.out_kind == 1 ? 1.0f / *g.sy : 0.0f;
+#pragma unroll
+  for (int j = 0; j < U; ++j) {
+    const int64_t i = 8 * (int64_t)(j * T + t);
+    if (i < g.H) {
+      float f[8];
+      values8<F32>(x[j], f);
+      norm8(g, i, mean, rstd, f);
+      emit8(g, base, i, rs, f);
     }
-    if (threadIdx.x == 0) {
-      if (g.mean != nullptr) g.mean[r] = mean;
-      if (g.rstd != nullptr) g.rstd[r] = rstd;
-    }
+  }
   }
 }
 
-// dx: one workgroup per row.
-__global__ __launch_bounds__(kThreads) void layer_norm_dx_kernel(LayerNormBwdArgs g) {
-  __shared__ float red[kThreads / 64];
+// Rows too long for registers: read three times, from cache after the first.
+template <bool F32>
+__global__ __launch_bounds__(1024) void layer_norm_long_kernel(LayerNormArgs g) {
+  __shared__ float red[2][16];
   const float inv_h = 1.0f / (float)g.H;
   for (int64_t r = blockIdx.x; r < g.rows; r += gridDim.x) {
-    const int64_t base = r * g.H;
-    const float mean = g.mean[r], rstd = g.rstd[r];
-    float s1 = 0.0f, s2 = 0.0f;
-    for (int64_t i = threadIdx.x; i < g.H; i += kThreads) {
-      const float xh = __fmul_rn(__fadd_rn(load_elem(g.x, g.x_f32, base + i), -mean), rstd);
-      float d = load_elem(g.dy, g.dy_f32, base + i);
-      if (g.w != nullptr) d = __fmul_rn(d, load_elem(g.w, g.w_f32, i));
-      s1 = __fadd_rn(s1, d);
-      s2 = __builtin_fmaf(d, xh, s2);
+  const int64_t base = r * g.H;
+  const void* xr = static_cast<const uint8_t*>(g.x) + base * (F32 ? 4 : 2);
+  float s = 0.0f;
+  for (int64_t i = 8 * (int64_t)threadIdx.x; i < g.H; i += 8 * 1024) {
+    float f[8];
+    values8<F32>(load8<F32>(xr, i, g.H), f);
+    s = __fadd_rn(s, __fadd_rn(__fadd_rn(__fadd_rn(f[0], f[1]), __fadd_rn(f[2], f[3])),
+                               __fadd_rn(__fadd_rn(f[4], f[5]), __fadd_rn(f[6], f[7]))));
+  }
+  const float mean = __fmul_rn(row_sum<1024>(s, red[0]), inv_h);
+  float v = 0.0f;
+  for (int64_t i = 8 * (int64_t)threadIdx.x; i < g.H; i += 8 * 1024) {
+    float f[8];
+    values8<F32>(load8<F32>(xr, i, g.H), f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float d = i + k < g.H ? __fadd_rn(f[k], -mean) : 0.0f;
+      v = __builtin_fmaf(d, d, v);
     }
-    const float c1 = __fmul_rn(block_sum(s1, red), inv_h), c2 = __fmul_rn(block_sum(s2, red), inv_h);
-    for (int64_t i = threadIdx.x; i < g.H; i += kThreads) {
-      const float xh = __fmul_rn(__fadd_rn(load_elem(g.x, g.x_f32, base + i), -mean), rstd);
-      float d = load_elem(g.dy, g.dy_f32, base + i);
-      if (g.w != nullptr) d = __fmul_rn(d, load_elem(g.w, g.w_f32, i));
-      float v = __fmul_rn(rstd, __builtin_fmaf(-xh, c2, __fadd_rn(d, -c1)));
-      if (g.dres != nullptr) v = __fadd_rn(v, load_elem(g.dres, g.x_f32, base + i));
-      if (g.x_f32) static_cast<float*>(g.dx)[base + i] = v;
-      else static_cast<uint16_t*>(g.dx)[base + i] = bf16_of(v);
+  }
+  const float var = __fmul_rn(row_sum<1024>(v, red[1]), inv_h);
+  const float rstd = 1.0f / __fsqrt_rn(__fadd_rn(var, g.eps));
+  if (threadIdx.x == 0) {
+    if (g.mean != nullptr) g.mean[r] = mean;
+    if (g.rstd != nullptr) g.rstd[r] = rstd;
+  }
+  const float rs = g.out_kind == 1 ? 1.0f / *g.sy : 0.0f;
+  for (int64_t i = 8 * (int64_t)threadIdx.x; i < g.H; i += 8 * 1024) {
+    float f[8];
+    values8<F32>(load8<F32>(xr, i, g.H), f);
+    norm8(g, i, mean, rstd, f);
+    emit8(g, base, i, rs, f);
+  }
+  }
+}
+
+// Backward pass.  A workgroup of T threads (T a multiple of 64 that covers the
+// row: U groups of eight columns per thread) walks the rows of its slab: the
+// row's two sums through one barrier, dx, and the columns' sums of dy xh and
+// dy in registers, which go to part[slab, 0:H) and [H:2H) at the end.  The
+// next row's x, dy and dres are loaded before this row's sums.
+template <bool XF, bool DF, int U>
+__global__ __launch_bounds__(1024) void layer_norm_backward_kernel(LayerNormBwdArgs g, int64_t slab_rows,
+                                                                   float* __restrict__ part) {
+  __shared__ float red[2][2][16];
+  const int T = blockDim.x, waves = T >> 6, t = threadIdx.x;
+  const float inv_h = 1.0f / (float)g.H;
+  const int64_t r0 = (int64_t)blockIdx.x * slab_rows;
+  const int64_t r1 = r0 + slab_rows < g.rows ? r0 + slab_rows : g.rows;
+  float w[U][8], sw[U][8], sb[U][8];
+#pragma unroll
+  for (int j = 0; j < U; ++j) {
+    const int64_t i = 8 * (int64_t)(j * T + t);
+    if (g.w != nullptr) load8_values(g.w, g.w_f32, i, g.H, w[j]);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (g.w == nullptr) w[j][k] = 1.0f;
+      sw[j][k] = sb[j][k] = 0.0f;
+    }
+  }
+  Raw8<XF> x[U], rs[U];
+  Raw8<DF> d[U];
+  float mean = 0.0f, rstd = 0.0f;
+  auto load = [&](int64_t r) {
+    const int64_t base = r * g.H;
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int64_t i = 8 * (int64_t)(j * T + t);
+      x[j] = load8<XF>(static_cast<const uint8_t*>(g.x) + base * (XF ? 4 : 2), i, g.H);
+      d[j] = load8<DF>(static_cast<const uint8_t*>(g.dy) + base * (DF ? 4 : 2), i, g.H);
+      if (g.dres != nullptr) rs[j] = load8<XF>(static_cast<const uint8_t*>(g.dres) + base * (XF ? 4 : 2), i, g.H);
+    }
+    mean = g.mean[r];
+    rstd = g.rstd[r];
+  };
+  if (r0 < r1) load(r0);
+  int buf = 0;
+  for (int64_t r = r0; r < r1; ++r, buf ^= 1) {
+    // xh and g = dy w of this row; dy's sums
+    float xh[U][8], gw[U][8], res[U][8];
+    const float rstd_r = rstd;
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      float dy[8];
+      values8<XF>(x[j], xh[j]);
+      values8<DF>(d[j], dy);
+      if (g.dres != nullptr) values8<XF>(rs[j], res[j]);
+      const int64_t left = g.H - 8 * (int64_t)(j * T + t);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        xh[j][k] = k < left ? __fmul_rn(__fadd_rn(xh[j][k], -mean), rstd) : 0.0f;
+        gw[j][k] = __fmul_rn(dy[k], w[j][k]);
+        s1 = __fadd_rn(s1, gw[j][k]);
+        s2 = __builtin_fmaf(gw[j][k], xh[j][k], s2);
+        sw[j][k] = __builtin_fmaf(dy[k], xh[j][k], sw[j][k]);
+        sb[j][k] = __fadd_rn(sb[j][k], dy[k]);
+      }
+    }
+    if (r + 1 < r1) load(r + 1);
+    s1 = wave_sum(s1);
+    s2 = wave_sum(s2);
+    if ((t & 63) == 0) {
+      red[buf][0][t >> 6] = s1;
+      red[buf][1][t >> 6] = s2;
+    }
+    __syncthreads();   // the other buffer's readers are past the barrier before this one
+    s1 = red[buf][0][0];
+    s2 = red[buf][1][0];
+    for (int v = 1; v < waves; ++v) {
+      s1 = __fadd_rn(s1, red[buf][0][v]);
+      s2 = __fadd_rn(s2, red[buf][1][v]);
+    }
+    const float c1 = __fmul_rn(s1, inv_h), c2 = __fmul_rn(s2, inv_h);
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int64_t i = 8 * (int64_t)(j * T + t);
+      if (i < g.H) {
+        float y[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          y[k] = __fmul_rn(rstd_r, __builtin_fmaf(-xh[j][k], c2, __fadd_rn(gw[j][k], -c1)));
+          if (g.dres != nullptr) y[k] = __fadd_rn(y[k], res[j][k]);
+        }
+        if constexpr (XF) store8_f32(static_cast<float*>(g.dx) + r * g.H, i, g.H, y);
+        else store8_bf16(static_cast<uint16_t*>(g.dx) + r * g.H, i, g.H, y);
+      }
+    }
+  }
+  if (part != nullptr) {
+    float* p = part + (int64_t)blockIdx.x * 2 * g.H;
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int64_t i = 8 * (int64_t)(j * T + t);
+      if (i < g.H) {
+        store8_f32(p, i, g.H, sw[j]);
+        store8_f32(p + g.H, i, g.H, sb[j]);
+      }
     }
   }
 }
 
-// Column sums of dy xh and dy over a slab of rows: part[slab, 0:H) and [H:2H).
-__global__ __launch_bounds__(kThreads) void layer_norm_dw_kernel(LayerNormBwdArgs g, int64_t slab_rows,
+// Rows too long for that: column sums first (dx may be written over dy or x),
+// eight columns per thread over a slab, then dx with two reads of the row.
+__global__ __launch_bounds__(256) void layer_norm_dw_long_kernel(LayerNormBwdArgs g, int64_t slab_rows,
                                                                  float* __restrict__ part) {
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int64_t i = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
   if (i >= g.H) return;
   const int64_t r0 = (int64_t)blockIdx.y * slab_rows;
   const int64_t r1 = r0 + slab_rows < g.rows ? r0 + slab_rows : g.rows;
-  float sw = 0.0f, sb = 0.0f;
+  float sw[8] = {}, sb[8] = {};
   for (int64_t r = r0; r < r1; ++r) {
-    const float xh = __fmul_rn(__fadd_rn(load_elem(g.x, g.x_f32, r * g.H + i), -g.mean[r]), g.rstd[r]);
-    const float d = load_elem(g.dy, g.dy_f32, r * g.H + i);
-    sw = __builtin_fmaf(d, xh, sw);
-    sb = __fadd_rn(sb, d);
+    float x[8], d[8];
+    load8_values(static_cast<const uint8_t*>(g.x) + r * g.H * (g.x_f32 ? 4 : 2), g.x_f32, i, g.H, x);
+    load8_values(static_cast<const uint8_t*>(g.dy) + r * g.H * (g.dy_f32 ? 4 : 2), g.dy_f32, i, g.H, d);
+    const float mean = g.mean[r], rstd = g.rstd[r];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      sw[k] = __builtin_fmaf(d[k], __fmul_rn(__fadd_rn(x[k], -mean), rstd), sw[k]);
+      sb[k] = __fadd_rn(sb[k], d[k]);
+    }
   }
   float* p = part + (int64_t)blockIdx.y * 2 * g.H;
-  p[i] = sw;
-  p[g.H + i] = sb;
+  store8_f32(p, i, g.H, sw);
+  store8_f32(p + g.H, i, g.H, sb);
 }
 
-// out[n] = sum over slabs of part[slab, n], in slab order (row stride ld).
-__global__ __launch_bounds__(kThreads) void sum_slabs_kernel(const float* __restrict__ part,
-                                                             float* __restrict__ out, int64_t slabs,
-                                                             int64_t N, int64_t ld) {
-  const int64_t n = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (n >= N) return;
-  float s = 0.0f;
-  for (int64_t p = 0; p < slabs; ++p) s = __fadd_rn(s, part[p * ld + n]);
-  out[n] = s;
+__global__ __launch_bounds__(1024) void layer_norm_dx_long_kernel(LayerNormBwdArgs g) {
+  __shared__ float red[2][16];
+  const float inv_h = 1.0f / (float)g.H;
+  for (int64_t r = blockIdx.x; r < g.rows; r += gridDim.x) {
+  const uint8_t* xr = static_cast<const uint8_t*>(g.x) + r * g.H * (g.x_f32 ? 4 : 2);
+  const uint8_t* dr = static_cast<const uint8_t*>(g.dy) + r * g.H * (g.dy_f32 ? 4 : 2);
+  const float mean = g.mean[r], rstd = g.rstd[r];
+  auto row8 = [&](int64_t i, float* xh, float* gw) {
+    load8_values(xr, g.x_f32, i, g.H, xh);
+    load8_values(dr, g.dy_f32, i, g.H, gw);
+    float w[8];
+    if (g.w != nullptr) load8_values(g.w, g.w_f32, i, g.H, w);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      xh[k] = i + k < g.H ? __fmul_rn(__fadd_rn(xh[k], -mean), rstd) : 0.0f;
+      if (g.w != nullptr) gw[k] = __fmul_rn(gw[k], w[k]);
+    }
+  };
+  float s1 = 0.0f, s2 = 0.0f, xh[8], gw[8];
+  for (int64_t i = 8 * (int64_t)threadIdx.x; i < g.H; i += 8 * 1024) {
+    row8(i, xh, gw);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      s1 = __fadd_rn(s1, gw[k]);
+      s2 = __builtin_fmaf(gw[k], xh[k], s2);
+    }
+  }
+  const float c1 = __fmul_rn(row_sum<1024>(s1, red[0]), inv_h), c2 = __fmul_rn(row_sum<1024>(s2, red[1]), inv_h);
+  for (int64_t i = 8 * (int64_t)threadIdx.x; i < g.H; i += 8 * 1024) {
+    row8(i, xh, gw);
+    float y[8], res[8];
+    if (g.dres != nullptr)
+      load8_values(static_cast<const uint8_t*>(g.dres) + r * g.H * (g.x_f32 ? 4 : 2), g.x_f32, i, g.H, res);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      y[k] = __fmul_rn(rstd, __builtin_fmaf(-xh[k], c2, __fadd_rn(gw[k], -c1)));
+      if (g.dres != nullptr) y[k] = __fadd_rn(y[k], res[k]);
+    }
+    if (g.x_f32) store8_f32(static_cast<float*>(g.dx) + r * g.H, i, g.H, y);
+    else store8_bf16(static_cast<uint16_t*>(g.dx) + r * g.H, i, g.H, y);
+  }
+  }
+}
+
+// Column sums over slabs: out_a[n] (n < N) and out_b[n - N] (n >= N), either of
+// them NULL to leave it out, of part [slabs, cols] in an order that depends on
+// slabs alone.  A workgroup takes 64 columns, four per thread, and 16 threads
+// share a column's slabs.
+__global__ __launch_bounds__(256) void sum_slabs_kernel(const float* __restrict__ part, float* __restrict__ out_a,
+                                                        float* __restrict__ out_b, int64_t slabs, int64_t N,
+                                                        int64_t cols) {
+  __shared__ float red[16][64];
+  const int q = threadIdx.x & 15, s = threadIdx.x >> 4;
+  const int64_t n = (int64_t)blockIdx.x * 64 + 4 * q;
+  float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int64_t p = s; p < slabs; p += 16) {
+    const float* v = part + p * cols + n;
+    if (n + 4 <= cols) {
+      const f4 x = *reinterpret_cast<const f4a4*>(v);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) a[k] = __fadd_rn(a[k], x[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (n + k < cols) a[k] = __fadd_rn(a[k], v[k]);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) red[s][4 * q + k] = a[k];
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    float v = red[0][threadIdx.x];
+#pragma unroll
+    for (int p = 1; p < 16; ++p) v = __fadd_rn(v, red[p][threadIdx.x]);
+    const int64_t c = (int64_t)blockIdx.x * 64 + threadIdx.x;
+    if (c < N) {
+      if (out_a != nullptr) out_a[c] = v;
+    } else if (c < cols) {
+      if (out_b != nullptr) out_b[c - N] = v;
+    }
+  }
+}
+
+// Workgroups of a grid over rows; more rows than that are walked.
+unsigned row_grid(int64_t n) { return (unsigned)(n < (1 << 20) ? n : (1 << 20)); }
+
+template <bool F32, int T, int U>
+hipError_t run_norm(const LayerNormArgs& g, hipStream_t stream) {
+  constexpr int rpb = T < 256 ? 256 / T : 1;
+  hipLaunchKernelGGL((layer_norm_kernel<F32, T, U>), dim3(row_grid((g.rows + rpb - 1) / rpb)),
+                     dim3(T < 256 ? 256 : T), 0, stream, g);
+  return hipGetLastError();
+}
+
+template <bool F32>
+hipError_t norm_of_type(const LayerNormArgs& g, hipStream_t stream) {
+  const int64_t units = (g.H + 7) / 8;
+  if (units <= 64) return run_norm<F32, 64, 1>(g, stream);
+  if (units <= 128 && g.rows > 512) return run_norm<F32, 64, 2>(g, stream);
+  if (units <= 256) return run_norm<F32, 256, 1>(g, stream);
+  if (units <= 512 && g.rows > 512) return run_norm<F32, 256, 2>(g, stream);
+  if (units <= 768 && g.rows > 512) return run_norm<F32, 256, 3>(g, stream);
+  if (units <= 1024) return g.rows > 512 ? run_norm<F32, 256, 4>(g, stream) : run_norm<F32, 1024, 1>(g, stream);
+  if (units <= 2048) return run_norm<F32, 1024, 2>(g, stream);
+  if (units <= 4096) return run_norm<F32, 1024, 4>(g, stream);
+  hipLaunchKernelGGL((layer_norm_long_kernel<F32>), dim3(row_grid(g.rows)), dim3(1024), 0, stream, g);
+  return hipGetLastError();
+}
+
+// rows of up to this many elements go through layer_norm_backward_kernel
+constexpr int64_t kBwdRegs = 1024 * 8 * 2;
+
+template <bool XF, bool DF>
+hipError_t run_backward(const LayerNormBwdArgs& g, int64_t slabs, float* part, hipStream_t stream) {
+  const int64_t units = (g.H + 7) / 8, slab_rows = (g.rows + slabs - 1) / slabs;
+  const int u = units <= 1024 ? 1 : 2;
+  const unsigned threads = (unsigned)(((units + u - 1) / u + 63) / 64 * 64);
+  if (u == 1)
+    hipLaunchKernelGGL((layer_norm_backward_kernel<XF, DF, 1>), dim3((unsigned)slabs), dim3(threads), 0, stream, g,
+                       slab_rows, part);
+  else
+    hipLaunchKernelGGL((layer_norm_backward_kernel<XF, DF, 2>), dim3((unsigned)slabs), dim3(threads), 0, stream, g,
+                       slab_rows, part);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_sum_slabs(const float* part, float* out, int64_t slabs, int64_t N, hipStream_t stream) {
-  hipLaunchKernelGGL(sum_slabs_kernel, dim3((unsigned)((N + kThreads - 1) / kThreads)), dim3(kThreads), 0,
-                     stream, part, out, slabs, N, N);
+hipError_t launch_sum_slabs(const float* part, float* out_a, float* out_b, int64_t slabs, int64_t N, int64_t cols,
+                            hipStream_t stream) {
+  hipLaunchKernelGGL(sum_slabs_kernel, dim3((unsigned)((cols + 63) / 64)), dim3(256), 0, stream, part, out_a, out_b,
+                     slabs, N, cols);
   return hipGetLastError();
 }
 
-hipError_t launch_layer_norm(const LayerNormArgs& g, int num_cus, hipStream_t stream) {
-  const int64_t most = (int64_t)num_cus * 64;
-  hipLaunchKernelGGL(layer_norm_kernel, dim3((unsigned)(g.rows < most ? g.rows : most)), dim3(kThreads), 0,
-                     stream, g);
-  return hipGetLastError();
+hipError_t launch_layer_norm(const LayerNormArgs& g, hipStream_t stream) {
+  return g.x_f32 ? norm_of_type<true>(g, stream) : norm_of_type<false>(g, stream);
 }
 
 int64_t layer_norm_backward_slabs(int64_t rows, int64_t H) {
-  (void)H;
-  return rows < 32 ? (rows > 0 ? 1 : 0) : (rows / 32 < 256 ? rows / 32 : 256);
+  if (rows == 0) return 0;
+  const int64_t waves = ((H + 7) / 8 + 63) / 64;
+  // workgroups of about 16 waves per CU in all, at least 8 rows each
+  int64_t most = 256 * 16 / (waves < 16 ? waves : 16);
+  if (most > (rows + 7) / 8) most = (rows + 7) / 8;
+  return most;
 }
 
 hipError_t launch_layer_norm_backward(const LayerNormBwdArgs& g, float* dw, float* db, float* part,
-                                      int num_cus, hipStream_t stream) {
+                                      hipStream_t stream) {
   const int64_t slabs = layer_norm_backward_slabs(g.rows, g.H);
-  const unsigned gx = (unsigned)((g.H + kThreads - 1) / kThreads);
-  if (slabs > 0) {
-    const int64_t most = (int64_t)num_cus * 64;
-    // the column sums first: dx may be written over dy or x
-    if (dw != nullptr || db != nullptr)
-      hipLaunchKernelGGL(layer_norm_dw_kernel, dim3(gx, (unsigned)slabs), dim3(kThreads), 0, stream, g,
-                         (g.rows + slabs - 1) / slabs, part);
-    hipLaunchKernelGGL(layer_norm_dx_kernel, dim3((unsigned)(g.rows < most ? g.rows : most)),
-                       dim3(kThreads), 0, stream, g);
+  const bool sums = dw != nullptr || db != nullptr;
+  hipError_t e = hipSuccess;
+  if (slabs > 0 && g.H <= kBwdRegs) {
+    float* p = sums ? part : nullptr;
+    if (g.x_f32) e = g.dy_f32 ? run_backward<true, true>(g, slabs, p, stream) : run_backward<true, false>(g, slabs, p, stream);
+    else e = g.dy_f32 ? run_backward<false, true>(g, slabs, p, stream) : run_backward<false, false>(g, slabs, p, stream);
+  } else if (slabs > 0) {
+    if (sums)
+      hipLaunchKernelGGL(layer_norm_dw_long_kernel, dim3((unsigned)((g.H + 2047) / 2048), (unsigned)slabs), dim3(256),
+                         0, stream, g, (g.rows + slabs - 1) / slabs, part);
+    hipLaunchKernelGGL(layer_norm_dx_long_kernel, dim3(row_grid(g.rows)), dim3(1024), 0, stream, g);
+    e = hipGetLastError();
   }
-  if (dw != nullptr)
-    hipLaunchKernelGGL(sum_slabs_kernel, dim3(gx), dim3(kThreads), 0, stream, part, dw, slabs, g.H, 2 * g.H);
-  if (db != nullptr)
-    hipLaunchKernelGGL(sum_slabs_kernel, dim3(gx), dim3(kThreads), 0, stream, part + g.H, db, slabs, g.H,
-                       2 * g.H);
-  return hipGetLastError();
+  if (e != hipSuccess || !sums) return e;
+  return launch_sum_slabs(part, dw, db, slabs, g.H, 2 * g.H, stream);
 }
 
 }  // namespace fp8mot

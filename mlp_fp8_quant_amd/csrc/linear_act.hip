@@ -14,6 +14,7 @@
 #include "gemm_parts.h"
 #include "kernels.h"
 #include "linear_epilogue.h"
+#include "rowwise.h"
 
 namespace fp8mot {
 
@@ -23,8 +24,6 @@ using tile::decode8;
 using tile::f16x8;
 using tile::v4f;
 using tile::v4i;
-
-__device__ __forceinline__ uint16_t bf16_of(float v) { return (uint16_t)bf16x2_rne(v, v); }
 
 // Products of few rows.  A workgroup computes 16 * MB rows of X against 16 * NB
 // rows of W; its NW waves take the 128-K stages of K in turn, each through a
@@ -219,27 +218,75 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearActArgs g, const
   }
 }
 
-// dz = dy act'(pre) for kActRows rows of 256 columns, one column per thread,
-// with the column's sum over those rows (of dz before its rounding to BF16)
-// into part[slab, n].
-constexpr int kThreads = 256;
+// dz = dy act'(pre) for a slab of rows and 8 LP columns, with the columns'
+// sums over the slab (of dz before its rounding to BF16) into part[slab, n].
+// Bound by memory.  LP threads side by side hold eight consecutive columns
+// each, kActThreads / LP of them share the slab's rows (narrow tensors thus
+// keep all lanes busy) and are added through LDS in order; R rows are in
+// flight per thread.
+constexpr int kActThreads = 256;
 
-__global__ __launch_bounds__(kThreads) void act_backward_kernel(
-    const uint16_t* __restrict__ dy, const uint16_t* __restrict__ pre, int act,
-    uint16_t* __restrict__ dz, float* __restrict__ part, int64_t M, int64_t N, int64_t slab_rows) {
-  const int64_t n = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (n >= N) return;
+template <int LP>
+__global__ __launch_bounds__(kActThreads) void act_backward_kernel(
+    const uint16_t* dy, const uint16_t* pre, int act, uint16_t* dz, float* __restrict__ part, int64_t M, int64_t N,
+    int64_t slab_rows) {
+  constexpr int RL = kActThreads / LP, R = 4;
+  __shared__ float red[RL][LP * 8];
+  const int cl = threadIdx.x % LP, rl = threadIdx.x / LP;
+  const int64_t n = ((int64_t)blockIdx.x * LP + cl) * 8;
   const int64_t r0 = (int64_t)blockIdx.y * slab_rows;
   const int64_t r1 = r0 + slab_rows < M ? r0 + slab_rows : M;
-  float s = 0.0f;
-  for (int64_t r = r0; r < r1; ++r) {
-    const int64_t i = r * N + n;
-    float d = bf16_to_f32(dy[i]);
-    if (act != kActNone) d = __fmul_rn(d, act_slope(bf16_to_f32(pre[i]), act));
-    if (dz != nullptr) dz[i] = bf16_of(d);
-    s = __fadd_rn(s, d);
+  float s[8] = {};
+  if (n < N) {
+    for (int64_t r = r0 + rl; r < r1; r += RL * R) {
+      rows::Raw8<false> d[R], z[R];
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        if (r + k * RL < r1) {
+          d[k] = rows::load8<false>(dy + (r + k * RL) * N, n, N);
+          if (act != kActNone) z[k] = rows::load8<false>(pre + (r + k * RL) * N, n, N);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        if (r + k * RL < r1) {
+          float v[8], a[8];
+          rows::values8<false>(d[k], v);
+          if (act != kActNone) {
+            rows::values8<false>(z[k], a);
+            slope_all<8>(a, act);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) v[c] = __fmul_rn(v[c], a[c]);
+          }
+          if (dz != nullptr) rows::store8_bf16(dz + (r + k * RL) * N, n, N, v);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) s[c] = __fadd_rn(s[c], v[c]);
+        }
+      }
+    }
   }
-  if (part != nullptr) part[(int64_t)blockIdx.y * N + n] = s;
+  if (part == nullptr) return;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) red[rl][cl * 8 + c] = s[c];
+  __syncthreads();
+  for (int c = threadIdx.x; c < LP * 8; c += kActThreads) {
+    float v = red[0][c];
+#pragma unroll
+    for (int k = 1; k < RL; ++k) v = __fadd_rn(v, red[k][c]);
+    const int64_t at = (int64_t)blockIdx.x * (LP * 8) + c;
+    if (at < N) part[(int64_t)blockIdx.y * N + at] = v;
+  }
+}
+
+// Threads side by side: the row's groups of eight, up to 64.
+int act_lanes(int64_t N) { return N <= 64 ? 8 : N <= 128 ? 16 : N <= 256 ? 32 : 64; }
+
+template <int LP>
+hipError_t run_act_backward(const uint16_t* dy, const uint16_t* pre, int act, uint16_t* dz, float* part, int64_t M,
+                            int64_t N, int64_t slabs, hipStream_t stream) {
+  hipLaunchKernelGGL((act_backward_kernel<LP>), dim3((unsigned)((N + LP * 8 - 1) / (LP * 8)), (unsigned)slabs),
+                     dim3(kActThreads), 0, stream, dy, pre, act, dz, part, M, N, (M + slabs - 1) / slabs);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -327,23 +374,31 @@ hipError_t launch_linear_act(const LinearActArgs& g, int accum, float* ws, int n
 }
 
 int64_t act_backward_slabs(int64_t M, int64_t N) {
-  (void)N;
-  return M < 64 ? (M > 0 ? 1 : 0) : (M / 64 < 64 ? M / 64 : 64);
+  if (M == 0 || N == 0) return 0;
+  // about eight workgroups per CU, at least two passes over the rows in flight each
+  const int64_t lp = act_lanes(N), across = (N + lp * 8 - 1) / (lp * 8), rl = kActThreads / lp;
+  int64_t slabs = (256 * 8 + across - 1) / across;
+  const int64_t most = (M + rl * 8 - 1) / (rl * 8);
+  if (slabs > most) slabs = most;
+  return slabs < 1 ? 1 : slabs;
 }
 
 hipError_t launch_act_backward(const uint16_t* dy, const uint16_t* pre, int act, uint16_t* dz,
                                float* dbias, int64_t M, int64_t N, float* part, hipStream_t stream) {
   const int64_t slabs = act_backward_slabs(M, N);
   if (slabs > 0) {
-    const int64_t slab_rows = (M + slabs - 1) / slabs;
-    hipLaunchKernelGGL(act_backward_kernel, dim3((unsigned)((N + kThreads - 1) / kThreads), (unsigned)slabs),
-                       dim3(kThreads), 0, stream, dy, pre, act, dz, dbias != nullptr ? part : nullptr, M, N,
-                       slab_rows);
-    const hipError_t e = hipGetLastError();
+    float* p = dbias != nullptr ? part : nullptr;
+    hipError_t e;
+    switch (act_lanes(N)) {
+      case 8: e = run_act_backward<8>(dy, pre, act, dz, p, M, N, slabs, stream); break;
+      case 16: e = run_act_backward<16>(dy, pre, act, dz, p, M, N, slabs, stream); break;
+      case 32: e = run_act_backward<32>(dy, pre, act, dz, p, M, N, slabs, stream); break;
+      default: e = run_act_backward<64>(dy, pre, act, dz, p, M, N, slabs, stream); break;
+    }
     if (e != hipSuccess) return e;
   }
   if (dbias == nullptr) return hipSuccess;
-  return launch_sum_slabs(part, dbias, slabs, N, stream);
+  return launch_sum_slabs(part, dbias, nullptr, slabs, N, N, stream);
 }
 
 }  // namespace fp8mot

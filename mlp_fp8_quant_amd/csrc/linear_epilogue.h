@@ -102,31 +102,6 @@ __device__ __forceinline__ void store4_fp8(const Rows& t, int at, int nv, const 
   }
 }
 
-// The activation over n values: the switch is outside the loops, so that only
-// the chosen one's instructions are fetched.
-template <int n>
-__device__ __forceinline__ void act_all(float* z, int act) {
-  switch (act) {
-    case kActRelu:
-#pragma unroll
-      for (int i = 0; i < n; ++i) z[i] = act_value(z[i], kActRelu);
-      break;
-    case kActGelu:
-#pragma unroll
-      for (int i = 0; i < n; ++i) z[i] = act_value(z[i], kActGelu);
-      break;
-    case kActGeluTanh:
-#pragma unroll
-      for (int i = 0; i < n; ++i) z[i] = act_value(z[i], kActGeluTanh);
-      break;
-    case kActSilu:
-#pragma unroll
-      for (int i = 0; i < n; ++i) z[i] = act_value(z[i], kActSilu);
-      break;
-    default: break;
-  }
-}
-
 // What the epilogue needs of a launch and of a workgroup's rows, read once.
 struct Epilogue {
   Rows y, residual, pre;
