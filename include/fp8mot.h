@@ -366,7 +366,7 @@ size_t fp8_linear_act_backward_workspace(int64_t M, int64_t N);
  * dy, pre, dz: BF16 [M, N]; dbias: FP32 [N]; all 16-byte aligned.  dz or
  * dbias may be NULL (not computed), and with FP8MOT_ACT_NONE pre too.  dz may
  * be dy or pre itself.  relu's slope at 0 is 0.  M == 0 writes dbias = 0.
- * M up to INT32_MAX, N up to 2^28.
+ * M up to INT32_MAX, N up to 2^26.
  * ws: 16-byte aligned, at least fp8_linear_act_backward_workspace(M, N)
  * bytes; unused where dbias is NULL. */
 int fp8_linear_act_backward(const uint16_t* dy, const uint16_t* pre, int act, uint16_t* dz,
@@ -387,7 +387,7 @@ int fp8_linear_act_backward(const uint16_t* dy, const uint16_t* pre, int act, ui
  * x: [rows, H] of x_elem (fp8mot_elem); weight, bias: [H] of wb_elem, either
  * may be NULL (ones, zeros); y: [rows, H]; mean, rstd: FP32 [rows] for the
  * backward pass, or NULL.  eps finite and >= 0.  y may be x itself where the
- * element types agree; no other overlap.  H up to 2^28, rows up to INT32_MAX;
+ * element types agree; no other overlap.  H up to 2^26, rows up to INT32_MAX;
  * x, y, weight, bias 16-byte aligned.  A row that holds a NaN or an infinity becomes NaN. */
 int fp8_layer_norm(const void* x, int x_elem, const void* weight, const void* bias,
                    int wb_elem, void* y, int out_kind, const float* d_sy, float* mean,

@@ -12,6 +12,7 @@ are ``torch.uint8`` holding E4M3FN codes; scales are one-element
 """
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -24,7 +25,6 @@ ACC_EXACT, ACC_FP8_MFMA = 0, 1
 ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
 OBS_MAX, OBS_MOVING_AVG = 0, 1
 CONV_E4M3_PACKED, CONV_E4M3_INT, CONV_BF16 = 0, 1, 2
-_ELEM = {torch.bfloat16: 0, torch.float32: 1}     # FP8MOT_ELEM_*
 _OUT_DTYPE = {OUT_BF16: torch.bfloat16, OUT_FP8: torch.uint8, OUT_F32: torch.float32}
 
 
@@ -169,17 +169,47 @@ def fp8_linear_rowwise(qx, qw, sx, sw, out_kind=OUT_BF16, out=None, accum=ACC_EX
     return out
 
 
-def _need_float(t, name, device=None, dtype=None):
-    """A BF16 or FP32 tensor (``dtype`` where only one of them fits); returns
-    its FP8MOT_ELEM code (0 for None)."""
+# The calls below take many small tensors and are made once per token, so
+# their checks are written for the common case: a plain tensor of the right
+# type on the right GPU passes with a few comparisons, anything else goes
+# through the checks above for its message.
+_Tensor = torch.Tensor
+_BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
+
+
+def _fit(t, name, dtype, dev, n=None, what=None):
+    if not (type(t) is _Tensor and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()):
+        _need(t, name, dtype, torch.device("cuda", dev))
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{name} must hold {what}")
+
+
+def _fit_float(t, name, dev, n, what, dtype=None):
+    """A BF16 or FP32 tensor of n elements (``dtype`` where only one of the
+    types fits), or None; returns its FP8MOT_ELEM code (0 for None)."""
     if t is None:
         return 0
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in _ELEM or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{name} must be {dtype or 'torch.bfloat16 or torch.float32'}, got {t.dtype}")
-    _need(t, name, t.dtype, device)
-    return _ELEM[t.dtype]
+    d = t.dtype
+    if (d is not _BF16 and d is not _F32) or (dtype is not None and d is not dtype):
+        raise ValueError(f"{name} must be {dtype or 'torch.bfloat16 or torch.float32'}, got {d}")
+    _fit(t, name, d, dev, n, what)
+    return 1 if d is _F32 else 0
+
+
+def _on_gpu(t, name, dtype=None):
+    """The device index of a call's first tensor, checked by itself."""
+    if not isinstance(t, _Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if dtype is None and t.dtype is not _BF16 and t.dtype is not _F32:
+        raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    dev = t.get_device()
+    if dev < 0 or not t.is_contiguous() or (dtype is not None and t.dtype is not dtype):
+        _need(t, name, dtype or t.dtype)
+    if t.dim() == 0:
+        raise ValueError(f"{name} must have a last dimension")
+    return dev
 
 
 def _out_dtype(out_kind):
@@ -189,13 +219,27 @@ def _out_dtype(out_kind):
     return dtype
 
 
-def _opt_workspace(nbytes, device, ws):
-    # like _workspace, but a call that needs none gets none
-    return None if ws is None and nbytes == 0 else _workspace(nbytes, device, ws)
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(func, *sizes):
+    # a pure function of the sizes
+    return int(getattr(_lib.lib(), func)(*sizes))
+
+
+def _scratch(func, sizes, t, ws):
+    """(pointer, bytes) of a call's workspace: the caller's, a new one, or
+    none where the sizes need none."""
+    if ws is None:
+        nb = _workspace_bytes(func, *sizes)
+        if nb == 0:
+            return None, None, 0
+        ws = t.new_empty(nb, dtype=_U8)
+    else:
+        _fit(ws, "workspace", _U8, t.get_device())
+    return ws, ws.data_ptr(), ws.numel()
 
 
 def fp8_linear_act_workspace(M, N, K):
-    return int(_lib.lib().fp8_linear_act_workspace(M, N, K))
+    return _workspace_bytes("fp8_linear_act_workspace", M, N, K)
 
 
 def fp8_linear_act(qx, qw, sx, sw, bias=None, act=ACT_NONE, residual=None, out_kind=OUT_BF16,
@@ -210,53 +254,49 @@ def fp8_linear_act(qx, qw, sx, sw, bias=None, act=ACT_NONE, residual=None, out_k
     qx and sw one per row of qw (as fp8_linear_rowwise); else one scale each.
     ``pre``: True, or a BF16 tensor [..., N], keeps the activation's argument
     for fp8_linear_act_backward and makes the call return (y, pre)."""
-    _need(qx, "qx", torch.uint8)
-    dev = qx.device
-    _need(qw, "qw", torch.uint8, dev)
-    if qw.dim() != 2 or qx.dim() < 1 or qx.shape[-1] != qw.shape[1]:
+    dev = _on_gpu(qx, "qx", _U8)
+    _fit(qw, "qw", _U8, dev)
+    shape = qx.shape
+    if qw.dim() != 2 or shape[-1] != qw.shape[1]:
         raise ValueError("shapes: qx [..., K], qw [N, K]")
     N, K = qw.shape
-    M = math.prod(qx.shape[:-1])
+    M = qx.numel() // K if K else math.prod(shape[:-1])
     if rowwise:
-        _need(sx, "sx", torch.float32, dev)
-        _need(sw, "sw", torch.float32, dev)
-        if sx.numel() != M or sw.numel() != N:
-            raise ValueError("sx must hold one scale per row of qx and sw one per row of qw")
+        _fit(sx, "sx", _F32, dev, M, "one scale per row of qx")
+        _fit(sw, "sw", _F32, dev, N, "one scale per row of qw")
     else:
-        _scale(sx, "sx", dev)
-        _scale(sw, "sw", dev)
+        if sx is not None:   # the library refuses a NULL scale (dynamic quantization)
+            _fit(sx, "sx", _F32, dev, 1, "exactly one float32")
+        if sw is not None:
+            _fit(sw, "sw", _F32, dev, 1, "exactly one float32")
     dtype = _out_dtype(out_kind)
-    if out_kind == OUT_FP8:
-        _scale(sy, "sy", dev)
-    bias_elem = _need_float(bias, "bias", dev)
-    if bias is not None and bias.numel() != N:
-        raise ValueError("bias must hold N elements")
-    res_elem = _need_float(residual, "residual", dev)
-    if residual is not None and residual.numel() != M * N:
-        raise ValueError("residual must hold M * N elements")
-    shape = (*qx.shape[:-1], N)
+    sy_ptr = None
+    if out_kind == OUT_FP8 and sy is not None:
+        _fit(sy, "sy", _F32, dev, 1, "exactly one float32")
+        sy_ptr = sy.data_ptr()
+    bias_elem = _fit_float(bias, "bias", dev, N, "N elements")
+    res_elem = _fit_float(residual, "residual", dev, M * N, "M * N elements")
+    out_shape = (*shape[:-1], N)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dev)
-    _need(out, "out", dtype, dev)
-    if out.numel() != M * N:
-        raise ValueError("out must hold M * N elements")
+        out = qx.new_empty(out_shape, dtype=dtype)
+    else:
+        _fit(out, "out", dtype, dev, M * N, "M * N elements")
     keep = None
     if pre is not False and pre is not None:
-        keep = torch.empty(shape, dtype=torch.bfloat16, device=dev) if pre is True else pre
-        _need(keep, "pre", torch.bfloat16, dev)
-        if keep.numel() != M * N:
-            raise ValueError("pre must hold M * N elements")
-    nb = fp8_linear_act_workspace(M, N, K)
-    ws = _opt_workspace(nb, dev, workspace)
-    _lib.call("fp8_linear_act", _ptr(qx), _ptr(qw), _ptr(out), M, N, K, _ptr(sx), _ptr(sw),
-              int(bool(rowwise)), _ptr(bias), bias_elem, act, _ptr(residual), res_elem,
-              _ptr(keep), out_kind, _ptr(sy) if out_kind == OUT_FP8 else None, accum,
-              _ptr(ws), ws.numel() if ws is not None else 0, _stream(qx))
+        if pre is True:
+            keep = qx.new_empty(out_shape, dtype=_BF16)
+        else:
+            keep = pre
+            _fit(keep, "pre", _BF16, dev, M * N, "M * N elements")
+    _ws, ws_ptr, ws_bytes = _scratch("fp8_linear_act_workspace", (M, N, K), qx, workspace)
+    _lib.call("fp8_linear_act", qx.data_ptr(), qw.data_ptr(), out.data_ptr(), M, N, K, _ptr(sx), _ptr(sw),
+              1 if rowwise else 0, _ptr(bias), bias_elem, act, _ptr(residual), res_elem, _ptr(keep),
+              out_kind, sy_ptr, accum, ws_ptr, ws_bytes, _stream(qx))
     return out if keep is None else (out, keep)
 
 
 def fp8_linear_act_backward_workspace(M, N):
-    return int(_lib.lib().fp8_linear_act_backward_workspace(M, N))
+    return _workspace_bytes("fp8_linear_act_backward_workspace", M, N)
 
 
 def fp8_linear_act_backward(dy, pre, act=ACT_NONE, dz=None, dbias=None, workspace=None):
@@ -265,27 +305,23 @@ def fp8_linear_act_backward(dy, pre, act=ACT_NONE, dz=None, dbias=None, workspac
     rows (FP32 [N], summed before the rounding of dz).  ``pre`` is what
     fp8_linear_act kept (None allowed for ACT_NONE); ``dz`` may be dy or pre
     itself."""
-    _need(dy, "dy", torch.bfloat16)
-    dev = dy.device
-    if dy.dim() == 0:
-        raise ValueError("dy must have a last (N) dimension")
+    dev = _on_gpu(dy, "dy", _BF16)
+    n = dy.numel()
     N = dy.shape[-1]
-    M = math.prod(dy.shape[:-1])
+    M = n // N if N else 0
     if pre is not None:
-        _need(pre, "pre", torch.bfloat16, dev)
-        if pre.numel() != M * N:
-            raise ValueError("pre must have as many elements as dy")
+        _fit(pre, "pre", _BF16, dev, n, "as many elements as dy")
     if dz is None:
-        dz = torch.empty(dy.shape, dtype=torch.bfloat16, device=dev)
+        dz = torch.empty_like(dy)
+    else:
+        _fit(dz, "dz", _BF16, dev, n, "as many elements as dy")
     if dbias is None:
-        dbias = torch.empty(N, dtype=torch.float32, device=dev)
-    _need(dz, "dz", torch.bfloat16, dev)
-    _need(dbias, "dbias", torch.float32, dev)
-    if dz.numel() != M * N or dbias.numel() != N:
-        raise ValueError("dz must have as many elements as dy and dbias N")
-    ws = _opt_workspace(fp8_linear_act_backward_workspace(M, N), dev, workspace)
-    _lib.call("fp8_linear_act_backward", _ptr(dy), _ptr(pre), act, _ptr(dz), _ptr(dbias), M, N,
-              _ptr(ws), ws.numel() if ws is not None else 0, _stream(dy))
+        dbias = dy.new_empty(N, dtype=_F32)
+    else:
+        _fit(dbias, "dbias", _F32, dev, N, "N elements")
+    _ws, ws_ptr, ws_bytes = _scratch("fp8_linear_act_backward_workspace", (M, N), dy, workspace)
+    _lib.call("fp8_linear_act_backward", dy.data_ptr(), _ptr(pre), act, dz.data_ptr(), dbias.data_ptr(), M, N,
+              ws_ptr, ws_bytes, _stream(dy))
     return dz, dbias
 
 
@@ -297,38 +333,34 @@ def fp8_layer_norm(x, weight=None, bias=None, eps=1e-5, out_kind=OUT_BF16, sy=No
     both BF16 or both FP32, or None.  ``stats`` makes the call return
     (y, mean, rstd), FP32 [...], for fp8_layer_norm_backward.  ``out`` may be
     x itself where the types agree."""
-    x_elem = _need_float(x, "x")
-    if x is None or x.dim() == 0:
-        raise ValueError("x must be a tensor with a last (H) dimension")
-    dev = x.device
+    dev = _on_gpu(x, "x")
+    xt = x.dtype
+    n = x.numel()
     H = x.shape[-1]
-    rows = math.prod(x.shape[:-1])
-    wb_elem = _need_float(weight, "weight", dev)
-    b_elem = _need_float(bias, "bias", dev, weight.dtype if weight is not None else None)
-    for t, n in ((weight, "weight"), (bias, "bias")):
-        if t is not None and t.numel() != H:
-            raise ValueError(f"{n} must hold H elements")
+    rows = n // H if H else 0
+    wb_elem = _fit_float(weight, "weight", dev, H, "H elements")
+    b_elem = _fit_float(bias, "bias", dev, H, "H elements", None if weight is None else weight.dtype)
     dtype = _out_dtype(out_kind)
-    if out_kind == OUT_FP8:
-        _scale(sy, "sy", dev)
+    sy_ptr = None
+    if out_kind == OUT_FP8 and sy is not None:
+        _fit(sy, "sy", _F32, dev, 1, "exactly one float32")
+        sy_ptr = sy.data_ptr()
     if out is None:
-        out = torch.empty(x.shape, dtype=dtype, device=dev)
-    _need(out, "out", dtype, dev)
-    if out.numel() != rows * H:
-        raise ValueError("out must have as many elements as x")
+        out = torch.empty_like(x) if dtype is xt else x.new_empty(x.shape, dtype=dtype)
+    else:
+        _fit(out, "out", dtype, dev, n, "as many elements as x")
     mean = rstd = None
     if stats:
-        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-    _lib.call("fp8_layer_norm", _ptr(x), x_elem, _ptr(weight), _ptr(bias),
-              wb_elem if weight is not None else b_elem, _ptr(out), out_kind,
-              _ptr(sy) if out_kind == OUT_FP8 else None, _ptr(mean), _ptr(rstd), rows, H,
-              float(eps), _stream(x))
+        mean = x.new_empty(x.shape[:-1], dtype=_F32)
+        rstd = torch.empty_like(mean)
+    _lib.call("fp8_layer_norm", x.data_ptr(), 1 if xt is _F32 else 0, _ptr(weight), _ptr(bias),
+              wb_elem if weight is not None else b_elem, out.data_ptr(), out_kind, sy_ptr, _ptr(mean),
+              _ptr(rstd), rows, H, eps, _stream(x))
     return (out, mean, rstd) if stats else out
 
 
 def fp8_layer_norm_backward_workspace(rows, H):
-    return int(_lib.lib().fp8_layer_norm_backward_workspace(rows, H))
+    return _workspace_bytes("fp8_layer_norm_backward_workspace", rows, H)
 
 
 def fp8_layer_norm_backward(dy, x, weight, mean, rstd, dres=None, dx=None, dweight=None,
@@ -338,40 +370,34 @@ def fp8_layer_norm_backward(dy, x, weight, mean, rstd, dres=None, dx=None, dweig
     fp8_layer_norm(stats=True) returned; ``dres`` (x's type) is the gradient
     that reaches x past the norm and is added to dx before its rounding; dx
     has x's type, dweight and dbias are FP32 [H]."""
-    x_elem = _need_float(x, "x")
-    if x is None or x.dim() == 0:
-        raise ValueError("x must be a tensor with a last (H) dimension")
-    dev = x.device
+    dev = _on_gpu(x, "x")
+    xt = x.dtype
+    n = x.numel()
     H = x.shape[-1]
-    rows = math.prod(x.shape[:-1])
+    rows = n // H if H else 0
     if dy is None:
         raise ValueError("dy must be a tensor")
-    dy_elem = _need_float(dy, "dy", dev)
-    w_elem = _need_float(weight, "weight", dev)
-    _need_float(dres, "dres", dev, x.dtype)
-    _need(mean, "mean", torch.float32, dev)
-    _need(rstd, "rstd", torch.float32, dev)
+    dy_elem = _fit_float(dy, "dy", dev, n, "as many elements as x")
+    w_elem = _fit_float(weight, "weight", dev, H, "H elements")
+    _fit_float(dres, "dres", dev, n, "as many elements as x", xt)
+    _fit(mean, "mean", _F32, dev, rows, "one value per row")
+    _fit(rstd, "rstd", _F32, dev, rows, "one value per row")
     if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        dx = torch.empty_like(x)
+    else:
+        _fit(dx, "dx", xt, dev, n, "as many elements as x")
     if dweight is None:
-        dweight = torch.empty(H, dtype=torch.float32, device=dev)
+        dweight = x.new_empty(H, dtype=_F32)
+    else:
+        _fit(dweight, "dweight", _F32, dev, H, "H elements")
     if dbias is None:
-        dbias = torch.empty(H, dtype=torch.float32, device=dev)
-    _need(dx, "dx", x.dtype, dev)
-    _need(dweight, "dweight", torch.float32, dev)
-    _need(dbias, "dbias", torch.float32, dev)
-    for t, n in ((dy, "dy"), (dres, "dres"), (dx, "dx")):
-        if t is not None and t.numel() != rows * H:
-            raise ValueError(f"{n} must have as many elements as x")
-    for t, n in ((weight, "weight"), (dweight, "dweight"), (dbias, "dbias")):
-        if t is not None and t.numel() != H:
-            raise ValueError(f"{n} must hold H elements")
-    if mean.numel() != rows or rstd.numel() != rows:
-        raise ValueError("mean and rstd must hold one value per row")
-    ws = _opt_workspace(fp8_layer_norm_backward_workspace(rows, H), dev, workspace)
-    _lib.call("fp8_layer_norm_backward", _ptr(dy), dy_elem, _ptr(x), x_elem, _ptr(weight), w_elem,
-              _ptr(mean), _ptr(rstd), _ptr(dres), _ptr(dx), _ptr(dweight), _ptr(dbias), rows, H,
-              _ptr(ws), ws.numel() if ws is not None else 0, _stream(x))
+        dbias = torch.empty_like(dweight)
+    else:
+        _fit(dbias, "dbias", _F32, dev, H, "H elements")
+    _ws, ws_ptr, ws_bytes = _scratch("fp8_layer_norm_backward_workspace", (rows, H), x, workspace)
+    _lib.call("fp8_layer_norm_backward", dy.data_ptr(), dy_elem, x.data_ptr(), 1 if xt is _F32 else 0, _ptr(weight),
+              w_elem, mean.data_ptr(), rstd.data_ptr(), _ptr(dres), dx.data_ptr(), dweight.data_ptr(),
+              dbias.data_ptr(), rows, H, ws_ptr, ws_bytes, _stream(x))
     return dx, dweight, dbias
 
 

@@ -108,9 +108,9 @@ int check_linear(const uint8_t* qx, const uint8_t* qw, const void* y, int64_t M,
 // Argument checks of the Linear epilogue and the layer norm.
 bool elem_ok(int e) { return e == FP8MOT_ELEM_BF16 || e == FP8MOT_ELEM_F32; }
 bool act_ok(int a) { return a >= FP8MOT_ACT_NONE && a <= FP8MOT_ACT_SILU; }
-// rows at most INT32_MAX and at most 2^28 columns (32-bit counts of threads in
-// a launch); byte offsets are 64-bit
-constexpr int64_t kMaxColumns = int64_t(1) << 28;
+// rows at most INT32_MAX and at most 2^26 columns (a launch over the columns
+// counts its threads, 32 a column at most, in 32 bits); byte offsets are 64-bit
+constexpr int64_t kMaxColumns = int64_t(1) << 26;
 bool rows_ok(int64_t rows, int64_t cols) {
   return rows >= 0 && cols >= 0 && rows <= INT32_MAX && cols <= kMaxColumns;
 }

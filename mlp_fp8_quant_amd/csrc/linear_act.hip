@@ -375,10 +375,10 @@ hipError_t launch_linear_act(const LinearActArgs& g, int accum, float* ws, int n
 
 int64_t act_backward_slabs(int64_t M, int64_t N) {
   if (M == 0 || N == 0) return 0;
-  // about eight workgroups per CU, at least two passes over the rows in flight each
+  // about eight workgroups per CU, at least a row per thread
   const int64_t lp = act_lanes(N), across = (N + lp * 8 - 1) / (lp * 8), rl = kActThreads / lp;
   int64_t slabs = (256 * 8 + across - 1) / across;
-  const int64_t most = (M + rl * 8 - 1) / (rl * 8);
+  const int64_t most = (M + rl - 1) / rl;
   if (slabs > most) slabs = most;
   return slabs < 1 ? 1 : slabs;
 }

@@ -138,11 +138,11 @@ def test_binding_checks_shapes():
                 (ln, dict(weight=e(7)), "weight"), (ln, dict(bias=e(9)), "bias"),
                 (ln, dict(bias=e(8, t=bf)), "bias must be"), (ln, dict(x=e(8, 4).t()), "contiguous"),
                 (ln, dict(out=e(4, 8)), "out must be"), (ln, dict(x=e()), "last"),
-                (lb, dict(dy=e(4, 7)), "dy must have"), (lb, dict(dres=e(4, 8, t=bf)), "dres must be"),
+                (lb, dict(dy=e(4, 7)), "dy must hold"), (lb, dict(dres=e(4, 8, t=bf)), "dres must be"),
                 (lb, dict(mean=e(3)), "one value per row"), (lb, dict(dweight=e(7)), "dweight"),
                 (lb, dict(dx=e(4, 8, t=bf)), "dx must be"), (lb, dict(dy=None), "dy"),
-                (ab, dict(pre=e(4, 7, t=bf)), "pre must have"), (ab, dict(dy=e(4, 8)), "dy must be"),
-                (ab, dict(dbias=e(7)), "dbias"), (ab, dict(dz=e(3, 8, t=bf)), "dz must have")]:
+                (ab, dict(pre=e(4, 7, t=bf)), "pre must hold"), (ab, dict(dy=e(4, 8)), "dy must be"),
+                (ab, dict(dbias=e(7)), "dbias"), (ab, dict(dz=e(3, 8, t=bf)), "dz must hold")]:
             with pytest.raises(ValueError, match=match):
                 call(**args)
 
