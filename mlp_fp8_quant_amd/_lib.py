@@ -122,5 +122,10 @@ def call(name, *args):
         f = _funcs[name] = getattr(lib(), name)
     st = f(*args)
     if st != 0:
-        raise Fp8motError(name, st, lib().fp8mot_status_string(st).decode())
+        fail(name, st)
     return st
+
+
+def fail(name, st):
+    """Raise the error of a call that returned the status ``st``."""
+    raise Fp8motError(name, st, lib().fp8mot_status_string(st).decode())

@@ -169,10 +169,25 @@ def fp8_linear_rowwise(qx, qw, sx, sw, out_kind=OUT_BF16, out=None, accum=ACC_EX
     return out
 
 
-# The calls below take many small tensors and are made once per token, so
-# their checks are written for the common case: a plain tensor of the right
-# type on the right GPU passes with a few comparisons, anything else goes
-# through the checks above for its message.
+# The four calls below take many tensors and are made once per token or
+# training step.  Their common case -- plain contiguous tensors that fit, on
+# the current device -- is marshalled natively (csrc/binding.cpp), which
+# returns None for anything else and the status where the library refuses;
+# what follows the native call is every check and its message.
+_native = None
+
+
+def _load_native():
+    global _native
+    try:
+        from . import _binding
+    except ImportError as e:
+        raise RuntimeError("the native binding is missing or does not load: build it with "
+                           "`python -m mlp_fp8_quant_amd.build`") from e
+    _native = _binding
+    return _binding
+
+
 _Tensor = torch.Tensor
 _BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
 
@@ -254,6 +269,10 @@ def fp8_linear_act(qx, qw, sx, sw, bias=None, act=ACT_NONE, residual=None, out_k
     qx and sw one per row of qw (as fp8_linear_rowwise); else one scale each.
     ``pre``: True, or a BF16 tensor [..., N], keeps the activation's argument
     for fp8_linear_act_backward and makes the call return (y, pre)."""
+    r = (_native or _load_native()).linear_act(qx, qw, sx, sw, bias, act, residual, out_kind, sy,
+                                               rowwise, pre, out, accum, workspace)
+    if r is not None:
+        return r if type(r) is not int else _lib.fail("fp8_linear_act", r)
     dev = _on_gpu(qx, "qx", _U8)
     _fit(qw, "qw", _U8, dev)
     shape = qx.shape
@@ -305,6 +324,9 @@ def fp8_linear_act_backward(dy, pre, act=ACT_NONE, dz=None, dbias=None, workspac
     rows (FP32 [N], summed before the rounding of dz).  ``pre`` is what
     fp8_linear_act kept (None allowed for ACT_NONE); ``dz`` may be dy or pre
     itself."""
+    r = (_native or _load_native()).linear_act_backward(dy, pre, act, dz, dbias, workspace)
+    if r is not None:
+        return r if type(r) is not int else _lib.fail("fp8_linear_act_backward", r)
     dev = _on_gpu(dy, "dy", _BF16)
     n = dy.numel()
     N = dy.shape[-1]
@@ -333,6 +355,9 @@ def fp8_layer_norm(x, weight=None, bias=None, eps=1e-5, out_kind=OUT_BF16, sy=No
     both BF16 or both FP32, or None.  ``stats`` makes the call return
     (y, mean, rstd), FP32 [...], for fp8_layer_norm_backward.  ``out`` may be
     x itself where the types agree."""
+    r = (_native or _load_native()).layer_norm(x, weight, bias, eps, out_kind, sy, stats, out)
+    if r is not None:
+        return r if type(r) is not int else _lib.fail("fp8_layer_norm", r)
     dev = _on_gpu(x, "x")
     xt = x.dtype
     n = x.numel()
@@ -370,6 +395,10 @@ def fp8_layer_norm_backward(dy, x, weight, mean, rstd, dres=None, dx=None, dweig
     fp8_layer_norm(stats=True) returned; ``dres`` (x's type) is the gradient
     that reaches x past the norm and is added to dx before its rounding; dx
     has x's type, dweight and dbias are FP32 [H]."""
+    r = (_native or _load_native()).layer_norm_backward(dy, x, weight, mean, rstd, dres, dx,
+                                                        dweight, dbias, workspace)
+    if r is not None:
+        return r if type(r) is not int else _lib.fail("fp8_layer_norm_backward", r)
     dev = _on_gpu(x, "x")
     xt = x.dtype
     n = x.numel()

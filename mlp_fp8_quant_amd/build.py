@@ -1,4 +1,6 @@
-"""Builds libfp8mot.so (the HIP kernels and the C ABI) in-tree for gfx950.
+"""Builds libfp8mot.so (the HIP kernels and the C ABI) in-tree for gfx950, and
+_binding.so, the native front of the binding's small calls (host code: g++
+against Python, torch and libfp8mot).
 
 Compiler flags:
   --offload-arch=gfx950          the only target (no other architecture);
@@ -24,6 +26,8 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["elementwise.hip", "gemm.hip", "linear_act_tile.hip", "linear_act.hip", "layer_norm.hip",
            "mfma_ceiling.hip", "verify.hip", "capi.hip"]
 
+BINDING_PATH = os.path.join(PKG, "_binding.so")
+
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
@@ -42,7 +46,8 @@ def _run(cmd):
 
 
 def build(verbose=False, jobs=4) -> str:
-    """Compile every source and link libfp8mot.so; returns the library path."""
+    """Compile every source, link libfp8mot.so and build the native front of
+    the binding; returns the library path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
 
     def compile_one(src):
@@ -58,7 +63,31 @@ def build(verbose=False, jobs=4) -> str:
     tmp = LIB_PATH + ".tmp"
     _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp])
     os.replace(tmp, LIB_PATH)
+    build_binding(verbose)
     return LIB_PATH
+
+
+def build_binding(verbose=False) -> str:
+    """Compile the native front against the installed torch and the in-tree
+    libfp8mot.so (found at run time beside it); returns its path."""
+    import sysconfig
+
+    from torch.utils import cpp_extension as ext
+
+    tmp = BINDING_PATH + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__",
+           "-isystem", "/opt/rocm/include", "-isystem", sysconfig.get_paths()["include"]]
+    for d in ext.include_paths():
+        cmd += ["-isystem", d]
+    cmd += [os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", PKG, "-lfp8mot"]
+    for d in ext.library_paths():
+        cmd += ["-L", d]
+    cmd += ["-lc10", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    _run(cmd)
+    os.replace(tmp, BINDING_PATH)
+    return BINDING_PATH
 
 
 def device_assembly(src) -> str:

@@ -205,3 +205,38 @@ def test_custom_ops():
         return ops.linear_act(h, t["w2"], t["sh"], t["s2"], t["b2"], 0, x)
 
     assert torch.equal(torch.compile(chain, fullgraph=True, backend="aot_eager")(t["x"]), f["y"])
+
+
+def test_native_front_and_python_checks_give_the_same(monkeypatch):
+    # the native front of the binding against the path behind it
+    from mlp_fp8_quant_amd import api
+
+    class Nothing:
+        linear_act = linear_act_backward = layer_norm = layer_norm_backward = staticmethod(lambda *a: None)
+
+    ts = [block(3, 256, 512, 8), block(150, 256, 512, 9)]
+    assert api._load_native() is api._native
+    native = [results(t) for t in ts]
+    monkeypatch.setattr(api, "_native", Nothing)
+    assert all(equal(results(t), want) for t, want in zip(ts, native))
+
+
+def test_errors_and_parameters_through_the_native_front():
+    t = block(4, 256, 512, 10)
+    x = t["x"]
+    want = fp8.fp8_layer_norm(x, t["g"], t["b"])
+    assert torch.equal(fp8.fp8_layer_norm(x, torch.nn.Parameter(t["g"]), torch.nn.Parameter(t["b"])), want)
+    assert torch.equal(fp8.fp8_layer_norm(x.view(2, 2, 256), t["g"], t["b"]).view(4, 256), want)
+    with pytest.raises(fp8.Fp8motError, match="ERR_INVALID_ARG"):
+        fp8.fp8_layer_norm(x, eps=-1.0)
+    with pytest.raises(fp8.Fp8motError, match="ERR_UNSUPPORTED"):
+        fp8.fp8_layer_norm(x, out_kind=fp8.OUT_FP8)
+    with pytest.raises(fp8.Fp8motError, match="ERR_INVALID_ARG"):
+        fp8.fp8_linear_act_backward(x, x, act=9)
+    with pytest.raises(ValueError, match="contiguous"):
+        fp8.fp8_layer_norm(x.t())
+    with pytest.raises(ValueError, match="bias"):
+        fp8.fp8_linear_act(t["w1"], t["w1"], t["s1"], t["s1"], bias=t["b2"])
+    odd = torch.empty(4 * 256 + 8, dtype=BF16, device=x.device)[1:1 + 4 * 256].view(4, 256)
+    with pytest.raises(fp8.Fp8motError, match="ERR_MISALIGNED"):
+        fp8.fp8_layer_norm(odd)
