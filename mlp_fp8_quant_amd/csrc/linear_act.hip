@@ -43,8 +43,13 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_rows_kernel(LinearActArgs g
   static_assert(NW * D * STAGE <= 160 * 1024 && NW * MB * NB * 1024 <= NW * D * STAGE, "LDS");
   static_assert(D >= 2 && D <= 4 && D * COPIES < 64, "wait_copies");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[NW * D * STAGE];
-  constexpr int ITEMS = (MB * NB + NW - 1) / NW;   // 16x16 blocks joined by a wave
-  constexpr bool EARLY = ITEMS == 1;               // the epilogue's operands are read during the product
+  // Epilogue: a wave takes G 16-row blocks of the same 16 columns at once
+  // (their operands in flight together), ROUNDS times; one copy of the code,
+  // since every launch fetches it cold.
+  constexpr int PER = MB * NB / NW;
+  constexpr int G = PER < 1 ? 1 : (PER < MB ? PER : MB), CHUNKS = MB * NB / G, ROUNDS = (CHUNKS + NW - 1) / NW;
+  static_assert(MB % G == 0, "chunks of rows");
+  constexpr bool EARLY = ROUNDS == 1;   // operands are read during the product, or else round by round
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int l15 = lane & 15, kq = lane >> 4;
@@ -54,22 +59,22 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_rows_kernel(LinearActArgs g
 
   const bool vec = (g.N & 3) == 0;
   const linear::Epilogue epi = linear::open_epilogue(g, m0);
-  linear::u4v res[ITEMS];
-  linear::Columns col[ITEMS];
-  // block b = wave + i * NW of the tile: row 16 (b / NB) + l15 from m0, columns from n
-  auto operands = [&](int i) {
-    const int b = wave + i * NW;
-    if (b >= MB * NB) return;
-    const int row = 16 * (b / NB) + l15, n = (int)n0 + 16 * (b % NB) + 4 * kq, nv = (int)g.N - n;
+  linear::Operands<G> op;
+  linear::Columns col;
+  // chunk q: rows row_of(q), + 16, .. from m0, columns col_of(q) .. + 3
+  auto row_of = [&](int q) { return 16 * G * (q / NB) + l15; };
+  auto col_of = [&](int q) { return (int)n0 + 16 * (q % NB) + 4 * kq; };
+  auto operands = [&](int q) {
+    const int row = row_of(q), n = col_of(q), nv = (int)g.N - n;
     if (vec) {
-      if (g.residual != nullptr) linear::load_residual<1, true>(g, epi, row, 1, n, nv, &res[i]);
-      col[i] = linear::load_columns<true>(g, n, nv);
+      linear::load_operands<G, true>(g, epi, m0, row, 16, n, nv, &op);
+      col = linear::load_columns<true>(g, n, nv);
     } else {
-      if (g.residual != nullptr) linear::load_residual<1, false>(g, epi, row, 1, n, nv, &res[i]);
-      col[i] = linear::load_columns<false>(g, n, nv);
+      linear::load_operands<G, false>(g, epi, m0, row, 16, n, nv, &op);
+      col = linear::load_columns<false>(g, n, nv);
     }
   };
-  if constexpr (EARLY) operands(0);
+  if (wave < CHUNKS && EARLY) operands(wave);
 
   // copy q of a stage fills LDS rows 8q .. 8q + 7 (W's 16 NB rows, then X's):
   // lane l brings row 8q + l/8, physical chunk l % 8
@@ -162,23 +167,31 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_rows_kernel(LinearActArgs g
   for (int b = 0; b < MB; ++b)
 #pragma unroll
     for (int c = 0; c < NB; ++c) red[(wave * (MB * NB) + b * NB + c) * 64 + lane] = acc[b][c];
+  if (wave < CHUNKS && !EARLY) operands(wave);
   __syncthreads();
+#pragma unroll 1
+  for (int q = wave; q < CHUNKS; q += NW) {
+    float z[G][4];
 #pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-    const int b = wave + i * NW;
-    if (b >= MB * NB) break;
-    if constexpr (!EARLY) operands(i);
-    v4f s = red[b * 64 + lane];
+    for (int k = 0; k < G; ++k) {
+      const int b = ((q / NB) * G + k) * NB + q % NB;
+      v4f s = red[b * 64 + lane];
 #pragma unroll
-    for (int w = 1; w < NW; ++w) {
-      const v4f o = red[(w * (MB * NB) + b) * 64 + lane];
+      for (int w = 1; w < NW; ++w) {
+        const v4f o = red[(w * (MB * NB) + b) * 64 + lane];
 #pragma unroll
-      for (int v = 0; v < 4; ++v) s[v] = __fadd_rn(s[v], o[v]);
+        for (int v = 0; v < 4; ++v) s[v] = __fadd_rn(s[v], o[v]);
+      }
+#pragma unroll
+      for (int v = 0; v < 4; ++v) z[k][v] = s[v];
     }
-    float z[1][4] = {{s[0], s[1], s[2], s[3]}};
-    const int row = 16 * (b / NB) + l15, n = (int)n0 + 16 * (b % NB) + 4 * kq, nv = (int)g.N - n;
-    if (vec) linear::finish<1, true>(g, epi, col[i], m0, row, 1, n, nv, &res[i], z, [] {});
-    else linear::finish<1, false>(g, epi, col[i], m0, row, 1, n, nv, &res[i], z, [] {});
+    const int row = row_of(q), n = col_of(q), nv = (int)g.N - n;
+    const linear::Columns c = col;
+    auto next = [&] {
+      if (q + NW < CHUNKS) operands(q + NW);
+    };
+    if (vec) linear::finish<G, true>(g, epi, c, row, 16, n, nv, op, z, next);
+    else linear::finish<G, false>(g, epi, c, row, 16, n, nv, op, z, next);
   }
 }
 
@@ -205,8 +218,8 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearActArgs g, const
   const linear::Epilogue e = linear::open_epilogue(g, m0);
   for (int i = (int)blockIdx.x * 256 + (int)threadIdx.x; i < rows * per_row; i += (int)gridDim.x * 256) {
     const int row = i / per_row, n = (i - row * per_row) * 4, nv = N - n;
-    linear::u4v r[1];
-    if (g.residual != nullptr) linear::load_residual<1, VEC>(g, e, row, 1, n, nv, r);
+    linear::Operands<1> op;
+    linear::load_operands<1, VEC>(g, e, m0, row, 1, n, nv, &op);
     const linear::Columns col = linear::load_columns<VEC>(g, n, nv);
     float z[1][4] = {{0.0f, 0.0f, 0.0f, 0.0f}}, o[4];
     for (int p = 0; p < splits; ++p) {
@@ -214,7 +227,7 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearActArgs g, const
 #pragma unroll
       for (int c = 0; c < 4; ++c) z[0][c] = p == 0 ? o[c] : __fadd_rn(z[0][c], o[c]);
     }
-    linear::finish<1, VEC>(g, e, col, m0, row, 1, n, nv, r, z, [] {});
+    linear::finish<1, VEC>(g, e, col, row, 1, n, nv, op, z, [] {});
   }
 }
 
@@ -297,18 +310,19 @@ hipError_t run_act_backward(const uint16_t* dy, const uint16_t* pre, int act, ui
 // than one workgroup, since a CU's share of the rows has to pass through its
 // own L1 at 40-50 bytes a clock whatever the tile: 1x4096x4096 5.2 with 16x16
 // blocks and 16 waves (16x32: 5.6), 64x4096x4096 7.3 with 32x32 (64x32 10.3,
-// 32x16 8.2), 256x4096x4096 16.6 with 64x64 (64x32 19.3; 128x128 tiles split
+// 32x16 8.2), 256x4096x4096 15.4 with 64x64 (64x32 19.3; 128x128 tiles split
 // four ways over K 23.1).  Above that, up to two workgroups per CU (64x64,
-// two waves): 512x4096x4096 27.3 (128x128 tiles split in two 29.8).
+// two waves): 512x4096x2048 16.1 (128x128 tiles 23.0), 512x4096x12288 55.7
+// (128x128 split in two 54.7), 777x2053x2064 20.4 (27.1).
 //
 // More outputs: the cheapest of the tiles and splits by an estimate of rounds
 // of workgroups times (rate * K + what a tile costs besides), plus the second
 // launch that joins splits of K.  The rates are fitted to sweeps: 256x256
 // tiles 4096x4096x12288 303 (256x128 333, 128x128 337), 128x128 with two K
-// groups 2048x2048x8192 66 (256x128 split in two 72) and 1024x4096x4096 38.6
-// (256x128 52), 256x128 split in three 3000x700x8000 50 (128x128, two K
-// groups, unsplit: 59), 128x128 two to a CU 3000x3000x1024 39.4 (256x256 41,
-// 256x128 45).
+// groups 2048x2048x8192 67 (256x128 split in two 70) and 1024x4096x4096 40.1
+// (256x128 50.7), 256x128 split in three 3000x700x8000 49 (128x128, two K
+// groups, unsplit: 60), 128x128 two to a CU 3000x3000x512 30 (256x256 34,
+// 256x128 33) and 5000x5000x4096 202 (256x256 216).
 LinearPlan linear_plan(int64_t M, int64_t N, int64_t K) {
   constexpr int64_t kCus = 256;
   auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
@@ -320,25 +334,28 @@ LinearPlan linear_plan(int64_t M, int64_t N, int64_t K) {
   if (area <= 8) return {kRows4x2, 1};
   if (area <= 16) return {kRows4x4, 1};
   if (M <= 64) return {kRows4x4Pair, 1};
-  LinearPlan best{kTile256x256, 1};
+  if (area <= 32) return {kRows4x4Pair, 1};
   auto tiles = [&](int bm, int bn) { return up(M, bm) * up(N, bn); };
-  double least = (double)up(tiles(256, 256), kCus) * (0.0235 * (double)K + 13.0);
+  const double k0 = (double)K;
+  LinearPlan best{kTile256x256, 1};
+  double least = (double)up(tiles(256, 256), kCus) * (0.0225 * k0 + 25.0);
   auto offer = [&](LinearPlan p, double us) {
     if (us < least) {
       least = us;
       best = p;
     }
   };
-  if (area <= 32) offer({kRows4x4Pair, 1}, 0.0038 * (double)K + 11.7);
-  const double pairs = (double)tiles(128, 128) / (2 * kCus);
-  if (pairs > 0.5) offer({kTile128x128, 1}, (pairs + 0.3) * (0.0150 * (double)K + 10.0));
+  const double pairs = (double)tiles(128, 128) / (2 * kCus);   // rounds of two workgroups per CU
+  if (pairs <= 0.5) offer({kTile128x128, 1}, 0.0075 * k0 + 12.0);
+  else offer({kTile128x128, 1}, (pairs <= 1.0 ? 1.0 : 0.5 * (pairs + (double)up(tiles(128, 128), 2 * kCus))) *
+                                    (0.0122 * k0 + 12.0));
   const int64_t stages = up(K, 128);
   for (int s = 1; s <= 4 && (s == 1 || stages >= 8 * s); ++s) {
     const double k = (double)(up(stages, s) * 128);
     const double join = s == 1 ? 0.0 : 4.0 + (double)s * (double)M * (double)N * 8.0 / 12e6;
-    offer({kTile256x128, s}, (double)up(tiles(256, 128) * s, kCus) * (0.0132 * k + 9.0) + join);
-    offer({kTile128x128K2, s}, (double)up(tiles(128, 128) * s, kCus) * (0.0072 * k + 8.0) + join);
+    offer({kTile256x128, s}, (double)up(tiles(256, 128) * s, kCus) * (0.0118 * k + 13.0) + join);
   }
+  offer({kTile128x128K2, 1}, (double)up(tiles(128, 128), kCus) * (0.0066 * k0 + 13.0));
   return best;
 }
 

@@ -373,18 +373,17 @@ __global__ __launch_bounds__(WM* WN * 64 * KSPL, 1) void linear_tile_kernel(Tile
     const bool raw = part != nullptr;
     const linear::Epilogue e = raw ? linear::Epilogue{} : linear::open_epilogue(g, m0);
     const linear::Rows pr = raw ? linear::rows_of(part + (int64_t)blockIdx.y * M * N, m0, M, N, 4) : linear::Rows{};
-    const bool with_res = !raw && g.residual != nullptr;
     linear::Columns cols[FN];
-    linear::u4v res[4];
-    auto residual_of = [&](int b) {
+    linear::Operands<4> op;
+    auto operands_of = [&](int b) {
       const int n = nw + 32 * (b % FN);
-      linear::load_residual<4, VEC>(g, e, row_w + 32 * (b / FN), 8, n, N - n, res);
+      linear::load_operands<4, VEC>(g, e, m0, row_w + 32 * (b / FN), 8, n, N - n, &op);
     };
     if (!raw) {
 #pragma unroll
       for (int j = 0; j < FN; ++j) cols[j] = linear::load_columns<VEC>(g, nw + 32 * j, N - nw - 32 * j);
     }
-    if (with_res) residual_of(0);
+    if (!raw) operands_of(0);
 #pragma unroll 1
     for (int b = 0; b < FM * FN; ++b) {
 #pragma unroll
@@ -414,8 +413,8 @@ __global__ __launch_bounds__(WM* WN * 64 * KSPL, 1) void linear_tile_kernel(Tile
 #pragma unroll
         for (int j = 1; j < FN; ++j)
           if (b % FN == j) col = cols[j];
-        linear::finish<4, VEC>(g, e, col, m0, row, 8, n, N - n, res, z, [&] {
-          if (with_res && b + 1 < FM * FN) residual_of(b + 1);
+        linear::finish<4, VEC>(g, e, col, row, 8, n, N - n, op, z, [&] {
+          if (b + 1 < FM * FN) operands_of(b + 1);
         });
       }
     }

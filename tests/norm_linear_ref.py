@@ -211,7 +211,8 @@ def check_fp8(codes, want, err, sy, what=""):
     assert torch.equal(torch.isnan(got), torch.isnan(want)), f"{what}: NaN elsewhere"
     fine = ~torch.isnan(want)
     t = (want / s)
-    e = (torch.where(torch.isfinite(err), err, torch.zeros_like(err)) / s) + t.abs().clamp(max=1e30) * U
+    # 1 / sy and the product with it round once each, and their product's error term a third
+    e = (torch.where(torch.isfinite(err), err, torch.zeros_like(err)) / s) + t.abs().clamp(max=1e30) * 3 * U
     t = t.clamp(-E4M3_MAX, E4M3_MAX)
     off = (got - t).abs()[fine]
     tol = (e + torch.maximum((t.abs() + e) * E4M3_HALF, torch.full_like(t, E4M3_SUB_HALF)))[fine]

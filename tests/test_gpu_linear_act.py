@@ -81,6 +81,67 @@ def test_row_scales(M, N, K):
         run_and_check(t, ref.SILU, out, rowwise=True, pre=True, sy=torch.tensor([0.05], device=device()))
 
 
+def reference_on_gpu(t, act):
+    """linear_act's reference with its products on the GPU, for shapes whose
+    64-bit product takes long on the CPU."""
+    d = t["qx"].device
+    val = lambda q: q.view(torch.float8_e4m3fn).double()  # noqa: E731
+    a, b = val(t["qx"]), val(t["qw"]).t().contiguous()
+    alpha = (t["sx"].reshape(-1, 1) * t["sw"].reshape(1, -1)).double()
+    z = (a @ b) * alpha
+    err_z = 1e-5 * alpha * (a.abs() @ b.abs()) + z.abs() * ref.U
+    if t["bias"] is not None:
+        z = z + t["bias"].double()
+    err_z = err_z + z.abs() * ref.U
+    y = ref.act(z, act)
+    err = 1.13 * err_z + ref.act_error(z, act)
+    if t["residual"] is not None:
+        y = y + t["residual"].double()
+        err = err + y.abs() * ref.U
+    assert y.device == d
+    return y.cpu(), z.cpu(), err.cpu(), err_z.cpu()
+
+
+# shapes that between them reach every few-row tile and every output tile, with
+# and without splits of K, K a multiple of the 128-K stage and not, N a
+# multiple of 4 and not
+@pytest.mark.parametrize("M,N,K", [
+    (10, 6000, 272), (5, 9001, 256), (40, 2000, 272), (30, 9000, 144), (60, 5000, 272), (60, 12002, 128),
+    (64, 20000, 144), (400, 3000, 1040), (777, 2053, 272), (2500, 2501, 272), (2500, 2500, 256), (3000, 700, 4000),
+    (3000, 701, 4096), (1500, 1500, 1504), (700, 5001, 2048), (1319, 3016, 2560), (1319, 3015, 2576), (7278, 290, 9984),
+    (578, 7537, 14240), (3989, 3990, 672), (2048, 8192, 1024)], ids=lambda v: str(v))
+def test_every_tile(M, N, K):
+    i = M + N + K
+    act = ref.ACTS[i % 5]
+    t = make(M, N, K, i, (BF16, F32)[i % 2], (F32, BF16, None)[i % 3], rowwise=i % 7 == 0)
+    y64, z64, err, err_z = reference_on_gpu(t, act)
+    sy = torch.tensor([0.03], device=device())
+    for out in (fp8.OUT_BF16, fp8.OUT_F32, fp8.OUT_FP8):
+        y, pre = fp8.fp8_linear_act(t["qx"], t["qw"], t["sx"], t["sw"], t["bias"], act, t["residual"], out, sy,
+                                    rowwise=i % 7 == 0, pre=True)
+        if out == fp8.OUT_FP8:
+            ref.check_fp8(y, y64, err, sy, "y")
+        else:
+            ref.check(y, y64, err, "y")
+        ref.check(pre, z64, err_z, "pre")
+
+
+@pytest.mark.parametrize("M,N,K", [(300, 5000, 272), (2500, 2500, 272), (3000, 700, 4096), (700, 5000, 2048),
+                                   (1319, 3016, 2560), (3989, 3990, 672), (2048, 8192, 1024)])
+def test_native_engine_tiles(M, N, K):
+    # the native engine on the tiles of many outputs: |error| at most 7 products
+    # of each 8 held 13 bits below the largest, so 7 * 2^-13 of sum|terms| / 8
+    # times at most 8 (the largest is at most the group's sum)
+    t = make(M, N, K, 21, BF16, BF16)
+    y64, _, err, _ = reference_on_gpu(t, ref.NONE)
+    val = lambda q: q.view(torch.float8_e4m3fn).double().abs()  # noqa: E731
+    terms = (val(t["qx"]) @ val(t["qw"]).t().contiguous()).cpu()
+    err = err + (t["sx"] * t["sw"]).cpu().double() * 7 * 2.0 ** -13 * terms
+    y = fp8.fp8_linear_act(t["qx"], t["qw"], t["sx"], t["sw"], t["bias"], ref.NONE, t["residual"], fp8.OUT_F32,
+                           accum=fp8.ACC_FP8_MFMA)
+    ref.check(y, y64, err)
+
+
 def test_row_scales_of_one_value_equal_the_tensor_scale():
     for M in (20, 300):
         t = make(M, 200, 256, 3, BF16, BF16)
@@ -104,27 +165,30 @@ def test_wide_codes_and_long_sums():
         ref.check(fp8.fp8_linear_act(qx, qw, s, s, out_kind=fp8.OUT_F32), y64, err)
 
 
-@pytest.mark.parametrize("M", [4, 40, 130, 300])
-def test_equal_calls_give_equal_bits(M):
-    t = make(M, 520, 1040, 11, BF16, BF16)
+@pytest.mark.parametrize("M,N,K", [(4, 520, 1040), (40, 520, 1040), (300, 520, 1040), (400, 3000, 1040),
+                                   (3000, 700, 4096), (2500, 2500, 256)])
+def test_equal_calls_give_equal_bits(M, N, K):
+    t = make(M, N, K, 11, BF16, BF16)
     y = [fp8.fp8_linear_act(t["qx"], t["qw"], t["sx"], t["sw"], t["bias"], ref.SILU, t["residual"]) for _ in range(3)]
     assert torch.equal(y[0], y[1]) and torch.equal(y[0], y[2])
 
 
 @pytest.mark.parametrize("dtype,out", [(BF16, fp8.OUT_BF16), (F32, fp8.OUT_F32)])
-@pytest.mark.parametrize("M,N", [(1, 100), (20, 77), (150, 136), (300, 259)])
-def test_residual_in_place(M, N, dtype, out):
-    t = make(M, N, 272, 1, F32, dtype)
+@pytest.mark.parametrize("M,N,K", [(1, 100, 272), (20, 77, 272), (150, 136, 272), (700, 2001, 272), (2500, 2500, 272),
+                                   (3000, 700, 4096)])
+def test_residual_in_place(M, N, K, dtype, out):
+    t = make(M, N, K, 1, F32, dtype)
     want = fp8.fp8_linear_act(t["qx"], t["qw"], t["sx"], t["sw"], t["bias"], ref.NONE, t["residual"], out)
     got = t["residual"].clone()
     fp8.fp8_linear_act(t["qx"], t["qw"], t["sx"], t["sw"], t["bias"], ref.NONE, got, out, out=got)
     assert torch.equal(got, want)
 
 
-@pytest.mark.parametrize("M", [1, 30, 100, 270])
-def test_nothing_behind_the_outputs_is_written(M):
+@pytest.mark.parametrize("M,widths", [(1, (61, 64, 130)), (30, (61, 64, 130)), (270, (61, 64, 130)), (700, (2001, 2004)),
+                                      (3001, (2501, 2500))])
+def test_nothing_behind_the_outputs_is_written(M, widths):
     d = device()
-    for N in (61, 64, 130):
+    for N in widths:
         t = make(M, N, 64, 9, BF16, None)
         for out, dtype in ((fp8.OUT_BF16, torch.int16), (fp8.OUT_F32, torch.int32), (fp8.OUT_FP8, torch.uint8)):
             buf = torch.full((M * N + 4096,), 85, dtype=dtype, device=d)

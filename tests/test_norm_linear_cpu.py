@@ -46,12 +46,15 @@ def test_linear_workspace_refusals():
     lib = L.lib()
     assert lib.fp8_linear_act_workspace(-1, 4, 16) == 0
     assert lib.fp8_linear_act_workspace(0, 4, 16) == 0
-    for M, N, K in ((1, 64, 65536), (1, 16, 8192), (100, 512, 25600), (4, 8, 16), (16384, 25600, 5120)):
+    for M, N, K in ((4, 8, 16), (16384, 25600, 5120), (1, 4096, 4096), (512, 4096, 12288)):
+        assert lib.fp8_linear_act_workspace(M, N, K) == 0
+    # K split over two, three and four workgroups
+    for M, N, K, splits in ((7278, 290, 9984, 2), (3000, 700, 4000, 3), (578, 7537, 14240, 4)):
         need = lib.fp8_linear_act_workspace(M, N, K)
-        if need:
-            assert linear(M=M, N=N, K=K) == WORKSPACE
-            assert linear(M=M, N=N, K=K, ws=FAKE, wb=need - 1) == WORKSPACE
-            assert linear(M=M, N=N, K=K, ws=ODD, wb=need) == WORKSPACE
+        assert need == splits * M * N * 4
+        assert linear(M=M, N=N, K=K) == WORKSPACE
+        assert linear(M=M, N=N, K=K, ws=FAKE, wb=need - 1) == WORKSPACE
+        assert linear(M=M, N=N, K=K, ws=ODD, wb=need) == WORKSPACE
 
 
 def linear_backward(dy=FAKE, pre=FAKE, act=1, dz=FAKE, db=FAKE, M=4, N=8, ws=FAKE, wb=1 << 30):
