@@ -318,16 +318,16 @@ int fp8_linear_rowwise(const uint8_t* qx, const uint8_t* qw, void* y, int64_t M,
 
 /* Bytes of workspace fp8_linear_act needs: 0 for most shapes, FP32 partial
  * sums where K is split over workgroups (few outputs, long K).  Depends on
- * (M, N, K) only.  Returns 0 for negative sizes. */
+ * (M, N, K) only.  Returns 0 for sizes that fp8_linear_act refuses. */
 size_t fp8_linear_act_workspace(int64_t M, int64_t N, int64_t K);
 
 /* FP8 Linear with bias, activation and residual in its epilogue:
  *   acc[m,n] = sum_k e4m3_value(qx[m,k]) * e4m3_value(qw[n,k])
- *   z        = fp32(acc * alpha) + bias[n],  alpha = fp32(s_x * s_w)
+ *   z        = fma(acc, alpha, bias[n]),     alpha = fp32(s_x * s_w)
  *   v        = act(z) + residual[m,n]
- *   y[m,n]   = bf16_rne(v) | e4m3(v / *d_sy) | v    per out_kind
- * each step one FP32 operation; NULL bias or residual leaves its addition
- * out.  The bias of a projection, the activation of an ungated MLP and the
+ *   y[m,n]   = bf16_rne(v) | e4m3(v * r) | v    per out_kind
+ * each step one FP32 operation, r = fp32(1 / *d_sy), which has to be finite;
+ * NULL bias or residual leaves its addition out.  The bias of a projection, the activation of an ungated MLP and the
  * residual stream's addition after o and down are what a decoder layer does
  * to a projection's output; here no pass over [M, N] is spent on them.
  *  - row_scales 0: d_sx, d_sw one scale each, as fp8_linear; row_scales 1:
@@ -339,8 +339,9 @@ size_t fp8_linear_act_workspace(int64_t M, int64_t N, int64_t K);
  *  - y may be the residual itself where the element types agree (the sum is
  *    then added in place); no other overlap of y or pre with an input or
  *    with each other.
- *  - accum as fp8_linear.  Calls of few rows (M <= 64) are bound by the
- *    weight's bytes and always sum as FP8MOT_ACC_EXACT does.
+ *  - accum as fp8_linear.  Calls of few rows (M <= 64) or few outputs (about
+ *    two million and less) are bound by bytes, not by the matrix cores, and
+ *    always sum as FP8MOT_ACC_EXACT does.
  *  - ws: 16-byte aligned device workspace of at least
  *    fp8_linear_act_workspace(M, N, K) bytes (may be NULL where that is 0).
  *    Calls that may overlap need workspaces of their own.
@@ -354,7 +355,8 @@ int fp8_linear_act(const uint8_t* qx, const uint8_t* qw, void* y, int64_t M, int
                    int accum, void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* Bytes of workspace fp8_linear_act_backward needs for dbias (column sums
- * over slabs of rows).  Returns 0 for negative sizes. */
+ * over slabs of rows; 0 where one slab is all).  Returns 0 for sizes that
+ * fp8_linear_act_backward refuses. */
 size_t fp8_linear_act_backward_workspace(int64_t M, int64_t N);
 
 /* Backward pass of fp8_linear_act's epilogue: for the gradient dy of y,
@@ -382,19 +384,22 @@ int fp8_linear_act_backward(const uint16_t* dy, const uint16_t* pre, int act, ui
  * as silu_mul_2in_fp8 emits the down projection's input):
  *   mean = sum_i x[i] / H,   var = sum_i (x[i] - mean)^2 / H
  *   rstd = 1 / sqrt(var + eps)
- *   v    = (x[i] - mean) * rstd * weight[i] + bias[i]       (FP32)
- *   y[i] = bf16_rne(v) | e4m3(v / *d_sy) | v    per out_kind
+ *   v    = fma((x[i] - mean) * rstd, weight[i], bias[i])       (FP32)
+ *   y[i] = bf16_rne(v) | e4m3(v * r) | v    per out_kind, r = fp32(1 / *d_sy)
  * x: [rows, H] of x_elem (fp8mot_elem); weight, bias: [H] of wb_elem, either
  * may be NULL (ones, zeros); y: [rows, H]; mean, rstd: FP32 [rows] for the
  * backward pass, or NULL.  eps finite and >= 0.  y may be x itself where the
  * element types agree; no other overlap.  H up to 2^26, rows up to INT32_MAX;
- * x, y, weight, bias 16-byte aligned.  A row that holds a NaN or an infinity becomes NaN. */
+ * x, y, weight, bias 16-byte aligned.  1 / *d_sy has to be finite.  A row that
+ * holds a NaN or an infinity, or whose sums leave FP32's range, becomes NaN
+ * (or what 1 / sqrt(Inf) = 0 makes of it, where the squares alone overflow). */
 int fp8_layer_norm(const void* x, int x_elem, const void* weight, const void* bias,
                    int wb_elem, void* y, int out_kind, const float* d_sy, float* mean,
                    float* rstd, int64_t rows, int64_t H, float eps, hipStream_t stream);
 
 /* Bytes of workspace fp8_layer_norm_backward needs for dweight and dbias
- * (column sums over slabs of rows).  Returns 0 for negative sizes. */
+ * (column sums over slabs of rows; 0 where one slab is all).  Returns 0 for
+ * sizes that fp8_layer_norm_backward refuses. */
 size_t fp8_layer_norm_backward_workspace(int64_t rows, int64_t H);
 
 /* Backward pass of fp8_layer_norm, for the gradient dy of y (an FP8 y passes
@@ -407,9 +412,9 @@ size_t fp8_layer_norm_backward_workspace(int64_t rows, int64_t H);
  * rounded.  dy: of dy_elem; x, dres, dx: of x_elem; weight: [H] of w_elem or
  * NULL (ones); dweight, dbias: FP32 [H], either may be NULL (not computed).
  * dx may be dy or dres itself where the element types agree, or x; no other
- * overlap.  rows == 0 writes dweight = dbias = 0.  Sizes as fp8_layer_norm.  The sums over rows take an
- * order that depends on (rows, H) only.  All tensors 16-byte aligned but
- * mean and rstd.  ws: 16-byte aligned, at least
+ * overlap.  rows == 0 writes dweight = dbias = 0.  Sizes as fp8_layer_norm.
+ * The sums over rows take an order that depends on (rows, H) only.  All
+ * tensors 16-byte aligned but mean and rstd.  ws: 16-byte aligned, at least
  * fp8_layer_norm_backward_workspace(rows, H) bytes; unused where dweight and
  * dbias are NULL. */
 int fp8_layer_norm_backward(const void* dy, int dy_elem, const void* x, int x_elem,

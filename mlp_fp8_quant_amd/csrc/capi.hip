@@ -253,7 +253,8 @@ int fp8_requantize_onto_max(const uint8_t* qw, uint8_t* out, int64_t n,
 }
 
 size_t fp8_linear_act_workspace(int64_t M, int64_t N, int64_t K) {
-  if (M < 0 || N < 0 || K < 0) return 0;
+  if (M < 0 || N < 0 || K < 0 || M > INT32_MAX || N > INT32_MAX || K > INT32_MAX) return 0;
+  if (!gemm_sizes_ok(M, N, K, N, 1)) return 0;
   return linear_act_workspace(M, N, K);
 }
 
@@ -290,8 +291,8 @@ int fp8_linear_act(const uint8_t* qx, const uint8_t* qw, void* y, int64_t M, int
 }
 
 size_t fp8_linear_act_backward_workspace(int64_t M, int64_t N) {
-  if (M < 0 || N < 0) return 0;
-  return (size_t)act_backward_slabs(M, N) * (size_t)N * sizeof(float);
+  if (!rows_ok(M, N)) return 0;
+  return (size_t)act_backward_partials(M, N) * (size_t)N * sizeof(float);
 }
 
 int fp8_linear_act_backward(const uint16_t* dy, const uint16_t* pre, int act, uint16_t* dz,
@@ -332,8 +333,8 @@ int fp8_layer_norm(const void* x, int x_elem, const void* weight, const void* bi
 }
 
 size_t fp8_layer_norm_backward_workspace(int64_t rows, int64_t H) {
-  if (rows < 0 || H < 0) return 0;
-  return (size_t)layer_norm_backward_slabs(rows, H) * 2 * (size_t)H * sizeof(float);
+  if (!rows_ok(rows, H)) return 0;
+  return (size_t)layer_norm_backward_partials(rows, H) * 2 * (size_t)H * sizeof(float);
 }
 
 int fp8_layer_norm_backward(const void* dy, int dy_elem, const void* x, int x_elem,

@@ -148,8 +148,8 @@ hipError_t launch_linear_act(const LinearActArgs& g, int accum, float* ws, int n
 hipError_t launch_linear_tile(const LinearActArgs& g, const LinearPlan& p, int accum, float* part,
                               int num_cus, hipStream_t stream);
 
-// dz = dy act'(pre), dbias[n] = sum_m dz; part: [act_backward_slabs(M, N), N] floats.
-int64_t act_backward_slabs(int64_t M, int64_t N);
+// dz = dy act'(pre), dbias[n] = sum_m dz; part: [act_backward_partials(M, N), N] floats.
+int64_t act_backward_partials(int64_t M, int64_t N);
 hipError_t launch_act_backward(const uint16_t* dy, const uint16_t* pre, int act, uint16_t* dz,
                                float* dbias, int64_t M, int64_t N, float* part, hipStream_t stream);
 
@@ -188,8 +188,8 @@ struct LayerNormBwdArgs {
   void* dx;               // [rows, H]
   int64_t rows, H;
 };
-// part: [layer_norm_backward_slabs(rows, H), 2 H] floats; dw, db: [H] or NULL.
-int64_t layer_norm_backward_slabs(int64_t rows, int64_t H);
+// part: [layer_norm_backward_partials(rows, H), 2 H] floats; dw, db: [H] or NULL.
+int64_t layer_norm_backward_partials(int64_t rows, int64_t H);
 hipError_t launch_layer_norm_backward(const LayerNormBwdArgs& g, float* dw, float* db, float* part,
                                       hipStream_t stream);
 

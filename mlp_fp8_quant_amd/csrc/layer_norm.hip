@@ -22,18 +22,19 @@ namespace {
 
 using namespace rows;
 
-// Sum over T threads that share a row (16 lanes, or whole waves), the same in
-// each.  red: T / 64 floats of LDS that no other sum in flight uses.
-template <int T>
+// Sum over the threads that share a row, the same in each: TC = 16 or 64
+// lanes, or (0) the whole workgroup.  red: 16 floats of LDS that no other sum
+// in flight uses.
+template <int TC>
 __device__ __forceinline__ float row_sum(float v, float* red) {
-  if constexpr (T == 16) return sum16(v);
+  if constexpr (TC == 16) return sum16(v);
   v = wave_sum(v);
-  if constexpr (T > 64) {
+  if constexpr (TC == 0) {
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
+    const int waves = blockDim.x >> 6;
     v = red[0];
-#pragma unroll
-    for (int w = 1; w < T / 64; ++w) v = __fadd_rn(v, red[w]);
+    for (int w = 1; w < waves; ++w) v = __fadd_rn(v, red[w]);
   }
   return v;
 }
@@ -67,26 +68,28 @@ __device__ __forceinline__ void affine8(const LayerNormArgs& g, int64_t i, float
   if (g.b != nullptr) load8_values(g.b, g.wb_f32, i, g.H, b);
 }
 
-// T threads per row, U groups of eight elements per thread (group j * T + t of
-// the row): a row of up to 8 T U elements in registers.  Workgroups of 256
-// threads hold 256 / T rows where T < 256.  A workgroup walks rows: the next
-// row is on its way while this one is summed, and (U <= 3) weight and bias
-// stay in registers.
-template <bool F32, int T, int U>
-__global__ __launch_bounds__(T < 256 ? 256 : T) void layer_norm_kernel(LayerNormArgs g) {
-  __shared__ float red[2][T < 64 ? 1 : T / 64];
-  constexpr int RPB = T < 256 ? 256 / T : 1;
-  constexpr bool KEEP = U <= 3;
-  const int t = T < 256 ? threadIdx.x % T : threadIdx.x;
+// T threads cover a row, U groups of eight elements each (group j * T + t of
+// the row), in registers.  TC: 16 or 64 of them, 256 / TC rows side by side in
+// a workgroup; or 0: the whole workgroup, any number of waves.  A workgroup
+// walks rows: the next row is on its way while this one is summed, and weight
+// and bias stay in registers.  FULL: the groups are exactly the row (512x4096
+// BF16 -> E4M3 4.1 us with its loads unguarded, 4.4 with the guards).
+// 16384x5120 BF16 -> E4M3: 58 us, 4.3 TB/s.
+template <bool F32, int TC, int U, bool FULL>
+__global__ __launch_bounds__(TC > 0 ? 256 : 1024) void layer_norm_kernel(LayerNormArgs g) {
+  __shared__ float red[2][16];
+  constexpr int RPB = TC > 0 ? 256 / (TC > 0 ? TC : 1) : 1;
+  constexpr bool KEEP = U <= 3;   // more would not fit beside the row
+  const int T = TC > 0 ? TC : blockDim.x, t = TC > 0 ? threadIdx.x % T : threadIdx.x;
   const float inv_h = 1.0f / (float)g.H;
   const int64_t step = (int64_t)gridDim.x * RPB;
-  int64_t r = (int64_t)blockIdx.x * RPB + (T < 256 ? threadIdx.x / T : 0);
-  if (r >= g.rows) return;   // with T > 64 whole workgroups
+  int64_t r = (int64_t)blockIdx.x * RPB + (TC > 0 ? threadIdx.x / T : 0);
+  if (r >= g.rows) return;   // with TC = 0 whole workgroups
   Raw8<F32> next[U];
   auto load = [&](int64_t row) {
     const void* xr = static_cast<const uint8_t*>(g.x) + row * g.H * (F32 ? 4 : 2);
 #pragma unroll
-    for (int j = 0; j < U; ++j) next[j] = load8<F32>(xr, 8 * (int64_t)(j * T + t), g.H);
+    for (int j = 0; j < U; ++j) next[j] = load8<F32, FULL>(xr, 8 * (int64_t)(j * T + t), g.H);
   };
   load(r);
   float w[KEEP ? U : 1][8], b[KEEP ? U : 1][8];
@@ -105,14 +108,14 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void layer_norm_kernel(LayerNorm
       s = __fadd_rn(s, sum8(x[j]));
     }
     if (r + step < g.rows) load(r + step);
-    const float mean = __fmul_rn(row_sum<T>(s, red[0]), inv_h);
+    const float mean = __fmul_rn(row_sum<TC>(s, red[0]), inv_h);
     float v = 0.0f;
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       const int64_t i = 8 * (int64_t)(j * T + t);
 #pragma unroll
       for (int k = 0; k < 8; ++k) x[j][k] = __fadd_rn(x[j][k], -mean);
-      if (i + 8 <= g.H) {
+      if (FULL || i + 8 <= g.H) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) v = __builtin_fmaf(x[j][k], x[j][k], v);
       } else {
@@ -121,7 +124,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void layer_norm_kernel(LayerNorm
           if (i + k < g.H) v = __builtin_fmaf(x[j][k], x[j][k], v);
       }
     }
-    const float var = __fmul_rn(row_sum<T>(v, red[1]), inv_h);
+    const float var = __fmul_rn(row_sum<TC>(v, red[1]), inv_h);
     const float rstd = 1.0f / __fsqrt_rn(__fadd_rn(var, g.eps));
     if (t == 0) {
       if (g.mean != nullptr) g.mean[r] = mean;
@@ -130,7 +133,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void layer_norm_kernel(LayerNorm
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       const int64_t i = 8 * (int64_t)(j * T + t);
-      if (i < g.H) {
+      if (FULL || i < g.H) {
         if constexpr (!KEEP) affine8(g, i, w[0], b[0]);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
@@ -155,7 +158,7 @@ __global__ __launch_bounds__(1024) void layer_norm_long_kernel(LayerNormArgs g) 
     values8<F32>(load8<F32>(xr, i, g.H), f);
     s = __fadd_rn(s, sum8(f));
   }
-  const float mean = __fmul_rn(row_sum<1024>(s, red[0]), inv_h);
+  const float mean = __fmul_rn(row_sum<0>(s, red[0]), inv_h);
   float v = 0.0f;
   for (int64_t i = 8 * (int64_t)threadIdx.x; i < g.H; i += 8 * 1024) {
     float f[8];
@@ -166,7 +169,7 @@ __global__ __launch_bounds__(1024) void layer_norm_long_kernel(LayerNormArgs g) 
       v = __builtin_fmaf(d, d, v);
     }
   }
-  const float var = __fmul_rn(row_sum<1024>(v, red[1]), inv_h);
+  const float var = __fmul_rn(row_sum<0>(v, red[1]), inv_h);
   const float rstd = 1.0f / __fsqrt_rn(__fadd_rn(var, g.eps));
   if (threadIdx.x == 0) {
     if (g.mean != nullptr) g.mean[r] = mean;
@@ -187,21 +190,29 @@ __global__ __launch_bounds__(1024) void layer_norm_long_kernel(LayerNormArgs g) 
 
 // Backward pass.  T threads cover a row, U groups of eight columns each (TC:
 // 16 or 64, and as many rows side by side as the workgroup holds; or 0: the
-// whole workgroup, any number of waves).  They walk the rows of the workgroup's slab:
-// the row's two sums through one barrier, dx, and the columns' sums of dy xh
-// and dy in registers, which go to part[slab, 0:H) and [H:2H) at the end.  The
-// next row's x, dy and dres are on their way during this row's sums.
-template <bool XF, bool DF, int TC, int U>
+// whole workgroup, any number of waves).  They walk the rows of the workgroup's
+// slab: the row's two sums through one barrier, dx, and the columns' sums of
+// dy xh and dy, which go to rows `slab` of out_w and out_b (2 H floats apart;
+// NULL: not needed) at the end.  The next row's x, dy and dres are on their way
+// during this row's sums; the guards of a row that ends inside a group must not
+// make a wave wait for each load in turn (8000x6000 BF16 123 us so, 91 with
+// load8_ahead).  FULL: the groups are exactly the row.  16384x5120 BF16 with
+// dres: 141 us, 4.7 TB/s.
+template <bool XF, bool DF, int TC, int U, bool FULL>
 __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(LayerNormBwdArgs g, int64_t slab_rows,
-                                                                   float* __restrict__ part) {
+                                                                    float* out_w, float* out_b) {
+  // two groups: a row stays in its raw form over its sums and is worked out
+  // again for dx, and FP32 rows are not loaded ahead: 128 registers hold no more
+  constexpr bool AGAIN = U > 1, AHEAD = U == 1 || (!XF && !DF);
   const int G = TC > 0 ? (int)blockDim.x / TC : 1;   // rows side by side
   __shared__ float red[2][2][16];
   __shared__ float cols[TC > 0 ? 1024 * 8 : 1];      // [G][8 TC]
+  __shared__ f4 sums[AGAIN ? 4 * U * 1024 : 1];      // [dw, db][U][half][threads]: each thread's own
   const int T = TC > 0 ? TC : blockDim.x, waves = T >> 6, t = TC > 0 ? threadIdx.x % TC : threadIdx.x;
   const float inv_h = 1.0f / (float)g.H;
   const int64_t r0 = (int64_t)blockIdx.x * slab_rows;
   const int64_t r1 = r0 + slab_rows < g.rows ? r0 + slab_rows : g.rows;
-  float w[U][8], sw[U][8], sb[U][8];
+  float w[U][8], sw[AGAIN ? 1 : U][8], sb[AGAIN ? 1 : U][8];
 #pragma unroll
   for (int j = 0; j < U; ++j) {
     const int64_t i = 8 * (int64_t)(j * T + t);
@@ -209,62 +220,100 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(LayerNormBwdA
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       if (g.w == nullptr) w[j][k] = 1.0f;
-      sw[j][k] = sb[j][k] = 0.0f;
+      if constexpr (!AGAIN) sw[j][k] = sb[j][k] = 0.0f;
     }
+    if constexpr (AGAIN)
+      for (int q = 0; q < 4; ++q) sums[(4 * j + q) * 1024 + t] = (f4){0.0f, 0.0f, 0.0f, 0.0f};
   }
   Raw8<XF> x[U], rs[U];
   Raw8<DF> d[U];
   float mean = 0.0f, rstd = 0.0f;
+  auto load8_of = [&](auto& to, const void* from, int64_t base, int64_t i) {
+    constexpr bool F = sizeof(to) == 32;
+    const void* row = static_cast<const uint8_t*>(from) + base * (F ? 4 : 2);
+    to = TC == 16 || FULL ? load8<F, FULL>(row, i, g.H) : load8_ahead<F>(row, i, g.H);
+  };
+  auto load_res = [&](int64_t r) {
+    if (g.dres == nullptr) return;
+#pragma unroll
+    for (int j = 0; j < U; ++j) load8_of(rs[j], g.dres, r * g.H, 8 * (int64_t)(j * T + t));
+  };
   auto load = [&](int64_t r) {
-    const int64_t base = r * g.H;
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      const int64_t i = 8 * (int64_t)(j * T + t);
-      x[j] = load8<XF>(static_cast<const uint8_t*>(g.x) + base * (XF ? 4 : 2), i, g.H);
-      d[j] = load8<DF>(static_cast<const uint8_t*>(g.dy) + base * (DF ? 4 : 2), i, g.H);
-      if (g.dres != nullptr) rs[j] = load8<XF>(static_cast<const uint8_t*>(g.dres) + base * (XF ? 4 : 2), i, g.H);
+      load8_of(x[j], g.x, r * g.H, 8 * (int64_t)(j * T + t));
+      load8_of(d[j], g.dy, r * g.H, 8 * (int64_t)(j * T + t));
     }
     mean = g.mean[r];
     rstd = g.rstd[r];
   };
+  // xh and g of a group, from its raw elements
+  auto group = [&](const Raw8<XF>& xr, const Raw8<DF>& dr, float mean_r, float rstd_r, int j, float* dy, float* xh,
+                   float* gw) {
+    values8<XF>(xr, xh);
+    values8<DF>(dr, dy);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      xh[k] = __fmul_rn(__fadd_rn(xh[k], -mean_r), rstd_r);
+      gw[k] = __fmul_rn(dy[k], w[j][k]);
+    }
+  };
   int64_t r = r0 + (TC > 0 ? threadIdx.x / TC : 0);
-  if (r < r1) load(r);
+  if (r < r1) {
+    load(r);
+    if constexpr (!AGAIN) load_res(r);
+  }
   for (int buf = 0; r < r1; r += G, buf ^= 1) {
     float xh[U][8], gw[U][8], res[U][8];
-    const float rstd_r = rstd;
+    Raw8<XF> x_now[U];
+    Raw8<DF> d_now[U];
+    const float mean_r = mean, rstd_r = rstd;
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       float dy[8];
-      values8<XF>(x[j], xh[j]);
-      values8<DF>(d[j], dy);
-      if (g.dres != nullptr) values8<XF>(rs[j], res[j]);
-      // columns past H: dy is 0 there, and whatever xh is falls away
+      const int64_t i = 8 * (int64_t)(j * T + t);
+      if constexpr (TC != 16 && !FULL) {
+        shift8<XF>(x[j], i, g.H);
+        shift8<DF>(d[j], i, g.H);
+        if (!AGAIN && g.dres != nullptr) shift8<XF>(rs[j], i, g.H);
+      }
+      x_now[j] = x[j];
+      d_now[j] = d[j];
+      if (!AGAIN && g.dres != nullptr) values8<XF>(rs[j], res[j]);
+      // columns past H: x and dy are 0 there, and add nothing to the row's sums
+      group(x[j], d[j], mean_r, rstd_r, j, dy, xh[j], gw[j]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s1 = __fadd_rn(s1, gw[j][k]);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        xh[j][k] = __fmul_rn(__fadd_rn(xh[j][k], -mean), rstd);
-        gw[j][k] = __fmul_rn(dy[k], w[j][k]);
-        s1 = __fadd_rn(s1, gw[j][k]);
-      }
-      if (8 * (int64_t)(j * T + t) + 8 <= g.H) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          s2 = __builtin_fmaf(gw[j][k], xh[j][k], s2);
+        s2 = __builtin_fmaf(gw[j][k], xh[j][k], s2);
+        if constexpr (!AGAIN) {
           sw[j][k] = __builtin_fmaf(dy[k], xh[j][k], sw[j][k]);
+          sb[j][k] = __fadd_rn(sb[j][k], dy[k]);
         }
-      } else {
-        const int64_t left = g.H - 8 * (int64_t)(j * T + t);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (k < left) {
-            s2 = __builtin_fmaf(gw[j][k], xh[j][k], s2);
-            sw[j][k] = __builtin_fmaf(dy[k], xh[j][k], sw[j][k]);
-          }
       }
+      if constexpr (AGAIN) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sb[j][k] = __fadd_rn(sb[j][k], dy[k]);
+        for (int q = 0; q < 4; ++q) {
+          f4 a = sums[(4 * j + q) * 1024 + t];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float dk = dy[4 * (q & 1) + k];
+            a[k] = q < 2 ? __builtin_fmaf(dk, xh[j][4 * (q & 1) + k], a[k]) : __fadd_rn(a[k], dk);
+          }
+          sums[(4 * j + q) * 1024 + t] = a;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
-    if (r + G < r1) load(r + G);
+    if constexpr (AGAIN) load_res(r);
+    if constexpr (AHEAD) {
+      if (r + G < r1) {
+        load(r + G);
+        if constexpr (!AGAIN) load_res(r + G);
+      }
+    }
     if constexpr (TC == 16) {
       s1 = sum16(s1);
       s2 = sum16(s2);
@@ -289,8 +338,18 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(LayerNormBwdA
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       const int64_t i = 8 * (int64_t)(j * T + t);
-      if (i < g.H) {
+      if (FULL || i < g.H) {
         float y[8];
+        if constexpr (AGAIN) {
+          float dy[8];
+          for (u4& q : x_now[j].q) asm volatile("" : "+v"(q));   // not kept from above
+          for (u4& q : d_now[j].q) asm volatile("" : "+v"(q));
+          group(x_now[j], d_now[j], mean_r, rstd_r, j, dy, xh[j], gw[j]);
+          if (g.dres != nullptr) {
+            if constexpr (!FULL) shift8<XF>(rs[j], i, g.H);
+            values8<XF>(rs[j], res[j]);
+          }
+        }
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           y[k] = __fmul_rn(rstd_r, __builtin_fmaf(-xh[j][k], c2, __fadd_rn(gw[j][k], -c1)));
@@ -300,22 +359,26 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(LayerNormBwdA
         else store8_bf16(static_cast<uint16_t*>(g.dx) + r * g.H, i, g.H, y);
       }
     }
+    if constexpr (!AHEAD) {
+      if (r + G < r1) load(r + G);
+    }
   }
-  if (part == nullptr) return;
-  float* p = part + (int64_t)blockIdx.x * 2 * g.H;
+  const int64_t at = (int64_t)blockIdx.x * 2 * g.H;
   if constexpr (TC > 0) {
     // the rows side by side are added in order, one kind of sum at a time
     static_assert(U == 1, "");
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if (h > 0) __syncthreads();
+      float* out = h == 0 ? out_w : out_b;
+      if (out == nullptr) continue;
+      __syncthreads();
 #pragma unroll
       for (int k = 0; k < 8; ++k) cols[8 * threadIdx.x + k] = h == 0 ? sw[0][k] : sb[0][k];
       __syncthreads();
       for (int c = threadIdx.x; c < TC * 8; c += blockDim.x) {
         float v = cols[c];
         for (int q = 1; q < G; ++q) v = __fadd_rn(v, cols[q * (TC * 8) + c]);
-        if (c < g.H) p[h * g.H + c] = v;
+        if (c < g.H) out[at + c] = v;
       }
     }
   } else {
@@ -323,8 +386,15 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(LayerNormBwdA
     for (int j = 0; j < U; ++j) {
       const int64_t i = 8 * (int64_t)(j * T + t);
       if (i < g.H) {
-        store8_f32(p, i, g.H, sw[j]);
-        store8_f32(p + g.H, i, g.H, sb[j]);
+        if constexpr (AGAIN) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            sw[0][k] = sums[(4 * j + k / 4) * 1024 + t][k & 3];
+            sb[0][k] = sums[(4 * j + 2 + k / 4) * 1024 + t][k & 3];
+          }
+        }
+        if (out_w != nullptr) store8_f32(out_w + at, i, g.H, sw[AGAIN ? 0 : j]);
+        if (out_b != nullptr) store8_f32(out_b + at, i, g.H, sb[AGAIN ? 0 : j]);
       }
     }
   }
@@ -382,7 +452,7 @@ __global__ __launch_bounds__(1024) void layer_norm_dx_long_kernel(LayerNormBwdAr
       s2 = __builtin_fmaf(gw[k], xh[k], s2);
     }
   }
-  const float c1 = __fmul_rn(row_sum<1024>(s1, red[0]), inv_h), c2 = __fmul_rn(row_sum<1024>(s2, red[1]), inv_h);
+  const float c1 = __fmul_rn(row_sum<0>(s1, red[0]), inv_h), c2 = __fmul_rn(row_sum<0>(s2, red[1]), inv_h);
   for (int64_t i = 8 * (int64_t)threadIdx.x; i < g.H; i += 8 * 1024) {
     row8(i, xh, gw);
     float y[8], res[8];
@@ -460,28 +530,42 @@ __global__ __launch_bounds__(256) void sum_slabs_kernel(const float* __restrict_
 // Workgroups of a grid over rows: up to `most`, which walk the rest.
 unsigned row_grid(int64_t n, int64_t most) { return (unsigned)(n < most ? n : most); }
 
-template <bool F32, int T, int U>
-hipError_t run_norm(const LayerNormArgs& g, hipStream_t stream) {
-  constexpr int rpb = T < 256 ? 256 / T : 1, threads = T < 256 ? 256 : T;
-  // as many workgroups as are resident at once (256 CUs): 4 to 8 waves a SIMD
-  constexpr int64_t most = 256 * ((U <= 1 ? 32 : U == 2 ? 24 : 16) * 64 / threads);
-  hipLaunchKernelGGL((layer_norm_kernel<F32, T, U>), dim3(row_grid((g.rows + rpb - 1) / rpb, most)), dim3(threads), 0,
-                     stream, g);
+template <bool F32, int TC, int U>
+hipError_t run_norm(const LayerNormArgs& g, int threads, hipStream_t stream) {
+  const int rpb = TC > 0 ? 256 / (TC > 0 ? TC : 1) : 1;
+  // as many workgroups as are resident at once (256 CUs, 16 or 20 waves each)
+  const int waves = threads / 64, room = U <= 2 ? 20 : 16;
+  const int64_t most = 256 * (waves > room ? 1 : room / waves);
+  const dim3 grid(row_grid((g.rows + rpb - 1) / rpb, most));
+  if (TC == 0 && g.H == (int64_t)threads * U * 8)
+    hipLaunchKernelGGL((layer_norm_kernel<F32, TC, U, TC == 0>), grid, dim3(threads), 0, stream, g);
+  else
+    hipLaunchKernelGGL((layer_norm_kernel<F32, TC, U, false>), grid, dim3(threads), 0, stream, g);
   return hipGetLastError();
 }
 
+// Few rows: one group of eight per thread, so that a row's latency is least.
+// Many: two or three, which halves the sums over waves, in workgroups of four
+// waves or a multiple: five or six would load the SIMDs unevenly (8000x6000
+// BF16 -> E4M3 in 256 threads of three groups 35 us, in 384 of two 47;
+// 4096x4096 in 256 of two 14.2, in 128 of four 15.5, in 512 of one 16.1).
 template <bool F32>
 hipError_t norm_of_type(const LayerNormArgs& g, hipStream_t stream) {
   const int64_t units = (g.H + 7) / 8;
-  if (units <= 16) return run_norm<F32, 16, 1>(g, stream);
-  if (units <= 64) return run_norm<F32, 64, 1>(g, stream);
-  if (units <= 128 && g.rows > 512) return run_norm<F32, 64, 2>(g, stream);
-  if (units <= 256) return run_norm<F32, 256, 1>(g, stream);
-  if (units <= 512 && g.rows > 512) return run_norm<F32, 256, 2>(g, stream);
-  if (units <= 768 && g.rows > 512) return run_norm<F32, 256, 3>(g, stream);
-  if (units <= 1024) return run_norm<F32, 1024, 1>(g, stream);
-  if (units <= 2048) return run_norm<F32, 1024, 2>(g, stream);
-  if (units <= 4096) return run_norm<F32, 1024, 4>(g, stream);
+  if (units <= 16) return run_norm<F32, 16, 1>(g, 256, stream);
+  if (units <= 64) return run_norm<F32, 64, 1>(g, 256, stream);
+  if (g.rows <= 512) {
+    if (units <= 1024) return run_norm<F32, 0, 1>(g, (int)((units + 63) / 64 * 64), stream);
+  } else {
+    if (units <= 128) return run_norm<F32, 64, 2>(g, 256, stream);
+    if (units <= 256) return run_norm<F32, 0, 1>(g, 256, stream);
+    if (units <= 512) return run_norm<F32, 0, 2>(g, 256, stream);
+    if (units <= 768) return run_norm<F32, 0, 3>(g, 256, stream);
+    if (units <= 1024) return run_norm<F32, 0, 2>(g, 512, stream);
+    if (units <= 1536) return run_norm<F32, 0, 3>(g, 512, stream);
+  }
+  if (units <= 2048) return run_norm<F32, 0, 2>(g, 1024, stream);
+  if (units <= 4096) return run_norm<F32, 0, 4>(g, 1024, stream);
   hipLaunchKernelGGL((layer_norm_long_kernel<F32>), dim3(row_grid(g.rows, 1 << 20)), dim3(1024), 0, stream, g);
   return hipGetLastError();
 }
@@ -490,10 +574,13 @@ hipError_t norm_of_type(const LayerNormArgs& g, hipStream_t stream) {
 constexpr int64_t kBwdRegs = 1024 * 8 * 2;
 
 // How the backward pass covers rows of H elements: threads of a workgroup,
-// rows side by side in it, groups of eight per thread, and slabs: as many
-// workgroups as are resident at once (256 CUs, 16 to 20 waves each), but at
-// least two rows one after another in each.  Narrow rows go 1024 threads to a
-// workgroup where there are enough of them, which keeps the slabs few.
+// rows side by side in it, groups of eight per thread (one up to 8192 columns,
+// then two), and slabs, at least two rows one after another in each.  One workgroup of eight waves or
+// more per CU, two of three to seven, three of fewer: more slabs cost more in
+// partial sums than they hide (4096x4096 BF16 32.4 us with 256 slabs, 34.2
+// with 512, 39.4 with 768; 4000x2600 38.5, 29.6, 37.8; 4096x1024 18.8, 14.4,
+// 14.1).  Narrow rows go 1024 threads to a workgroup where there are enough of
+// them, which keeps the slabs few.
 struct BwdShape {
   int threads, side, groups;
   int64_t slabs;
@@ -507,31 +594,35 @@ BwdShape bwd_shape(int64_t rows, int64_t H) {
     b.side = b.threads / tc;
   } else {
     b.groups = units <= 1024 ? 1 : 2;
-    const int64_t t = (units + b.groups - 1) / b.groups;
-    b.threads = t < 1024 ? (int)((t + 63) / 64 * 64) : 1024;
+    b.threads = (int)((units + 64 * b.groups - 1) / (64 * b.groups) * 64);
   }
   const int waves = b.threads / 64;
-  b.slabs = 256 * (waves > 10 ? 1 : waves > 4 ? 20 / waves : 4);
+  b.slabs = waves >= 8 ? 256 : waves >= 3 ? 512 : 768;
   const int64_t most = (rows + 2 * b.side - 1) / (2 * b.side);
   if (b.slabs > most) b.slabs = most;
   return b;
 }
 
 template <bool XF, bool DF, int TC, int U>
-hipError_t run_backward_kernel(const LayerNormBwdArgs& g, int threads, int64_t slabs, float* part,
+hipError_t run_backward_kernel(const LayerNormBwdArgs& g, int threads, int64_t slabs, float* out_w, float* out_b,
                                hipStream_t stream) {
-  hipLaunchKernelGGL((layer_norm_backward_kernel<XF, DF, TC, U>), dim3((unsigned)slabs), dim3(threads), 0, stream, g,
-                     (g.rows + slabs - 1) / slabs, part);
+  const int64_t slab_rows = (g.rows + slabs - 1) / slabs;
+  if (TC == 0 && g.H == (int64_t)threads * U * 8)
+    hipLaunchKernelGGL((layer_norm_backward_kernel<XF, DF, TC, U, TC == 0>), dim3((unsigned)slabs), dim3(threads), 0,
+                       stream, g, slab_rows, out_w, out_b);
+  else
+    hipLaunchKernelGGL((layer_norm_backward_kernel<XF, DF, TC, U, false>), dim3((unsigned)slabs), dim3(threads), 0,
+                       stream, g, slab_rows, out_w, out_b);
   return hipGetLastError();
 }
 
 template <bool XF, bool DF>
-hipError_t run_backward(const LayerNormBwdArgs& g, int64_t slabs, float* part, hipStream_t stream) {
+hipError_t run_backward(const LayerNormBwdArgs& g, int64_t slabs, float* out_w, float* out_b, hipStream_t stream) {
   const BwdShape b = bwd_shape(g.rows, g.H);
-  if (g.H <= 128) return run_backward_kernel<XF, DF, 16, 1>(g, b.threads, slabs, part, stream);
-  if (g.H <= 512) return run_backward_kernel<XF, DF, 64, 1>(g, b.threads, slabs, part, stream);
-  if (b.groups == 1) return run_backward_kernel<XF, DF, 0, 1>(g, b.threads, slabs, part, stream);
-  return run_backward_kernel<XF, DF, 0, 2>(g, b.threads, slabs, part, stream);
+  if (g.H <= 128) return run_backward_kernel<XF, DF, 16, 1>(g, b.threads, slabs, out_w, out_b, stream);
+  if (g.H <= 512) return run_backward_kernel<XF, DF, 64, 1>(g, b.threads, slabs, out_w, out_b, stream);
+  if (b.groups == 1) return run_backward_kernel<XF, DF, 0, 1>(g, b.threads, slabs, out_w, out_b, stream);
+  return run_backward_kernel<XF, DF, 0, 2>(g, b.threads, slabs, out_w, out_b, stream);
 }
 
 }  // namespace
@@ -554,17 +645,24 @@ hipError_t launch_layer_norm(const LayerNormArgs& g, hipStream_t stream) {
   return g.x_f32 ? norm_of_type<true>(g, stream) : norm_of_type<false>(g, stream);
 }
 
-int64_t layer_norm_backward_slabs(int64_t rows, int64_t H) { return rows == 0 ? 0 : bwd_shape(rows, H).slabs; }
+// (one slab's sums are the results, where registers hold the row)
+int64_t layer_norm_backward_partials(int64_t rows, int64_t H) {
+  const int64_t slabs = rows == 0 || H == 0 ? 0 : bwd_shape(rows, H).slabs;
+  return slabs == 1 && H <= kBwdRegs ? 0 : slabs;
+}
 
 hipError_t launch_layer_norm_backward(const LayerNormBwdArgs& g, float* dw, float* db, float* part,
                                       hipStream_t stream) {
-  const int64_t slabs = layer_norm_backward_slabs(g.rows, g.H);
+  const int64_t slabs = g.rows == 0 ? 0 : bwd_shape(g.rows, g.H).slabs;
   const bool sums = dw != nullptr || db != nullptr;
   hipError_t e = hipSuccess;
   if (slabs > 0 && g.H <= kBwdRegs) {
-    float* p = sums ? part : nullptr;
-    if (g.x_f32) e = g.dy_f32 ? run_backward<true, true>(g, slabs, p, stream) : run_backward<true, false>(g, slabs, p, stream);
-    else e = g.dy_f32 ? run_backward<false, true>(g, slabs, p, stream) : run_backward<false, false>(g, slabs, p, stream);
+    const bool direct = slabs == 1;
+    float* ow = dw == nullptr ? nullptr : (direct ? dw : part);
+    float* ob = db == nullptr ? nullptr : (direct ? db : part + g.H);
+    if (g.x_f32) e = g.dy_f32 ? run_backward<true, true>(g, slabs, ow, ob, stream) : run_backward<true, false>(g, slabs, ow, ob, stream);
+    else e = g.dy_f32 ? run_backward<false, true>(g, slabs, ow, ob, stream) : run_backward<false, false>(g, slabs, ow, ob, stream);
+    if (direct) return e;
   } else if (slabs > 0) {
     if (sums)
       hipLaunchKernelGGL(layer_norm_dw_long_kernel, dim3((unsigned)((g.H + 2047) / 2048), (unsigned)slabs), dim3(256),

@@ -234,16 +234,14 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearActArgs g, const
 // dz = dy act'(pre) for a slab of rows and 8 LP columns, with the columns'
 // sums over the slab (of dz before its rounding to BF16) into part[slab, n].
 // Bound by memory.  LP threads side by side hold eight consecutive columns
-// each, kActThreads / LP of them share the slab's rows (narrow tensors thus
-// keep all lanes busy) and are added through LDS in order; R rows are in
-// flight per thread.
-constexpr int kActThreads = 256;
-
-template <int LP>
-__global__ __launch_bounds__(kActThreads) void act_backward_kernel(
+// each, NT / LP of them share the slab's rows (narrow tensors thus keep all
+// lanes busy) and are added through LDS in order; R rows are in flight per
+// thread.
+template <int LP, int NT>
+__global__ __launch_bounds__(NT) void act_backward_kernel(
     const uint16_t* dy, const uint16_t* pre, int act, uint16_t* dz, float* __restrict__ part, int64_t M, int64_t N,
     int64_t slab_rows) {
-  constexpr int RL = kActThreads / LP, R = 4;
+  constexpr int RL = NT / LP, R = 4;
   __shared__ float red[RL][LP * 8];
   const int cl = threadIdx.x % LP, rl = threadIdx.x / LP;
   const int64_t n = ((int64_t)blockIdx.x * LP + cl) * 8;
@@ -282,7 +280,7 @@ __global__ __launch_bounds__(kActThreads) void act_backward_kernel(
 #pragma unroll
   for (int c = 0; c < 8; ++c) red[rl][cl * 8 + c] = s[c];
   __syncthreads();
-  for (int c = threadIdx.x; c < LP * 8; c += kActThreads) {
+  for (int c = threadIdx.x; c < LP * 8; c += NT) {
     float v = red[0][c];
 #pragma unroll
     for (int k = 1; k < RL; ++k) v = __fadd_rn(v, red[k][c]);
@@ -291,14 +289,31 @@ __global__ __launch_bounds__(kActThreads) void act_backward_kernel(
   }
 }
 
-// Threads side by side: the row's groups of eight, up to 64.
-int act_lanes(int64_t N) { return N <= 64 ? 8 : N <= 128 ? 16 : N <= 256 ? 32 : 64; }
+// How the backward pass of the epilogue covers [M, N].  Up to kActOneSlab rows
+// a workgroup of 1024 threads takes 32 columns of all of them and its sums are
+// the results: a second launch costs more than the rows (64x4096 4.6 us,
+// 5.1 in slabs; but 777x2053 13.0, 9.2 in slabs).  Otherwise 256 threads, up to
+// 64 side by side, about eight workgroups per CU.
+constexpr int64_t kActOneSlab = 128;
+struct ActShape {
+  int lanes;
+  int64_t slabs;
+};
+ActShape act_shape(int64_t M, int64_t N) {
+  if (M <= kActOneSlab) return {4, 1};
+  const int lanes = N <= 64 ? 8 : N <= 128 ? 16 : N <= 256 ? 32 : 64;
+  const int64_t across = (N + lanes * 8 - 1) / (lanes * 8), side = 256 / lanes;
+  int64_t slabs = (256 * 8 + across - 1) / across;
+  const int64_t most = (M + side - 1) / side;   // at least a row per thread
+  if (slabs > most) slabs = most;
+  return {lanes, slabs};
+}
 
-template <int LP>
+template <int LP, int NT>
 hipError_t run_act_backward(const uint16_t* dy, const uint16_t* pre, int act, uint16_t* dz, float* part, int64_t M,
                             int64_t N, int64_t slabs, hipStream_t stream) {
-  hipLaunchKernelGGL((act_backward_kernel<LP>), dim3((unsigned)((N + LP * 8 - 1) / (LP * 8)), (unsigned)slabs),
-                     dim3(kActThreads), 0, stream, dy, pre, act, dz, part, M, N, (M + slabs - 1) / slabs);
+  hipLaunchKernelGGL((act_backward_kernel<LP, NT>), dim3((unsigned)((N + LP * 8 - 1) / (LP * 8)), (unsigned)slabs),
+                     dim3(NT), 0, stream, dy, pre, act, dz, part, M, N, (M + slabs - 1) / slabs);
   return hipGetLastError();
 }
 
@@ -390,32 +405,29 @@ hipError_t launch_linear_act(const LinearActArgs& g, int accum, float* ws, int n
   return hipGetLastError();
 }
 
-int64_t act_backward_slabs(int64_t M, int64_t N) {
-  if (M == 0 || N == 0) return 0;
-  // about eight workgroups per CU, at least a row per thread
-  const int64_t lp = act_lanes(N), across = (N + lp * 8 - 1) / (lp * 8), rl = kActThreads / lp;
-  int64_t slabs = (256 * 8 + across - 1) / across;
-  const int64_t most = (M + rl - 1) / rl;
-  if (slabs > most) slabs = most;
-  return slabs < 1 ? 1 : slabs;
+// (one slab's sums are the results)
+int64_t act_backward_partials(int64_t M, int64_t N) {
+  const int64_t slabs = M == 0 || N == 0 ? 0 : act_shape(M, N).slabs;
+  return slabs == 1 ? 0 : slabs;
 }
 
 hipError_t launch_act_backward(const uint16_t* dy, const uint16_t* pre, int act, uint16_t* dz,
                                float* dbias, int64_t M, int64_t N, float* part, hipStream_t stream) {
-  const int64_t slabs = act_backward_slabs(M, N);
-  if (slabs > 0) {
-    float* p = dbias != nullptr ? part : nullptr;
+  if (M > 0 && N > 0) {
+    const ActShape s = act_shape(M, N);
+    float* p = dbias != nullptr && s.slabs > 1 ? part : dbias;
     hipError_t e;
-    switch (act_lanes(N)) {
-      case 8: e = run_act_backward<8>(dy, pre, act, dz, p, M, N, slabs, stream); break;
-      case 16: e = run_act_backward<16>(dy, pre, act, dz, p, M, N, slabs, stream); break;
-      case 32: e = run_act_backward<32>(dy, pre, act, dz, p, M, N, slabs, stream); break;
-      default: e = run_act_backward<64>(dy, pre, act, dz, p, M, N, slabs, stream); break;
+    switch (s.lanes) {
+      case 4: e = run_act_backward<4, 1024>(dy, pre, act, dz, p, M, N, s.slabs, stream); break;
+      case 8: e = run_act_backward<8, 256>(dy, pre, act, dz, p, M, N, s.slabs, stream); break;
+      case 16: e = run_act_backward<16, 256>(dy, pre, act, dz, p, M, N, s.slabs, stream); break;
+      case 32: e = run_act_backward<32, 256>(dy, pre, act, dz, p, M, N, s.slabs, stream); break;
+      default: e = run_act_backward<64, 256>(dy, pre, act, dz, p, M, N, s.slabs, stream); break;
     }
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || s.slabs == 1) return e;
   }
   if (dbias == nullptr) return hipSuccess;
-  return launch_sum_slabs(part, dbias, nullptr, slabs, N, N, stream);
+  return launch_sum_slabs(part, dbias, nullptr, act_backward_partials(M, N), N, N, stream);
 }
 
 }  // namespace fp8mot

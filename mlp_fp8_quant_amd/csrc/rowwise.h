@@ -24,11 +24,12 @@ struct Raw8 {
   u4 q[F32 ? 2 : 1];
 };
 
-// Elements i .. i + 7 of a row of n; zeros past its end.
-template <bool F32>
+// Elements i .. i + 7 of a row of n; zeros past its end.  WHOLE: the row does
+// not end before them.
+template <bool F32, bool WHOLE = false>
 __device__ __forceinline__ Raw8<F32> load8(const void* row, int64_t i, int64_t n) {
   Raw8<F32> r;
-  if (i + 8 <= n) {
+  if (WHOLE || i + 8 <= n) {
     if constexpr (F32) {
       const float* p = static_cast<const float*>(row) + i;
       r.q[0] = __builtin_bit_cast(u4, (f4)(*reinterpret_cast<const f4a4*>(p)));
@@ -50,6 +51,49 @@ __device__ __forceinline__ Raw8<F32> load8(const void* row, int64_t i, int64_t n
     }
   }
   return r;
+}
+
+// The same of a row of n >= 8 without a branch: a group that crosses the row's
+// end is the row's last eight elements, which shift8 puts in their places once
+// they have arrived.  (load8's end is loads that wait for one another: a
+// workgroup whose last wave takes it waits for that wave in every row.)
+template <bool F32>
+__device__ __forceinline__ Raw8<F32> load8_ahead(const void* row, int64_t i, int64_t n) {
+  return load8<F32, true>(row, i + 8 <= n ? i : n - 8, n);
+}
+template <bool F32>
+__device__ __forceinline__ void shift8(Raw8<F32>& r, int64_t i, int64_t n) {
+  if (i + 8 <= n) return;
+  const int s = i >= n ? 8 : (int)(i + 8 - n);   // elements past the end
+  if constexpr (F32) {
+    uint32_t v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = r.q[k >> 2][k & 3];
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1)
+      if (s & d) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = k + d < 8 ? v[k + d] : 0;
+      }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) r.q[k >> 2][k & 3] = v[k];
+  } else {
+    uint32_t v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = r.q[0][k];
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1)
+      if (s & (2 * d)) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = k + d < 4 ? v[k + d] : 0;
+      }
+    if (s & 1) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = v[k] >> 16 | (k < 3 ? v[k + 1] << 16 : 0);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r.q[0][k] = v[k];
+  }
 }
 
 template <bool F32>

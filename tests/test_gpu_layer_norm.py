@@ -199,7 +199,20 @@ def test_backward_types(xt, dt, wt):
     check_backward(70, 521, 3, xt, dt, wt or F32, weight=wt is not None)
 
 
-@pytest.mark.parametrize("H", [520, 1027, 30000])
+@pytest.mark.parametrize("xt", [BF16, F32])
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("H", [129, 135, 1536, 8185, 8192, 8193, 10001, 15361, 16384])
+def test_backward_row_ends(xt, dt, H):
+    # rows that end at each place of a group, a wave and a workgroup
+    check_backward(5, H, H, xt, dt)
+
+
+def test_backward_of_many_long_rows():
+    check_backward(1100, 8200, 5)
+    check_backward(600, 16384, 6, F32, F32, dres=False)
+
+
+@pytest.mark.parametrize("H", [520, 1024, 1027, 9001, 16384, 30000])
 def test_backward_in_place(H):
     dy, x, w, mean, rstd, dr, want = check_backward(65, H, 12)
     for over in ("dy", "dres", "x"):

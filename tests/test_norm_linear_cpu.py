@@ -65,8 +65,8 @@ def linear_backward(dy=FAKE, pre=FAKE, act=1, dz=FAKE, db=FAKE, M=4, N=8, ws=FAK
     (INVALID, dict(act=5)), (INVALID, dict(M=-1)), (INVALID, dict(N=-1)), (INVALID, dict(N=1 << 31)),
     (INVALID, dict(M=1 << 31)), (INVALID, dict(dy=NULL)), (INVALID, dict(pre=NULL)),
     (MISALIGNED, dict(dy=ODD)), (MISALIGNED, dict(pre=ODD)), (MISALIGNED, dict(dz=ODD)),
-    (MISALIGNED, dict(db=ODD)), (WORKSPACE, dict(ws=NULL)), (WORKSPACE, dict(wb=16)), (WORKSPACE, dict(ws=ODD)),
-    (OK, dict(N=0)), (OK, dict(M=0, db=NULL)), (OK, dict(dz=NULL, db=NULL)),
+    (MISALIGNED, dict(db=ODD)), (WORKSPACE, dict(M=400, ws=NULL)), (WORKSPACE, dict(M=400, wb=16)),
+    (WORKSPACE, dict(M=400, ws=ODD)), (OK, dict(N=0)), (OK, dict(M=0, db=NULL)), (OK, dict(dz=NULL, db=NULL)),
 ])
 def test_linear_backward_refusals(want, args):
     assert linear_backward(**args) == want
@@ -97,11 +97,21 @@ def norm_backward(dy=FAKE, de=0, x=FAKE, xe=0, w=FAKE, we=0, mean=FAKE, rstd=FAK
     (INVALID, dict(H=-1)), (INVALID, dict(dy=NULL)), (INVALID, dict(x=NULL)), (INVALID, dict(mean=NULL)),
     (INVALID, dict(rstd=NULL)), (INVALID, dict(dx=NULL)), (MISALIGNED, dict(dy=ODD)), (MISALIGNED, dict(x=ODD)),
     (MISALIGNED, dict(w=ODD)), (MISALIGNED, dict(dres=ODD)), (MISALIGNED, dict(dx=ODD)),
-    (MISALIGNED, dict(dw=ODD)), (MISALIGNED, dict(db=ODD)), (WORKSPACE, dict(ws=NULL)), (WORKSPACE, dict(wb=4)),
-    (WORKSPACE, dict(ws=ODD)), (OK, dict(H=0)), (OK, dict(rows=0, dw=NULL, db=NULL)),
+    (MISALIGNED, dict(dw=ODD)), (MISALIGNED, dict(db=ODD)), (WORKSPACE, dict(rows=400, ws=NULL)),
+    (WORKSPACE, dict(rows=400, wb=4)), (WORKSPACE, dict(rows=400, ws=ODD)), (WORKSPACE, dict(H=20000, ws=NULL)),
+    (OK, dict(H=0)), (OK, dict(rows=0, dw=NULL, db=NULL)),
 ])
 def test_norm_backward_refusals(want, args):
     assert norm_backward(**args) == want
+
+
+def test_backward_workspaces():
+    lib, huge = L.lib(), 1 << 62
+    for f in (lib.fp8_linear_act_backward_workspace, lib.fp8_layer_norm_backward_workspace):
+        # one slab of rows writes its sums where they belong; refused sizes need nothing
+        assert f(4, 64) == f(0, 64) == f(64, 0) == f(-1, 64) == f(huge, 64) == f(64, huge) == 0
+        assert f(4000, 64) > 0
+    assert lib.fp8_linear_act_workspace(huge, 64, 64) == lib.fp8_linear_act_workspace(64, huge, 64) == 0
 
 
 def test_binding_refuses_before_the_library():
