@@ -206,7 +206,7 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(LayerNormBwdA
   constexpr bool AGAIN = U > 1, AHEAD = U == 1 || (!XF && !DF);
   const int G = TC > 0 ? (int)blockDim.x / TC : 1;   // rows side by side
   __shared__ float red[2][2][16];
-  __shared__ float cols[TC > 0 ? 1024 * 8 : 1];      // [G][8 TC]
+  __shared__ f4 cols[TC > 0 ? 4 * 512 : 1];          // half the threads' sums
   __shared__ f4 sums[AGAIN ? 4 * U * 1024 : 1];      // [dw, db][U][half][threads]: each thread's own
   const int T = TC > 0 ? TC : blockDim.x, waves = T >> 6, t = TC > 0 ? threadIdx.x % TC : threadIdx.x;
   const float inv_h = 1.0f / (float)g.H;
@@ -365,21 +365,31 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(LayerNormBwdA
   }
   const int64_t at = (int64_t)blockIdx.x * 2 * g.H;
   if constexpr (TC > 0) {
-    // the rows side by side are added in order, one kind of sum at a time
+    // the rows side by side (a power of two) are added in a tree
     static_assert(U == 1, "");
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float* out = h == 0 ? out_w : out_b;
-      if (out == nullptr) continue;
-      __syncthreads();
-#pragma unroll
-      for (int k = 0; k < 8; ++k) cols[8 * threadIdx.x + k] = h == 0 ? sw[0][k] : sb[0][k];
-      __syncthreads();
-      for (int c = threadIdx.x; c < TC * 8; c += blockDim.x) {
-        float v = cols[c];
-        for (int q = 1; q < G; ++q) v = __fadd_rn(v, cols[q * (TC * 8) + c]);
-        if (c < g.H) out[at + c] = v;
+    if (out_w == nullptr && out_b == nullptr) return;
+    const int q = threadIdx.x / TC;
+    for (int h = G >> 1; h > 0; h >>= 1) {
+      const int at4 = (q & (h - 1)) * TC + t, n4 = h * TC;
+      if (q >= h && q < 2 * h) {
+        cols[at4] = (f4){sw[0][0], sw[0][1], sw[0][2], sw[0][3]};
+        cols[n4 + at4] = (f4){sw[0][4], sw[0][5], sw[0][6], sw[0][7]};
+        cols[2 * n4 + at4] = (f4){sb[0][0], sb[0][1], sb[0][2], sb[0][3]};
+        cols[3 * n4 + at4] = (f4){sb[0][4], sb[0][5], sb[0][6], sb[0][7]};
       }
+      __syncthreads();
+      if (q < h) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          sw[0][k] = __fadd_rn(sw[0][k], cols[(k >> 2) * n4 + at4][k & 3]);
+          sb[0][k] = __fadd_rn(sb[0][k], cols[(2 + (k >> 2)) * n4 + at4][k & 3]);
+        }
+      }
+      __syncthreads();
+    }
+    if (q == 0 && 8 * t < g.H) {
+      if (out_w != nullptr) store8_f32(out_w + at, 8 * t, g.H, sw[0]);
+      if (out_b != nullptr) store8_f32(out_b + at, 8 * t, g.H, sb[0]);
     }
   } else {
 #pragma unroll
@@ -575,12 +585,14 @@ constexpr int64_t kBwdRegs = 1024 * 8 * 2;
 
 // How the backward pass covers rows of H elements: threads of a workgroup,
 // rows side by side in it, groups of eight per thread (one up to 8192 columns,
-// then two), and slabs, at least two rows one after another in each.  One workgroup of eight waves or
-// more per CU, two of three to seven, three of fewer: more slabs cost more in
-// partial sums than they hide (4096x4096 BF16 32.4 us with 256 slabs, 34.2
-// with 512, 39.4 with 768; 4000x2600 38.5, 29.6, 37.8; 4096x1024 18.8, 14.4,
-// 14.1).  Narrow rows go 1024 threads to a workgroup where there are enough of
-// them, which keeps the slabs few.
+// then two), and slabs.  One workgroup of eight waves or more per CU, two of
+// three to seven, three of fewer: more slabs cost more in partial sums than
+// they hide (4096x4096 FP32 41.7 us with 256 slabs, 44.3 with 512; 4000x2600
+// BF16 38.5, 29.6; 4096x1024 18.8, 14.4).  For the same reason a slab's rows
+// are one, two or at least four one after another (64x4096 6.5, 7.0, 8.6;
+// 256x4096 11.3, 9.0, 9.7; 512x4096 13.6, 13.6, 12.5; 777x2053 17.7, 16.2,
+// 14.1); narrow rows, which go side by side, need no second (5000x100 8.2, 9.2,
+// 11.6).  They take 1024 threads to a workgroup where there are enough of them.
 struct BwdShape {
   int threads, side, groups;
   int64_t slabs;
@@ -598,7 +610,8 @@ BwdShape bwd_shape(int64_t rows, int64_t H) {
   }
   const int waves = b.threads / 64;
   b.slabs = waves >= 8 ? 256 : waves >= 3 ? 512 : 768;
-  const int64_t most = (rows + 2 * b.side - 1) / (2 * b.side);
+  const int64_t walk = b.side > 1 || rows <= 64 ? 1 : rows <= 256 ? 2 : 4;
+  const int64_t most = (rows + walk * b.side - 1) / (walk * b.side);
   if (b.slabs > most) b.slabs = most;
   return b;
 }
