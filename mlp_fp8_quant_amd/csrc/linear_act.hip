@@ -45,11 +45,12 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_rows_kernel(LinearActArgs g
   __shared__ __attribute__((aligned(1024))) uint8_t smem[NW * D * STAGE];
   // Epilogue: a wave takes G 16-row blocks of the same 16 columns at once
   // (their operands in flight together), ROUNDS times; one copy of the code,
-  // since every launch fetches it cold.
+  // since every launch fetches it cold.  The first round's operands are read
+  // during the product, the second's during the join.
   constexpr int PER = MB * NB / NW;
   constexpr int G = PER < 1 ? 1 : (PER < MB ? PER : MB), CHUNKS = MB * NB / G, ROUNDS = (CHUNKS + NW - 1) / NW;
   static_assert(MB % G == 0, "chunks of rows");
-  constexpr bool EARLY = ROUNDS == 1;   // operands are read during the product, or else round by round
+  static_assert(ROUNDS <= 2, "operands of the first round and the next");
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int l15 = lane & 15, kq = lane >> 4;
@@ -59,12 +60,12 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_rows_kernel(LinearActArgs g
 
   const bool vec = (g.N & 3) == 0;
   const linear::Epilogue epi = linear::open_epilogue(g, m0);
-  linear::Operands<G> op;
-  linear::Columns col;
+  linear::Operands<G> op, op2;
+  linear::Columns col, col2;
   // chunk q: rows row_of(q), + 16, .. from m0, columns col_of(q) .. + 3
   auto row_of = [&](int q) { return 16 * G * (q / NB) + l15; };
   auto col_of = [&](int q) { return (int)n0 + 16 * (q % NB) + 4 * kq; };
-  auto operands = [&](int q) {
+  auto operands = [&](int q, linear::Operands<G>& op, linear::Columns& col) {
     const int row = row_of(q), n = col_of(q), nv = (int)g.N - n;
     if (vec) {
       linear::load_operands<G, true>(g, epi, m0, row, 16, n, nv, &op);
@@ -74,7 +75,7 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_rows_kernel(LinearActArgs g
       col = linear::load_columns<false>(g, n, nv);
     }
   };
-  if (wave < CHUNKS && EARLY) operands(wave);
+  if (wave < CHUNKS) operands(wave, op, col);   // they arrive during the product
 
   // copy q of a stage fills LDS rows 8q .. 8q + 7 (W's 16 NB rows, then X's):
   // lane l brings row 8q + l/8, physical chunk l % 8
@@ -152,10 +153,9 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_rows_kernel(LinearActArgs g
       for (int b = 0; b < MB; ++b) {
         const f16x8 x0 = decode8(f[NB + b][h][0], f[NB + b][h][1]), x1 = decode8(f[NB + b][h][2], f[NB + b][h][3]);
 #pragma unroll
-        for (int c = 0; c < NB; ++c) {
-          acc[b][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w0[c], x0, acc[b][c], 0, 0, 0);
-          acc[b][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w1[c], x1, acc[b][c], 0, 0, 0);
-        }
+        for (int c = 0; c < NB; ++c) acc[b][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w0[c], x0, acc[b][c], 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < NB; ++c) acc[b][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w1[c], x1, acc[b][c], 0, 0, 0);
       }
     }
   }
@@ -167,7 +167,7 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_rows_kernel(LinearActArgs g
   for (int b = 0; b < MB; ++b)
 #pragma unroll
     for (int c = 0; c < NB; ++c) red[(wave * (MB * NB) + b * NB + c) * 64 + lane] = acc[b][c];
-  if (wave < CHUNKS && !EARLY) operands(wave);
+  if (wave + NW < CHUNKS) operands(wave + NW, op2, col2);
   __syncthreads();
 #pragma unroll 1
   for (int q = wave; q < CHUNKS; q += NW) {
@@ -186,12 +186,12 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_rows_kernel(LinearActArgs g
       for (int v = 0; v < 4; ++v) z[k][v] = s[v];
     }
     const int row = row_of(q), n = col_of(q), nv = (int)g.N - n;
-    const linear::Columns c = col;
     auto next = [&] {
-      if (q + NW < CHUNKS) operands(q + NW);
+      op = op2;
+      col = col2;
     };
-    if (vec) linear::finish<G, true>(g, epi, c, row, 16, n, nv, op, z, next);
-    else linear::finish<G, false>(g, epi, c, row, 16, n, nv, op, z, next);
+    if (vec) linear::finish<G, true>(g, epi, col, row, 16, n, nv, op, z, next);
+    else linear::finish<G, false>(g, epi, col, row, 16, n, nv, op, z, next);
   }
 }
 
@@ -326,9 +326,10 @@ hipError_t run_act_backward(const uint16_t* dy, const uint16_t* pre, int act, ui
 // own L1 at 40-50 bytes a clock whatever the tile: 1x4096x4096 5.2 with 16x16
 // blocks and 16 waves (16x32: 5.6), 64x4096x4096 7.3 with 32x32 (64x32 10.3,
 // 32x16 8.2), 256x4096x4096 15.4 with 64x64 (64x32 19.3; 128x128 tiles split
-// four ways over K 23.1).  Above that, up to two workgroups per CU (64x64,
-// two waves): 512x4096x2048 16.1 (128x128 tiles 23.0), 512x4096x12288 55.7
-// (128x128 split in two 54.7), 777x2053x2064 20.4 (27.1).
+// four ways over K 23.1), 128x12288x4096 22.0 with 64x96 (64x64 in pairs 24.2),
+// 500x3000x3008 18.6 (24.8).  Above that, up to two workgroups per CU (64x64,
+// two waves): 512x4096x2048 16.1 (128x128 tiles 23.0), 512x4096x12288 55
+// (128x128 split in two 54.7), 777x2053x2064 20.0 (27.1).
 //
 // More outputs: the cheapest of the tiles and splits by an estimate of rounds
 // of workgroups times (rate * K + what a tile costs besides), plus the second
@@ -348,6 +349,7 @@ LinearPlan linear_plan(int64_t M, int64_t N, int64_t K) {
   if (M <= 32) return {kRows2x4, 1};
   if (area <= 8) return {kRows4x2, 1};
   if (area <= 16) return {kRows4x4, 1};
+  if (up(M, 64) * up(N, 96) <= kCus) return {kRows4x6, 1};
   if (M <= 64) return {kRows4x4Pair, 1};
   if (area <= 32) return {kRows4x4Pair, 1};
   auto tiles = [&](int bm, int bn) { return up(M, bm) * up(N, bn); };
@@ -391,6 +393,7 @@ hipError_t launch_linear_act(const LinearActArgs& g, int accum, float* ws, int n
     case kRows2x4: return launch_rows<2, 4, 4, 2>(g, stream);
     case kRows4x2: return launch_rows<4, 2, 4, 2>(g, stream);
     case kRows4x4: return launch_rows<4, 4, 4, 2>(g, stream);
+    case kRows4x6: return launch_rows<4, 6, 4, 2>(g, stream);
     case kRows4x4Pair: return launch_rows<4, 4, 2, 2>(g, stream);
     default: break;
   }

@@ -155,15 +155,16 @@ __device__ __forceinline__ Epilogue open_epilogue(const LinearActArgs& g, int64_
   return e;
 }
 
-// Bias and (with row scales) weight scales of four columns.
+// Bias and (with row scales) weight scales of four columns, as raw dwords: what
+// loads them does not wait for them.
 struct Columns {
-  float bias[4], sw[4];
+  u4v bias, sw;
 };
 template <bool VEC>
 __device__ __forceinline__ Columns load_columns(const LinearActArgs& g, int n, int nv) {
-  Columns c = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-  if (g.bias != nullptr) values4(load4<VEC>(rows_of(g.bias, 0, 1, g.N, g.bias_f32 ? 4 : 2), g.bias_f32, n, nv), g.bias_f32, c.bias);
-  if (g.row_scales) values4(load4<VEC>(rows_of(g.sw, 0, 1, g.N, 4), 1, n, nv), 1, c.sw);
+  Columns c = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+  if (g.bias != nullptr) c.bias = load4<VEC>(rows_of(g.bias, 0, 1, g.N, g.bias_f32 ? 4 : 2), g.bias_f32, n, nv);
+  if (g.row_scales) c.sw = load4<VEC>(rows_of(g.sw, 0, 1, g.N, 4), 1, n, nv);
   return c;
 }
 
@@ -198,16 +199,19 @@ template <int G, bool VEC, class Next>
 __device__ __forceinline__ void finish(const LinearActArgs& g, const Epilogue& e, const Columns& col, int row,
                                        int dm, int n, int nv, const Operands<G>& o, float (*z)[4], Next next) {
   const int N = (int)g.N;
+  float bias[4], sw[4];
+  values4(col.bias, g.bias_f32, bias);
   if (g.row_scales) {
+    values4(col.sw, 1, sw);
 #pragma unroll
     for (int k = 0; k < G; ++k)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) z[k][c] = __builtin_fmaf(z[k][c], __fmul_rn(o.sx[k], col.sw[c]), col.bias[c]);
+      for (int c = 0; c < 4; ++c) z[k][c] = __builtin_fmaf(z[k][c], __fmul_rn(o.sx[k], sw[c]), bias[c]);
   } else {
 #pragma unroll
     for (int k = 0; k < G; ++k)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) z[k][c] = __builtin_fmaf(z[k][c], e.alpha, col.bias[c]);
+      for (int c = 0; c < 4; ++c) z[k][c] = __builtin_fmaf(z[k][c], e.alpha, bias[c]);
   }
   if (g.pre != nullptr) {
 #pragma unroll
