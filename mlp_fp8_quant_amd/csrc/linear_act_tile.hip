@@ -105,7 +105,11 @@ __global__ __launch_bounds__(WM* WN * 64 * KSPL, 1) void linear_tile_kernel(Tile
   // Copy q (= wave * LPW + i) of a stage fills LDS rows q*RPI .. q*RPI+RPI-1
   // (A rows, then B rows); lane l brings row q*RPI + l/CH, physical chunk
   // l % CH, i.e. logical chunk swz(row, l % CH).
-  auto copy_offsets = [&](int m0, int n0, int* goff, int* gkc) {
+  // copy_offsets gives the lane's offset in each copy and, as kc, the column of
+  // its chunk in even and in odd ones (rows of consecutive copies lie RPI
+  // apart, so the swizzle has no other values).
+  static_assert(LPW % 2 == 0 && A_INS % 2 == 0 && (2 * RPI) % (2 * CH) == 0, "two columns per lane");
+  auto copy_offsets = [&](int m0, int n0, int* goff, int* kc) {
     int ln = lane0;
     // opaque, so that no part of this is kept in registers across the epilogue
     if constexpr (PERSIST) asm volatile("" : "+v"(ln));
@@ -115,28 +119,25 @@ __global__ __launch_bounds__(WM* WN * 64 * KSPL, 1) void linear_tile_kernel(Tile
       const int lr = (q < A_INS ? q : q - A_INS) * RPI + ln / CH;
       const int c = swz(lr, ln % CH);
       goff[i] = lr < (q < A_INS ? M - m0 : N - n0) ? lr * K + c * 16 : kOOB;
-      gkc[i] = c * 16;
+      if (i < 2) kc[i] = c * 16;
     }
   };
-  // Copy i of this wave for stage s into buffer b.  K a multiple of the stage
-  // (kfull): no per-lane arithmetic, the stage's column goes in as the wave's
-  // scalar offset, and a stage past s1 reads through an empty descriptor
-  // (zeros land in LDS).  Otherwise each chunk is checked against K.
-  auto issue_copy = [&](const Windows& w, const int* goff, const int* gkc, int b, int s, int i, auto kfull) {
+  // Copy i of this wave for stage s into buffer b: the stage's column is the
+  // wave's scalar offset, and a stage past s1 reads through an empty descriptor
+  // (zeros land in LDS).  Unless K is a multiple of the stage (kfull), chunks
+  // past K's end get an offset past the window.
+  auto issue_copy = [&](const Windows& w, const int* goff, const int* kc, int b, int s, int i, auto kfull) {
     const int k0 = s * KS;
     const int q = wave * LPW + i;
     const v4i rs = q < A_INS ? w.a : w.b;
     const uint32_t dst = (uint32_t)reinterpret_cast<uintptr_t>(
         (lds_ptr_t)(q < A_INS ? a_buf(b) + q * 1024 : b_buf(b) + (q - A_INS) * 1024));
-    if constexpr (decltype(kfull)::value) {
-      copy_to_lds(s < s1 ? rs : (v4i){0, 0, 0, 0x00020000}, dst, goff[i], s < s1 ? k0 : 0);
-    } else {
-      copy_to_lds(rs, dst, (goff[i] != kOOB && s < s1 && k0 + gkc[i] < K) ? goff[i] + k0 : kOOB, 0);
-    }
+    const int off = decltype(kfull)::value || kc[i & 1] < K - k0 ? goff[i] : kOOB;
+    copy_to_lds(s < s1 ? rs : (v4i){0, 0, 0, 0x00020000}, dst, off, s < s1 ? k0 : 0);
   };
-  auto issue_stage = [&](const Windows& w, const int* goff, const int* gkc, int b, int s, auto kfull) {
+  auto issue_stage = [&](const Windows& w, const int* goff, const int* kc, int b, int s, auto kfull) {
 #pragma unroll
-    for (int i = 0; i < LPW; ++i) issue_copy(w, goff, gkc, b, s, i, kfull);
+    for (int i = 0; i < LPW; ++i) issue_copy(w, goff, kc, b, s, i, kfull);
   };
 
   constexpr std::integral_constant<bool, KFULL> kfull{};
@@ -150,8 +151,8 @@ __global__ __launch_bounds__(WM* WN * 64 * KSPL, 1) void linear_tile_kernel(Tile
   tile_of(tile, tiles_m, tiles_n, kBand, tm, tn);
   const int m0 = tm * BM, n0 = tn * BN;
   const Windows win = windows(m0, n0);
-  int goff[LPW], gkc[LPW];
-  copy_offsets(m0, n0, goff, gkc);
+  int goff[LPW], kc[2];
+  copy_offsets(m0, n0, goff, kc);
   v16f acc[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
@@ -210,7 +211,7 @@ __global__ __launch_bounds__(WM* WN * 64 * KSPL, 1) void linear_tile_kernel(Tile
       if constexpr (kCopies) {
 #pragma unroll
         for (int c = 0; c < CPR; ++c)
-          if (i * CPR + c < LPW) issue_copy(win, goff, gkc, cb, cs, i * CPR + c, kfull);
+          if (i * CPR + c < LPW) issue_copy(win, goff, kc, cb, cs, i * CPR + c, kfull);
       }
     };
     if constexpr (ENGINE == 0) {
@@ -259,7 +260,7 @@ __global__ __launch_bounds__(WM* WN * 64 * KSPL, 1) void linear_tile_kernel(Tile
   if (!staged) {
 #pragma unroll
     for (int u = 0; u < NB; ++u)
-      if (u < KT) issue_stage(win, goff, gkc, u, gstage(u), kfull);
+      if (u < KT) issue_stage(win, goff, kc, u, gstage(u), kfull);
   }
   if (KT > 0) {
     // staged: the previous epilogue's accesses were issued after these copies
@@ -335,11 +336,11 @@ __global__ __launch_bounds__(WM* WN * 64 * KSPL, 1) void linear_tile_kernel(Tile
     int ntm, ntn;
     tile_of(tile + gridDim.x, tiles_m, tiles_n, kBand, ntm, ntn);
     const Windows nw = windows(ntm * BM, ntn * BN);
-    int ngoff[LPW], ngkc[LPW];
-    copy_offsets(ntm * BM, ntn * BN, ngoff, ngkc);
+    int ngoff[LPW], nkc[2];
+    copy_offsets(ntm * BM, ntn * BN, ngoff, nkc);
 #pragma unroll
     for (int u = 0; u < NB; ++u)
-      if (u < KT) issue_stage(nw, ngoff, ngkc, u, gstage(u), kfull);
+      if (u < KT) issue_stage(nw, ngoff, nkc, u, gstage(u), kfull);
     staged = true;
   }
 
