@@ -292,8 +292,10 @@ __global__ __launch_bounds__(NT) void act_backward_kernel(
 // How the backward pass of the epilogue covers [M, N].  Up to kActOneSlab rows
 // a workgroup of 1024 threads takes 32 columns of all of them and its sums are
 // the results: a second launch costs more than the rows (64x4096 4.6 us,
-// 5.1 in slabs; but 777x2053 13.0, 9.2 in slabs).  Otherwise 256 threads, up to
-// 64 side by side, about eight workgroups per CU.
+// 5.1 in slabs; but 777x2053 13.0, 8.8 in slabs).  Otherwise 256 threads, up to
+// 64 side by side, about eight workgroups per CU, and at least a row per thread
+// or (wide rows, whose partial sums cost more) two: 1024x4096 10.3 us, 11.9
+// with one, 10.5 with four; 2000x100 5.7 with one, 6.4 with two.
 constexpr int64_t kActOneSlab = 128;
 struct ActShape {
   int lanes;
@@ -304,7 +306,7 @@ ActShape act_shape(int64_t M, int64_t N) {
   const int lanes = N <= 64 ? 8 : N <= 128 ? 16 : N <= 256 ? 32 : 64;
   const int64_t across = (N + lanes * 8 - 1) / (lanes * 8), side = 256 / lanes;
   int64_t slabs = (256 * 8 + across - 1) / across;
-  const int64_t most = (M + side - 1) / side;   // at least a row per thread
+  const int64_t walk = lanes == 64 ? 2 : 1, most = (M + walk * side - 1) / (walk * side);
   if (slabs > most) slabs = most;
   return {lanes, slabs};
 }
