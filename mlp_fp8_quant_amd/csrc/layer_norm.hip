@@ -608,6 +608,14 @@ BwdShape bwd_shape(int64_t rows, int64_t H) {
     b.groups = units <= 1024 ? 1 : 2;
     b.threads = (int)((units + 64 * b.groups - 1) / (64 * b.groups) * 64);
   }
+  // (rows beyond registers: eight workgroups per CU over columns and slabs)
+  if (H > kBwdRegs) {
+    const int64_t across = (H + 2047) / 2048, room = 2048 / across;
+    b.slabs = room < 1 ? 1 : room < 256 ? room : 256;
+    const int64_t most = (rows + 3) / 4;
+    if (b.slabs > most) b.slabs = most;
+    return b;
+  }
   const int waves = b.threads / 64;
   b.slabs = waves >= 8 ? 256 : waves >= 3 ? 512 : 768;
   const int64_t walk = b.side > 1 || rows <= 64 ? 1 : rows <= 256 ? 2 : 4;

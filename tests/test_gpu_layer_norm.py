@@ -120,7 +120,7 @@ def test_empty():
     assert dx.shape == (0, 64) and not bool(dw.any()) and not bool(db.any()) and dw.shape == (64,)
 
 
-@pytest.mark.parametrize("H", [61, 64, 1030, 4096])
+@pytest.mark.parametrize("H", [61, 64, 1030, 4096, 8300])
 def test_nothing_behind_the_outputs_is_written(H):
     d = device()
     x, w, b = make(9, H, 8)
@@ -205,6 +205,18 @@ def test_backward_types(xt, dt, wt):
 def test_backward_row_ends(xt, dt, H):
     # rows that end at each place of a group, a wave and a workgroup
     check_backward(5, H, H, xt, dt)
+
+
+@pytest.mark.parametrize("H", [7, 100, 512, 700, 8192, 9000, 16384, 20000])
+def test_backward_of_one_row(H):
+    # one slab, whose sums are the results
+    check_backward(1, H, H)
+
+
+def test_backward_of_very_long_rows():
+    # few slabs, since the columns fill the machine
+    check_backward(40, 300007, 4)
+    check_backward(1000, 17000, 5, F32, BF16, dres=False)
 
 
 def test_backward_of_many_long_rows():

@@ -157,6 +157,34 @@ def test_captured_graphs_replay_the_eager_results(M):
     assert equal(outs[0], fresh) and not torch.equal(outs[0][5], want[0][5])
 
 
+@pytest.mark.parametrize("M,N,K", [(16, 640, 512), (100, 1000, 528), (300, 4001, 272), (777, 2053, 272), (3000, 700, 4000),
+                                   (2500, 2500, 272), (5000, 3000, 256)])
+def test_captured_products(M, N, K):
+    # every family of the products, with the launch that joins splits of K; one
+    # graph twice in the replays, eager calls of the same shape between them
+    d, g = device(), torch.Generator().manual_seed(M)
+    q = lambda r: torch.randint(0, 0x60, (r, K), generator=g, dtype=torch.uint8).to(d)  # noqa: E731
+    qx, qw, s = q(M), q(N), torch.tensor([0.01], device=d)
+    res, dy = (torch.randn(M, N, generator=g).to(BF16).to(d) for _ in range(2))
+
+    def run():
+        y, pre = fp8.fp8_linear_act(qx, qw, s, s, act=ref.SILU, residual=res, pre=True)
+        return [y, pre, *fp8.fp8_linear_act_backward(dy, pre, ref.SILU)]
+
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        out = run()
+    want = run()
+    for _ in range(3):
+        for t in out:
+            t.fill_(7.0)
+        graph.replay()
+        again = run()
+        torch.cuda.synchronize()
+        assert equal(out, want) and equal(again, want)
+
+
 def test_given_workspaces():
     d = device()
     for M, N, K in ((1, 64, 16384), (3000, 700, 4096), (5, 512, 512)):
