@@ -352,7 +352,7 @@ hipError_t run_act_backward(const uint16_t* dy, const uint16_t* pre, int act, ui
 // blocks and 16 waves (16x32: 5.6), 64x4096x4096 7.3 with 32x32 (64x32 10.3,
 // 32x16 8.2), 256x4096x4096 15.4 with 64x64 (64x32 19.3; 128x128 tiles split
 // four ways over K 23.1), 128x12288x4096 22.0 with 64x96 (64x64 in pairs 24.2),
-// 500x3000x3008 18.6 (24.8).  Above that, up to two workgroups per CU (64x64,
+// 500x3000x3008 18.6 (24.8; but 128x12288x512 10.3, in pairs 9.0).  Above that, up to two workgroups per CU (64x64,
 // two waves): 512x4096x2048 16.1 (128x128 tiles 23.0), 512x4096x12288 55
 // (128x128 split in two 54.7), 777x2053x2064 20.0 (27.1).
 //
@@ -374,7 +374,7 @@ LinearPlan linear_plan(int64_t M, int64_t N, int64_t K) {
   if (M <= 32) return {kRows2x4, 1};
   if (area <= 8) return {kRows4x2, 1};
   if (area <= 16) return {kRows4x4, 1};
-  if (up(M, 64) * up(N, 96) <= kCus) return {kRows4x6, 1};
+  if (K >= 1536 && up(M, 64) * up(N, 96) <= kCus) return {kRows4x6, 1};
   if (M <= 64) return {kRows4x4Pair, 1};
   if (area <= 32) return {kRows4x4Pair, 1};
   auto tiles = [&](int bm, int bn) { return up(M, bm) * up(N, bn); };

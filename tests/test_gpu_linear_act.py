@@ -110,7 +110,7 @@ def reference_on_gpu(t, act):
     (64, 20000, 144), (400, 3000, 1040), (777, 2053, 272), (2500, 2501, 272), (2500, 2500, 256), (3000, 700, 4000),
     (3000, 701, 4096), (1500, 1500, 1504), (700, 5001, 2048), (1319, 3016, 2560), (1319, 3015, 2576), (7278, 290, 9984),
     (578, 7537, 14240), (3989, 3990, 672), (2048, 8192, 1024), (300, 4001, 272), (128, 12288, 144), (64, 24000, 256),
-    (300, 4004, 272)], ids=lambda v: str(v))
+    (300, 4001, 1552), (128, 12288, 1536), (290, 4004, 1680)], ids=lambda v: str(v))
 def test_every_tile(M, N, K):
     i = M + N + K
     act = ref.ACTS[i % 5]
