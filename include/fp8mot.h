@@ -337,8 +337,8 @@ size_t fp8_linear_act_workspace(int64_t M, int64_t N, int64_t K);
  *  - pre: NULL, or BF16 [M, N] that receives bf16_rne(z), which the backward
  *    pass needs.
  *  - y may be the residual itself where the element types agree (the sum is
- *    then added in place); no other overlap of y or pre with an input or
- *    with each other.
+ *    then added in place); any other overlap of y or pre with an input or
+ *    with each other is refused.
  *  - accum as fp8_linear.  Calls of few rows (M <= 64) or few outputs (about
  *    two million and less) are bound by bytes, not by the matrix cores, and
  *    always sum as FP8MOT_ACC_EXACT does.
@@ -367,7 +367,7 @@ size_t fp8_linear_act_backward_workspace(int64_t M, int64_t N);
  * fp8_quant_per_row and fp8_linear_rowwise on the transposed codes.
  * dy, pre, dz: BF16 [M, N]; dbias: FP32 [N]; all 16-byte aligned.  dz or
  * dbias may be NULL (not computed), and with FP8MOT_ACT_NONE pre too.  dz may
- * be dy or pre itself.  relu's slope at 0 is 0.  M == 0 writes dbias = 0.
+ * be dy or pre itself; any other overlap is refused.  relu's slope at 0 is 0.  M == 0 writes dbias = 0.
  * M up to INT32_MAX, N up to 2^26.
  * ws: 16-byte aligned, at least fp8_linear_act_backward_workspace(M, N)
  * bytes; unused where dbias is NULL. */
@@ -389,7 +389,8 @@ int fp8_linear_act_backward(const uint16_t* dy, const uint16_t* pre, int act, ui
  * x: [rows, H] of x_elem (fp8mot_elem); weight, bias: [H] of wb_elem, either
  * may be NULL (ones, zeros); y: [rows, H]; mean, rstd: FP32 [rows] for the
  * backward pass, or NULL.  eps finite and >= 0.  y may be x itself where the
- * element types agree; no other overlap.  H up to 2^26, rows up to INT32_MAX;
+ * element types agree; any other overlap is refused.  H up to 2^26, rows up to
+ * INT32_MAX;
  * x, y, weight, bias 16-byte aligned.  1 / *d_sy has to be finite.  A row that
  * holds a NaN or an infinity, or whose sums leave FP32's range, becomes NaN
  * (or what 1 / sqrt(Inf) = 0 makes of it, where the squares alone overflow). */
@@ -411,8 +412,8 @@ size_t fp8_layer_norm_backward_workspace(int64_t rows, int64_t H);
  * reaches x past the norm (the residual stream's), added before dx is
  * rounded.  dy: of dy_elem; x, dres, dx: of x_elem; weight: [H] of w_elem or
  * NULL (ones); dweight, dbias: FP32 [H], either may be NULL (not computed).
- * dx may be dy or dres itself where the element types agree, or x; no other
- * overlap.  rows == 0 writes dweight = dbias = 0.  Sizes as fp8_layer_norm.
+ * dx may be dy or dres itself where the element types agree, or x; any other
+ * overlap of an output is refused.  rows == 0 writes dweight = dbias = 0.  Sizes as fp8_layer_norm.
  * The sums over rows take an order that depends on (rows, H) only.  All
  * tensors 16-byte aligned but mean and rstd.  ws: 16-byte aligned, at least
  * fp8_layer_norm_backward_workspace(rows, H) bytes; unused where dweight and

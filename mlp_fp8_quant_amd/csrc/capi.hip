@@ -7,6 +7,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "../../include/fp8mot.h"
@@ -114,6 +115,26 @@ constexpr int64_t kMaxColumns = int64_t(1) << 26;
 bool rows_ok(int64_t rows, int64_t cols) {
   return rows >= 0 && cols >= 0 && rows <= INT32_MAX && cols <= kMaxColumns;
 }
+int64_t elem_bytes(int e) { return e == FP8MOT_ELEM_F32 ? 4 : 2; }
+
+// A tensor of a call.  An output must lie apart from every other tensor of the
+// call, but for the inputs that it may be itself: kernels read those before
+// they write the same elements, of the same size.
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+bool apart(Span a, Span b) {
+  if (a.p == nullptr || b.p == nullptr || a.bytes == 0 || b.bytes == 0) return true;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x + (uint64_t)a.bytes <= y || y + (uint64_t)b.bytes <= x;
+}
+bool apart(Span out, std::initializer_list<Span> others) {
+  for (const Span& o : others)
+    if (!apart(out, o)) return false;
+  return true;
+}
+bool same_or_apart(Span out, Span in) { return (out.p == in.p && out.bytes == in.bytes) || apart(out, in); }
 
 }  // namespace
 
@@ -127,7 +148,7 @@ int fp8mot_init(int device) {
 const char* fp8mot_status_string(int status) {
   switch (status) {
     case FP8MOT_OK: return "ok";
-    case FP8MOT_ERR_INVALID_ARG: return "invalid argument (NULL pointer, negative or too large size, K % 16 != 0, bad enum or non-finite constant)";
+    case FP8MOT_ERR_INVALID_ARG: return "invalid argument (NULL pointer, negative or too large size, K % 16 != 0, bad enum, non-finite constant or an output over another tensor)";
     case FP8MOT_ERR_MISALIGNED: return "tensor base pointer not 16-byte aligned";
     case FP8MOT_ERR_SCALE_MISMATCH: return "input scales of a shared-quantization group differ";
     case FP8MOT_ERR_UNSUPPORTED: return "unsupported: NULL scale (dynamic quantization) or non-gfx950 device";
@@ -275,6 +296,15 @@ int fp8_linear_act(const uint8_t* qx, const uint8_t* qw, void* y, int64_t M, int
   if (row_scales && (!aligned16(d_sx) || !aligned16(d_sw))) return FP8MOT_ERR_MISALIGNED;
   const size_t need = linear_act_workspace(M, N, K);
   if (need > 0 && (ws == nullptr || !aligned16(ws) || ws_bytes < need)) return FP8MOT_ERR_WORKSPACE;
+  {
+    const Span sy = {y, M * N * out_bytes(out_kind)}, sp = {pre, M * N * 2};
+    const Span sr = {residual, M * N * elem_bytes(residual_elem)}, sb = {bias, N * elem_bytes(bias_elem)};
+    const Span x = {qx, M * K}, w = {qw, N * K}, px = {d_sx, row_scales ? M * 4 : 4}, pw = {d_sw, row_scales ? N * 4 : 4};
+    const Span scale = {out_kind == FP8MOT_OUT_FP8 ? d_sy : nullptr, 4};
+    if (!apart(sy, {sp, sb, x, w, px, pw, scale}) || !same_or_apart(sy, sr) ||
+        !apart(sp, {sr, sb, x, w, px, pw, scale}))
+      return FP8MOT_ERR_INVALID_ARG;
+  }
   int cus = 0;
   st = current_device(&cus);
   if (st != FP8MOT_OK) return st;
@@ -305,6 +335,9 @@ int fp8_linear_act_backward(const uint16_t* dy, const uint16_t* pre, int act, ui
   const size_t need = dbias != nullptr ? fp8_linear_act_backward_workspace(M, N) : 0;
   if (need > 0 && (ws == nullptr || !aligned16(ws) || ws_bytes < need)) return FP8MOT_ERR_WORKSPACE;
   if (dbias == nullptr && (dz == nullptr || M == 0)) return FP8MOT_OK;
+  const Span sy = {dy, M * N * 2}, sp = {act == FP8MOT_ACT_NONE ? nullptr : pre, M * N * 2}, sz = {dz, M * N * 2};
+  if (!same_or_apart(sz, sy) || !same_or_apart(sz, sp) || !apart({dbias, N * 4}, {sy, sp, sz}))
+    return FP8MOT_ERR_INVALID_ARG;
   int cus = 0;
   int st = current_device(&cus);
   if (st != FP8MOT_OK) return st;
@@ -320,6 +353,15 @@ int fp8_layer_norm(const void* x, int x_elem, const void* weight, const void* bi
   if (rows == 0 || H == 0) return FP8MOT_OK;
   if (x == nullptr || y == nullptr) return FP8MOT_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(y) || !aligned16(weight) || !aligned16(bias)) return FP8MOT_ERR_MISALIGNED;
+  {
+    const Span sx = {x, rows * H * elem_bytes(x_elem)}, sy = {y, rows * H * out_bytes(out_kind)};
+    const Span sw = {weight, H * elem_bytes(wb_elem)}, sb = {bias, H * elem_bytes(wb_elem)};
+    const Span sm = {mean, rows * 4}, sr = {rstd, rows * 4};
+    const Span scale = {out_kind == FP8MOT_OUT_FP8 ? d_sy : nullptr, 4};
+    if (!same_or_apart(sy, sx) || !apart(sy, {sw, sb, sm, sr, scale}) || !apart(sm, {sx, sw, sb, sr, scale}) ||
+        !apart(sr, {sx, sw, sb, scale}))
+      return FP8MOT_ERR_INVALID_ARG;
+  }
   int cus = 0;
   int st = current_device(&cus);
   if (st != FP8MOT_OK) return st;
@@ -354,6 +396,14 @@ int fp8_layer_norm_backward(const void* dy, int dy_elem, const void* x, int x_el
   const size_t need = sums ? fp8_layer_norm_backward_workspace(rows, H) : 0;
   if (need > 0 && (ws == nullptr || !aligned16(ws) || ws_bytes < need)) return FP8MOT_ERR_WORKSPACE;
   if (rows == 0 && !sums) return FP8MOT_OK;
+  {
+    const Span sy = {dy, rows * H * elem_bytes(dy_elem)}, sx = {x, rows * H * elem_bytes(x_elem)};
+    const Span sr = {dres, sx.bytes}, sd = {dx, sx.bytes}, sw = {weight, H * elem_bytes(w_elem)};
+    const Span mu = {mean, rows * 4}, rs = {rstd, rows * 4}, dw = {dweight, H * 4}, db = {dbias, H * 4};
+    if (!same_or_apart(sd, sy) || !same_or_apart(sd, sx) || !same_or_apart(sd, sr) || !apart(sd, {sw, mu, rs, dw, db}) ||
+        !apart(dw, {sy, sx, sr, sw, mu, rs, db}) || !apart(db, {sy, sx, sr, sw, mu, rs}))
+      return FP8MOT_ERR_INVALID_ARG;
+  }
   int cus = 0;
   int st = current_device(&cus);
   if (st != FP8MOT_OK) return st;

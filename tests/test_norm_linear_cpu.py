@@ -105,6 +105,48 @@ def test_norm_backward_refusals(want, args):
     assert norm_backward(**args) == want
 
 
+def at(i, byte=0):
+    return P((i << 20) + byte)             # a tensor of its own, 1 MiB apart
+
+
+@pytest.mark.parametrize("args", [
+    dict(y=1), dict(y=2), dict(y=4), dict(y=5), dict(y=6), dict(pre=1), dict(pre=2), dict(pre=3), dict(pre=4),
+    dict(pre=7), dict(pre=5), dict(y=7, out=2), dict(y=7, out=1, sy=8), dict(y=8, out=1, sy=8), dict(pre=8, out=1, sy=8),
+    dict(y=(7, 16)), dict(res=(3, 48)), dict(pre=(3, 16)), dict(rows=1, y=(4, 0)), dict(bias=(3, 48)),
+    dict(qx=(3, 48)), dict(qw=(3, 48))])
+def test_linear_refuses_overlaps(args):
+    # 1 qx, 2 qw, 3 y, 4 sx, 5 sw, 6 bias, 7 residual, 8 sy, 9 pre; y of 4 x 8 BF16 is 64 bytes
+    full = dict(qx=1, qw=2, y=3, sx=4, sw=5, bias=6, res=7, pre=9)
+    a = {k: v if k in ("out", "rows") else at(*v) if type(v) is tuple else at(v) for k, v in {**full, **args}.items()}
+    assert linear(**a) == INVALID
+
+
+@pytest.mark.parametrize("args", [
+    dict(dz=(1, 16)), dict(dz=(2, 48)), dict(db=1), dict(db=2), dict(db=3), dict(db=(3, 48)), dict(dy=(3, 32))])
+def test_linear_backward_refuses_overlaps(args):
+    full = dict(dy=1, pre=2, dz=3, db=4)
+    assert linear_backward(**{k: at(*v) if type(v) is tuple else at(v) for k, v in {**full, **args}.items()}) == INVALID
+
+
+@pytest.mark.parametrize("args", [
+    dict(y=2), dict(y=3), dict(y=4), dict(y=5), dict(y=(1, 16)), dict(y=1, out=2), dict(y=1, xe=1), dict(mean=1),
+    dict(mean=5), dict(mean=2), dict(rstd=6), dict(rstd=3), dict(y=7, out=1, sy=7), dict(mean=7, out=1, sy=7)])
+def test_norm_refuses_overlaps(args):
+    full = dict(x=1, w=2, b=3, mean=4, rstd=5, y=6)
+    a = {k: v if k in ("out", "xe") else at(*v) if type(v) is tuple else at(v) for k, v in {**full, **args}.items()}
+    assert norm(**a) == INVALID
+
+
+@pytest.mark.parametrize("args", [
+    dict(dx=3), dict(dx=4), dict(dx=5), dict(dx=8), dict(dx=(1, 16)), dict(dx=(2, 16)), dict(dx=(6, 16)), dict(dx=1, de=1),
+    dict(dw=1), dict(dw=2), dict(dw=3), dict(dw=4), dict(dw=6), dict(dw=9), dict(db=7), dict(db=5), dict(db=2)])
+def test_norm_backward_refuses_overlaps(args):
+    # 1 dy, 2 x, 3 weight, 4 mean, 5 rstd, 6 dres, 7 dx, 8 dweight, 9 dbias
+    full = dict(dy=1, x=2, w=3, mean=4, rstd=5, dres=6, dx=7, dw=8, db=9)
+    a = {k: v if k == "de" else at(*v) if type(v) is tuple else at(v) for k, v in {**full, **args}.items()}
+    assert norm_backward(**a) == INVALID
+
+
 def test_backward_workspaces():
     lib, huge = L.lib(), 1 << 62
     for f in (lib.fp8_linear_act_backward_workspace, lib.fp8_layer_norm_backward_workspace):
