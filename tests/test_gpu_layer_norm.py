@@ -185,7 +185,7 @@ def test_backward_widths(H):
     check_backward(33, H, H + 1, F32, F32, BF16, dres=False)
 
 
-@pytest.mark.parametrize("rows", [1, 2, 31, 32, 100, 513, 1500, 4096, 6000])
+@pytest.mark.parametrize("rows", [1, 2, 3, 4, 5, 16, 17, 31, 32, 100, 513, 1500, 4096, 6000])
 @pytest.mark.parametrize("H", [40, 512, 1027])
 def test_backward_rows(rows, H):
     check_backward(rows, H, rows, dres=rows % 2 == 0)
