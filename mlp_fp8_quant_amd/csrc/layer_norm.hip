@@ -45,6 +45,18 @@ __device__ __forceinline__ float sum8(const float* f) {
                    __fadd_rn(__fadd_rn(f[4], f[5]), __fadd_rn(f[6], f[7])));
 }
 
+// A sum that keeps what its additions round off (of many terms in one thread,
+// where the roundings of a plain sum would add up: 2e-5 of rstd at 2^26
+// columns).
+struct LongSum {
+  float s = 0.0f, lost = 0.0f;
+  __device__ __forceinline__ void add(float v) {
+    const float y = __fadd_rn(v, -lost), t = __fadd_rn(s, y);
+    lost = __fadd_rn(__fadd_rn(t, -s), -y);
+    s = t;
+  }
+};
+
 __device__ __forceinline__ void emit8(const LayerNormArgs& g, int64_t base, int64_t i, float rs, float* y) {
   if (g.out_kind == 0) {
     store8_bf16(static_cast<uint16_t*>(g.y) + base, i, g.H, y);
@@ -153,24 +165,24 @@ __global__ __launch_bounds__(1024) void layer_norm_long_kernel(LayerNormArgs g) 
   for (int64_t r = blockIdx.x; r < g.rows; r += gridDim.x) {
   const int64_t base = r * g.H;
   const void* xr = static_cast<const uint8_t*>(g.x) + base * (F32 ? 4 : 2);
-  float s = 0.0f;
+  LongSum s, v;
   for (int64_t i = 8 * (int64_t)threadIdx.x; i < g.H; i += 8 * 1024) {
     float f[8];
     values8<F32>(load8<F32>(xr, i, g.H), f);
-    s = __fadd_rn(s, sum8(f));
+    s.add(sum8(f));
   }
-  const float mean = __fmul_rn(row_sum<0>(s, red[0]), inv_h);
-  float v = 0.0f;
+  const float mean = __fmul_rn(row_sum<0>(s.s, red[0]), inv_h);
   for (int64_t i = 8 * (int64_t)threadIdx.x; i < g.H; i += 8 * 1024) {
     float f[8];
     values8<F32>(load8<F32>(xr, i, g.H), f);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const float d = i + k < g.H ? __fadd_rn(f[k], -mean) : 0.0f;
-      v = __builtin_fmaf(d, d, v);
+      f[k] = __fmul_rn(d, d);
     }
+    v.add(sum8(f));
   }
-  const float var = __fmul_rn(row_sum<0>(v, red[1]), inv_h);
+  const float var = __fmul_rn(row_sum<0>(v.s, red[1]), inv_h);
   const float rstd = 1.0f / __fsqrt_rn(__fadd_rn(var, g.eps));
   if (threadIdx.x == 0) {
     if (g.mean != nullptr) g.mean[r] = mean;
@@ -454,16 +466,16 @@ __global__ __launch_bounds__(1024) void layer_norm_dx_long_kernel(LayerNormBwdAr
       if (g.w != nullptr) gw[k] = __fmul_rn(gw[k], w[k]);
     }
   };
-  float s1 = 0.0f, s2 = 0.0f, xh[8], gw[8];
+  LongSum s1, s2;
+  float xh[8], gw[8];
   for (int64_t i = 8 * (int64_t)threadIdx.x; i < g.H; i += 8 * 1024) {
     row8(i, xh, gw);
+    s1.add(sum8(gw));
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      s1 = __fadd_rn(s1, gw[k]);
-      s2 = __builtin_fmaf(gw[k], xh[k], s2);
-    }
+    for (int k = 0; k < 8; ++k) xh[k] = __fmul_rn(gw[k], xh[k]);
+    s2.add(sum8(xh));
   }
-  const float c1 = __fmul_rn(row_sum<0>(s1, red[0]), inv_h), c2 = __fmul_rn(row_sum<0>(s2, red[1]), inv_h);
+  const float c1 = __fmul_rn(row_sum<0>(s1.s, red[0]), inv_h), c2 = __fmul_rn(row_sum<0>(s2.s, red[1]), inv_h);
   for (int64_t i = 8 * (int64_t)threadIdx.x; i < g.H; i += 8 * 1024) {
     row8(i, xh, gw);
     float y[8], res[8];

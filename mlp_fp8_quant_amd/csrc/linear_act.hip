@@ -236,10 +236,10 @@ template <bool VEC>
 __global__ __launch_bounds__(256) void linear_join_kernel(LinearActArgs g, const float* __restrict__ part,
                                                           int splits) {
   const int N = (int)g.N, per_row = (N + 3) / 4;
-  const int64_t m0 = (int64_t)blockIdx.y * kJoinRows;
+  const int64_t m0 = (int64_t)blockIdx.x * kJoinRows;
   const int rows = g.M - m0 < kJoinRows ? (int)(g.M - m0) : kJoinRows;
   const linear::Epilogue e = linear::open_epilogue(g, m0);
-  for (int i = (int)blockIdx.x * 256 + (int)threadIdx.x; i < rows * per_row; i += (int)gridDim.x * 256) {
+  for (int i = (int)blockIdx.y * 256 + (int)threadIdx.x; i < rows * per_row; i += (int)gridDim.y * 256) {
     const int row = i / per_row, n = (i - row * per_row) * 4, nv = N - n;
     linear::Operands<1> op;
     linear::load_operands<1, VEC>(g, e, m0, row, 1, n, nv, &op);
@@ -424,8 +424,9 @@ hipError_t launch_linear_act(const LinearActArgs& g, int accum, float* ws, int n
   }
   const hipError_t e = launch_linear_tile(g, p, accum, ws, num_cus, stream);
   if (e != hipSuccess || p.splits == 1) return e;
-  const int64_t blocks = (kJoinRows * ((g.N + 3) / 4) + 255) / 256;
-  const dim3 grid((unsigned)blocks, (unsigned)((g.M + kJoinRows - 1) / kJoinRows));
+  // rows along x, which takes any number of them
+  const int64_t across = (kJoinRows * ((g.N + 3) / 4) + 255) / 256;
+  const dim3 grid((unsigned)((g.M + kJoinRows - 1) / kJoinRows), (unsigned)(across < 65535 ? across : 65535));
   if ((g.N & 3) == 0)
     hipLaunchKernelGGL(linear_join_kernel<true>, grid, dim3(256), 0, stream, g, ws, p.splits);
   else

@@ -219,6 +219,32 @@ def test_backward_of_very_long_rows():
     check_backward(1000, 17000, 5, F32, BF16, dres=False)
 
 
+def test_widest_rows():
+    # the widest row that the calls take, forward and backward
+    d, H = device(), 1 << 26
+    x = torch.randn(2, H, device=d).to(BF16)
+    w = torch.randn(H, device=d).to(BF16)
+    y, mean, rstd = fp8.fp8_layer_norm(x, w, None, EPS, out_kind=fp8.OUT_F32, stats=True)
+    xd = x.double()
+    m64 = xd.mean(1)
+    r64 = ((xd - m64[:, None]).square().mean(1) + EPS).rsqrt()
+    # a thread's sum of groups of eight keeps what its additions round off, so
+    # a sum is within 3 (group) + 2 + 10 (lanes and waves) half steps of the sum of
+    # its terms' sizes: 16 of 2^-24, and the squares' a few more
+    assert bool(((mean - m64).abs() < 2.0 ** -20).all()) and bool(((rstd / r64 - 1).abs() < 2.0 ** -16).all())
+    dx, dw, db = fp8.fp8_layer_norm_backward(x, x, w, mean, rstd)
+    at = torch.tensor([0, 1, 8191, 8192, 1 << 20, H // 2, H - 9, H - 1], device=d)
+    xh = (xd[:, at] - mean.double()[:, None]) * rstd.double()[:, None]
+    assert torch.allclose(y[:, at].double(), xh * w[at].double(), rtol=2.0 ** -21, atol=2.0 ** -21)
+    assert torch.allclose(dw[at].double(), (xd[:, at] * xh).sum(0), rtol=2.0 ** -20, atol=2.0 ** -20)
+    assert torch.allclose(db[at].double(), xd[:, at].sum(0), rtol=2.0 ** -20, atol=2.0 ** -20)
+    xa = (xd - mean.double()[:, None]) * rstd.double()[:, None]
+    g = xd * w.double()
+    want = (rstd.double()[:, None] * (g - g.mean(1, keepdim=True) - xa * (g * xa).mean(1, keepdim=True)))[:, at]
+    # dx rounds to BF16; its two means are within 2^-19 of their terms' size
+    assert torch.allclose(dx[:, at].double(), want, rtol=2.0 ** -8, atol=2.0 ** -8)
+
+
 def test_backward_of_many_long_rows():
     check_backward(1100, 8200, 5)
     check_backward(600, 16384, 6, F32, F32, dres=False)

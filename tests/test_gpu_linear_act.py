@@ -285,6 +285,36 @@ def test_outputs_past_32_bit_offsets():
         ref.check(y[r:r + 1], z64, err)
 
 
+def test_joined_splits_of_very_many_rows():
+    # K split over workgroups with more 16-row blocks than a grid's second
+    # dimension holds: the first, middle and last rows against the reference
+    d = device()
+    M, N, K = 1048832, 1, 65536
+    assert fp8.fp8_linear_act_workspace(M, N, K) > 0
+    t = make(8, N, K, 9, BF16)
+    qx = torch.zeros(M, K, dtype=torch.uint8, device=d)
+    at = [0, 1, 2, M // 2, M - 4, M - 3, M - 2, M - 1]
+    for i, r in enumerate(at):
+        qx[r] = t["qx"][i]
+    y = fp8.fp8_linear_act(qx, t["qw"], t["sx"], t["sw"], t["bias"], ref.SILU, out_kind=fp8.OUT_F32)
+    y64, _, err, _ = ref.linear_act(t["qx"], t["qw"], t["sx"], t["sw"], t["bias"], ref.SILU, None)
+    ref.check(y[at], y64, err)
+    rest = torch.ones(M, dtype=torch.bool, device=d)
+    rest[at] = False
+    assert bool((y[rest] == y[3000]).all())
+    del qx
+    torch.cuda.empty_cache()
+
+
+def test_longest_rows():
+    # the longest K that the tile windows hold
+    for M, N, K in ((3, 40, 8388560), (70, 130, 1048576)):
+        t = make(M, N, K, 10, BF16, F32)
+        y = fp8.fp8_linear_act(t["qx"], t["qw"], t["sx"], t["sw"], t["bias"], ref.NONE, t["residual"], fp8.OUT_F32)
+        y64, _, err, _ = reference_on_gpu(t, ref.NONE)
+        ref.check(y, y64, err)
+
+
 # ---------------------------------------------------------------------------
 # Backward pass
 # ---------------------------------------------------------------------------
