@@ -12,6 +12,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "device_common.h"
 #include "kernels.h"
 #include "rowwise.h"
@@ -241,21 +243,22 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(LayerNormBwdA
   Raw8<XF> x[U], rs[U];
   Raw8<DF> d[U];
   float mean = 0.0f, rstd = 0.0f;
-  auto load8_of = [&](auto& to, const void* from, int64_t base, int64_t i) {
+  // last: what a group holds past the row's end, its last element or zeros
+  auto load8_of = [&](auto& to, const void* from, int64_t base, int64_t i, auto last) {
     constexpr bool F = sizeof(to) == 32;
     const void* row = static_cast<const uint8_t*>(from) + base * (F ? 4 : 2);
-    to = TC == 16 || FULL ? load8<F, FULL>(row, i, g.H) : load8_ahead<F>(row, i, g.H);
+    to = TC == 16 || FULL ? load8<F, FULL, decltype(last)::value>(row, i, g.H) : load8_ahead<F>(row, i, g.H);
   };
   auto load_res = [&](int64_t r) {
     if (g.dres == nullptr) return;
 #pragma unroll
-    for (int j = 0; j < U; ++j) load8_of(rs[j], g.dres, r * g.H, 8 * (int64_t)(j * T + t));
+    for (int j = 0; j < U; ++j) load8_of(rs[j], g.dres, r * g.H, 8 * (int64_t)(j * T + t), std::false_type{});
   };
   auto load = [&](int64_t r) {
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      load8_of(x[j], g.x, r * g.H, 8 * (int64_t)(j * T + t));
-      load8_of(d[j], g.dy, r * g.H, 8 * (int64_t)(j * T + t));
+      load8_of(x[j], g.x, r * g.H, 8 * (int64_t)(j * T + t), std::true_type{});
+      load8_of(d[j], g.dy, r * g.H, 8 * (int64_t)(j * T + t), std::false_type{});
     }
     mean = g.mean[r];
     rstd = g.rstd[r];
@@ -287,14 +290,16 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(LayerNormBwdA
       float dy[8];
       const int64_t i = 8 * (int64_t)(j * T + t);
       if constexpr (TC != 16 && !FULL) {
-        shift8<XF>(x[j], i, g.H);
+        shift8<XF, true>(x[j], i, g.H);
         shift8<DF>(d[j], i, g.H);
         if (!AGAIN && g.dres != nullptr) shift8<XF>(rs[j], i, g.H);
       }
       x_now[j] = x[j];
       d_now[j] = d[j];
       if (!AGAIN && g.dres != nullptr) values8<XF>(rs[j], res[j]);
-      // columns past H: x and dy are 0 there, and add nothing to the row's sums
+      // columns past H: dy is 0 there and xh the row's last, as finite as that
+      // (of x = 0, -mean rstd could overflow and 0 Inf reach the sums), so they
+      // add nothing to the row's sums
       group(x[j], d[j], mean_r, rstd_r, j, dy, xh[j], gw[j]);
 #pragma unroll
       for (int k = 0; k < 8; ++k) s1 = __fadd_rn(s1, gw[j][k]);

@@ -24,9 +24,9 @@ struct Raw8 {
   u4 q[F32 ? 2 : 1];
 };
 
-// Elements i .. i + 7 of a row of n; zeros past its end.  WHOLE: the row does
-// not end before them.
-template <bool F32, bool WHOLE = false>
+// Elements i .. i + 7 of a row of n; past its end zeros, or with LAST the row's
+// last element again.  WHOLE: the row does not end before them.
+template <bool F32, bool WHOLE = false, bool LAST = false>
 __device__ __forceinline__ Raw8<F32> load8(const void* row, int64_t i, int64_t n) {
   Raw8<F32> r;
   if (WHOLE || i + 8 <= n) {
@@ -36,6 +36,19 @@ __device__ __forceinline__ Raw8<F32> load8(const void* row, int64_t i, int64_t n
       r.q[1] = __builtin_bit_cast(u4, (f4)(*reinterpret_cast<const f4a4*>(p + 4)));
     } else {
       r.q[0] = *reinterpret_cast<const u4a2*>(static_cast<const uint16_t*>(row) + i);
+    }
+  } else if constexpr (LAST) {
+    auto at = [&](int k) { return i + k < n ? i + k : n - 1; };
+#pragma unroll
+    for (int k = 0; k < (F32 ? 8 : 4); ++k) {
+      uint32_t v;
+      if constexpr (F32) {
+        v = static_cast<const uint32_t*>(row)[at(k)];
+      } else {
+        v = static_cast<const uint16_t*>(row)[at(2 * k)];
+        v |= (uint32_t) static_cast<const uint16_t*>(row)[at(2 * k + 1)] << 16;
+      }
+      r.q[k >> 2][k & 3] = v;
     }
   } else {
 #pragma unroll
@@ -56,12 +69,13 @@ __device__ __forceinline__ Raw8<F32> load8(const void* row, int64_t i, int64_t n
 // The same of a row of n >= 8 without a branch: a group that crosses the row's
 // end is the row's last eight elements, which shift8 puts in their places once
 // they have arrived.  (load8's end is loads that wait for one another: a
-// workgroup whose last wave takes it waits for that wave in every row.)
+// workgroup whose last wave takes it waits for that wave in every row.)  Past
+// the row's end shift8 puts zeros, or with LAST the row's last element.
 template <bool F32>
 __device__ __forceinline__ Raw8<F32> load8_ahead(const void* row, int64_t i, int64_t n) {
   return load8<F32, true>(row, i + 8 <= n ? i : n - 8, n);
 }
-template <bool F32>
+template <bool F32, bool LAST = false>
 __device__ __forceinline__ void shift8(Raw8<F32>& r, int64_t i, int64_t n) {
   if (i + 8 <= n) return;
   const int s = i >= n ? 8 : (int)(i + 8 - n);   // elements past the end
@@ -69,11 +83,12 @@ __device__ __forceinline__ void shift8(Raw8<F32>& r, int64_t i, int64_t n) {
     uint32_t v[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = r.q[k >> 2][k & 3];
+    const uint32_t fill = LAST ? v[7] : 0;
 #pragma unroll
     for (int d = 8; d > 0; d >>= 1)
       if (s & d) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = k + d < 8 ? v[k + d] : 0;
+        for (int k = 0; k < 8; ++k) v[k] = k + d < 8 ? v[k + d] : fill;
       }
 #pragma unroll
     for (int k = 0; k < 8; ++k) r.q[k >> 2][k & 3] = v[k];
@@ -81,15 +96,16 @@ __device__ __forceinline__ void shift8(Raw8<F32>& r, int64_t i, int64_t n) {
     uint32_t v[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = r.q[0][k];
+    const uint32_t fill = LAST ? v[3] >> 16 | (v[3] & 0xFFFF0000u) : 0;
 #pragma unroll
     for (int d = 4; d > 0; d >>= 1)
       if (s & (2 * d)) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = k + d < 4 ? v[k + d] : 0;
+        for (int k = 0; k < 4; ++k) v[k] = k + d < 4 ? v[k + d] : fill;
       }
     if (s & 1) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = v[k] >> 16 | (k < 3 ? v[k + 1] << 16 : 0);
+      for (int k = 0; k < 4; ++k) v[k] = v[k] >> 16 | (k < 3 ? v[k + 1] : fill) << 16;
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) r.q[0][k] = v[k];
