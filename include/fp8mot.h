@@ -112,7 +112,10 @@ typedef enum {
 } fp8mot_elem;
 
 /* Activation of fp8_linear_act, evaluated in FP32.  At z = -Inf gelu,
- * gelu_tanh and silu give the NaN of -Inf * 0; a NaN stays a NaN. */
+ * gelu_tanh and silu give the NaN of -Inf * 0; a NaN stays a NaN.  gelu's
+ * Phi(-a) is within (1.25 a^2 + 14) 2^-24 of its own size while it is a normal
+ * FP32 number (a < 12.9); the sigma of the other two is within about |x| 2^-23
+ * of its size at an argument x < 0. */
 typedef enum {
   FP8MOT_ACT_NONE = 0,      /* z */
   FP8MOT_ACT_RELU = 1,      /* max(z, 0) */
