@@ -6,9 +6,12 @@
 //   g = dy w:  dx = rstd (g - sum g / H - xh sum(g xh) / H) + dres
 //   dw = sum_rows dy xh,  db = sum_rows dy
 //
-// All sums are FP32; the variance is taken about the mean (not from the
-// squares' mean, which cancels where the mean is large).  Bound by memory: a
-// row is read once and kept in registers over its sums.
+// All sums are FP32.  The variance is taken about the mean (not from the
+// squares' mean, which cancels where the mean is large).  A first mean is off by
+// some 2^-24 of itself (an ulp at 1000 is 6e-5, which the rstd of a constant
+// row, 316, makes 0.02): where the mean is far above the spread, the
+// differences from it are summed too, and that sum corrects mean, variance and
+// xh.  Bound by memory: a row is read once and kept in registers over its sums.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -39,6 +42,19 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
     for (int w = 1; w < waves; ++w) v = __fadd_rn(v, red[w]);
   }
   return v;
+}
+
+// Whether a row's mean needs the correction, from the mean square d2 of the
+// differences from it: below four standard deviations some 2^-24 of it is less
+// than the other roundings of (x - mean) rstd.  Equal in the threads that share a
+// row.  (A third sum in every row costs 2 to 7%: 16384x5120 BF16 -> E4M3 60.3
+// -> 64.4 us.)
+__device__ __forceinline__ bool off_centre(float mean, float d2, float eps) {
+  return __fmul_rn(mean, mean) > 16.0f * __fadd_rn(d2, eps);
+}
+// The variance about mean + off (0 where roundings would make it negative).
+__device__ __forceinline__ float centred(float d2, float off) {
+  return __builtin_fmaxf(__builtin_fmaf(-off, off, d2), 0.0f);
 }
 
 // A tree over eight values: fewer roundings in a row than one after another.
@@ -92,7 +108,7 @@ __device__ __forceinline__ void affine8(const LayerNormArgs& g, int64_t i, float
 // TB/s, by the arithmetic between the row's sums (loads two rows ahead: slower).
 template <bool F32, int TC, int U, bool FULL>
 __global__ __launch_bounds__(TC > 0 ? 256 : 1024) void layer_norm_kernel(LayerNormArgs g) {
-  __shared__ float red[2][16];
+  __shared__ float red[3][16];
   constexpr int RPB = TC > 0 ? 256 / (TC > 0 ? TC : 1) : 1;
   constexpr bool KEEP = U <= 3;   // more would not fit beside the row
   const int T = TC > 0 ? TC : blockDim.x, t = TC > 0 ? threadIdx.x % T : threadIdx.x;
@@ -113,7 +129,7 @@ __global__ __launch_bounds__(TC > 0 ? 256 : 1024) void layer_norm_kernel(LayerNo
     for (int j = 0; j < U; ++j) affine8(g, 8 * (int64_t)(j * T + t), w[j], b[j]);
   }
   const float rs = g.out_kind == 1 ? 1.0f / *g.sy : 0.0f;
-  // (the two sums' LDS takes turns, so a row's never meets the row before)
+  // (the sums' LDS takes turns, so a row's never meets the row before)
   for (; r < g.rows; r += step) {
     float x[U][8];
     float s = 0.0f;
@@ -123,7 +139,7 @@ __global__ __launch_bounds__(TC > 0 ? 256 : 1024) void layer_norm_kernel(LayerNo
       s = __fadd_rn(s, sum8(x[j]));
     }
     if (r + step < g.rows) load(r + step);
-    const float mean = __fmul_rn(row_sum<TC>(s, red[0]), inv_h);
+    float mean = __fmul_rn(row_sum<TC>(s, red[0]), inv_h);
     float v = 0.0f;
 #pragma unroll
     for (int j = 0; j < U; ++j) {
@@ -139,7 +155,28 @@ __global__ __launch_bounds__(TC > 0 ? 256 : 1024) void layer_norm_kernel(LayerNo
           if (i + k < g.H) v = __builtin_fmaf(x[j][k], x[j][k], v);
       }
     }
-    const float var = __fmul_rn(row_sum<TC>(v, red[1]), inv_h);
+    float var = __fmul_rn(row_sum<TC>(v, red[1]), inv_h);
+    if (__builtin_expect(off_centre(mean, var, g.eps), 0)) {
+      float c = 0.0f;
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const int64_t i = 8 * (int64_t)(j * T + t);
+        if (FULL || i + 8 <= g.H) {
+          c = __fadd_rn(c, sum8(x[j]));
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (i + k < g.H) c = __fadd_rn(c, x[j][k]);
+        }
+      }
+      const float off = __fmul_rn(row_sum<TC>(c, red[2]), inv_h);
+      var = centred(var, off);
+      mean = __fadd_rn(mean, off);
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[j][k] = __fadd_rn(x[j][k], -off);
+    }
     const float rstd = 1.0f / __fsqrt_rn(__fadd_rn(var, g.eps));
     if (t == 0) {
       if (g.mean != nullptr) g.mean[r] = mean;
@@ -159,10 +196,11 @@ __global__ __launch_bounds__(TC > 0 ? 256 : 1024) void layer_norm_kernel(LayerNo
   }
 }
 
-// Rows too long for registers: read three times, from cache after the first.
+// Rows too long for registers: read three times (four where the
+// mean is corrected), from cache after the first.
 template <bool F32>
 __global__ __launch_bounds__(1024) void layer_norm_long_kernel(LayerNormArgs g) {
-  __shared__ float red[2][16];
+  __shared__ float red[3][16];
   const float inv_h = 1.0f / (float)g.H;
   for (int64_t r = blockIdx.x; r < g.rows; r += gridDim.x) {
   const int64_t base = r * g.H;
@@ -184,10 +222,22 @@ __global__ __launch_bounds__(1024) void layer_norm_long_kernel(LayerNormArgs g) 
     }
     v.add(sum8(f));
   }
-  const float var = __fmul_rn(row_sum<0>(v.s, red[1]), inv_h);
+  float var = __fmul_rn(row_sum<0>(v.s, red[1]), inv_h), off = 0.0f;
+  if (off_centre(mean, var, g.eps)) {
+    LongSum c;
+    for (int64_t i = 8 * (int64_t)threadIdx.x; i < g.H; i += 8 * 1024) {
+      float f[8];
+      values8<F32>(load8<F32>(xr, i, g.H), f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] = i + k < g.H ? __fadd_rn(f[k], -mean) : 0.0f;
+      c.add(sum8(f));
+    }
+    off = __fmul_rn(row_sum<0>(c.s, red[2]), inv_h);
+    var = centred(var, off);
+  }
   const float rstd = 1.0f / __fsqrt_rn(__fadd_rn(var, g.eps));
   if (threadIdx.x == 0) {
-    if (g.mean != nullptr) g.mean[r] = mean;
+    if (g.mean != nullptr) g.mean[r] = __fadd_rn(mean, off);
     if (g.rstd != nullptr) g.rstd[r] = rstd;
   }
   const float rs = g.out_kind == 1 ? 1.0f / *g.sy : 0.0f;
@@ -197,7 +247,7 @@ __global__ __launch_bounds__(1024) void layer_norm_long_kernel(LayerNormArgs g) 
     float w[8], b[8];
     affine8(g, i, w, b);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = __builtin_fmaf(__fmul_rn(__fadd_rn(f[k], -mean), rstd), w[k], b[k]);
+    for (int k = 0; k < 8; ++k) f[k] = __builtin_fmaf(__fmul_rn(__fadd_rn(__fadd_rn(f[k], -mean), -off), rstd), w[k], b[k]);
     emit8(g, base, i, rs, f);
   }
   }

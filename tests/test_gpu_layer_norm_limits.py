@@ -1,6 +1,7 @@
 """GPU: the layer norm and its backward pass where range and rounding bite:
-backward passes whose statistics leave FP32's range in columns past the row's
-end.  References are 64-bit, from the formulas."""
+rows whose mean is far above their spread, backward passes whose statistics
+leave FP32's range in columns past the row's end.  References are 64-bit, from
+the formulas."""
 
 import pytest
 import torch
@@ -12,6 +13,81 @@ from gpu_util import device
 
 pytestmark = pytest.mark.gpu
 BF16, F32 = torch.bfloat16, torch.float32
+U = ref.U
+
+
+# ---------------------------------------------------------------------------
+# Means far above the spread
+# ---------------------------------------------------------------------------
+
+# (rows, H): each kernel of the forward pass, whole and ragged rows: 16 and 64
+# threads, one to four groups of eight per thread, three reads of the row
+SHAPES = [(5, 7), (700, 96), (700, 128), (5, 300), (700, 512), (9, 1027), (700, 1000), (700, 2048), (600, 4096),
+          (600, 4104), (700, 5120), (600, 6144), (600, 8192), (600, 9001), (550, 12288), (7, 5120), (7, 16384),
+          (600, 16000), (6, 20000), (6, 32768), (5, 40001)]
+# additions one after another in any of a row's sums: 32 of a thread's, four
+# inside 16 lanes, two over the wave, 15 over the waves, and the products
+DEPTH = 60 * U
+
+
+def corrected_errors(x):
+    """Bounds for a row whose mean is taken twice: first a sum of x, off by
+    e0, then the mean of the differences from it, which corrects mean and
+    variance.  Only the differences' roundings remain: of mean x as xh uses it
+    (absolute), and of the variance (absolute)."""
+    mean = x.mean(dim=-1, keepdim=True)
+    spread = (x - mean).abs().mean(dim=-1)
+    e0 = DEPTH * x.abs().mean(dim=-1)
+    e = DEPTH * (spread + e0)
+    var = (x - mean).square().mean(dim=-1)
+    return e, (var + e0 ** 2) * DEPTH + 2 * e0 * e
+
+
+def check_corrected(x, eps=1e-5):
+    y, mean, rstd = fp8.fp8_layer_norm(x, None, None, eps, fp8.OUT_F32, stats=True)
+    x64 = x.cpu().double()
+    e, e_var = corrected_errors(x64)
+    mean64 = x64.mean(dim=-1)
+    d64 = x64 - mean64[:, None]
+    var64 = d64.square().mean(dim=-1)
+    rstd64 = 1 / torch.sqrt(var64 + eps)
+    # the square root's slope: rstd moves by half the variance's relative error
+    # (e_var is far below eps here), and rounds three times
+    e_rstd = rstd64 * (0.6 * e_var / (var64 + eps) + 4 * U)
+    xh64 = d64 * rstd64[:, None]
+    err = (e * rstd64)[:, None] + d64.abs() * e_rstd[:, None] + 4 * U * xh64.abs()
+    for got, want, tol, what in ((mean, mean64, e + mean64.abs() * U, "mean"), (rstd, rstd64, e_rstd, "rstd"),
+                                 (y, xh64, err, "y")):
+        off = (got.cpu().double() - want).abs()
+        assert bool((off <= tol).all()), f"{what}: {(off / tol).max().item():.3g} of the bound, off by {off.max():.3g}"
+
+
+@pytest.mark.parametrize("rows,H", SHAPES)
+def test_norm_of_rows_around_a_large_mean(rows, H):
+    g = torch.Generator().manual_seed(H)
+    centre = 500 + 1000 * torch.rand(rows, 1, generator=g)
+    x = centre + 0.1 * torch.randn(rows, H, generator=g)
+    check_corrected(x.to(device()))
+    check_corrected((-3.0 + 0.05 * torch.randn(rows, H, generator=g)).to(BF16).to(device()))
+
+
+@pytest.mark.parametrize("rows,H", SHAPES)
+def test_norm_of_constant_rows(rows, H):
+    g = torch.Generator().manual_seed(H + 1)
+    for t in (F32, BF16):
+        x = (500 + 1000 * torch.rand(rows, 1, generator=g)).expand(rows, H).contiguous().to(t).to(device())
+        check_corrected(x)
+        _, mean, rstd = fp8.fp8_layer_norm(x, stats=True)
+        # what the backward pass makes of these statistics
+        assert torch.equal(mean, x[:, 0].float())
+
+
+def test_norm_of_constant_rows_with_tiny_eps():
+    # the variance that the roundings leave must not turn negative
+    for H in (96, 1027, 5120, 40001):
+        x = torch.full((600, H), 777.7, device=device())
+        y, mean, rstd = fp8.fp8_layer_norm(x, None, None, 1e-20, fp8.OUT_F32, stats=True)
+        assert bool(torch.isfinite(rstd).all()) and torch.equal(mean, x[:, 0])
 
 
 # ---------------------------------------------------------------------------
