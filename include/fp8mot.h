@@ -347,7 +347,8 @@ size_t fp8_linear_act_workspace(int64_t M, int64_t N, int64_t K);
  *    always sum as FP8MOT_ACC_EXACT does.
  *  - ws: 16-byte aligned device workspace of at least
  *    fp8_linear_act_workspace(M, N, K) bytes (may be NULL where that is 0).
- *    Calls that may overlap need workspaces of their own.
+ *    Calls that may run at the same time need workspaces of their own; one
+ *    that lies over another tensor of the call is refused.
  * K == 0 gives act(bias) + residual.  The order of the FP32 sum depends on
  * (M, N, K, accum) only; it is not fp8_linear's.  qx, qw, y, bias, residual,
  * pre 16-byte aligned; row scales too.  M, N, K as in fp8_linear. */
@@ -373,7 +374,7 @@ size_t fp8_linear_act_backward_workspace(int64_t M, int64_t N);
  * be dy or pre itself; any other overlap is refused.  relu's slope at 0 is 0.  M == 0 writes dbias = 0.
  * M up to INT32_MAX, N up to 2^26.
  * ws: 16-byte aligned, at least fp8_linear_act_backward_workspace(M, N)
- * bytes; unused where dbias is NULL. */
+ * bytes, apart from every tensor of the call; unused where dbias is NULL. */
 int fp8_linear_act_backward(const uint16_t* dy, const uint16_t* pre, int act, uint16_t* dz,
                             float* dbias, int64_t M, int64_t N, void* ws, size_t ws_bytes,
                             hipStream_t stream);
@@ -419,8 +420,8 @@ size_t fp8_layer_norm_backward_workspace(int64_t rows, int64_t H);
  * overlap of an output is refused.  rows == 0 writes dweight = dbias = 0.  Sizes as fp8_layer_norm.
  * The sums over rows take an order that depends on (rows, H) only.  All
  * tensors 16-byte aligned but mean and rstd.  ws: 16-byte aligned, at least
- * fp8_layer_norm_backward_workspace(rows, H) bytes; unused where dweight and
- * dbias are NULL. */
+ * fp8_layer_norm_backward_workspace(rows, H) bytes, apart from every tensor of
+ * the call; unused where dweight and dbias are NULL. */
 int fp8_layer_norm_backward(const void* dy, int dy_elem, const void* x, int x_elem,
                             const void* weight, int w_elem, const float* mean,
                             const float* rstd, const void* dres, void* dx, float* dweight,

@@ -119,7 +119,8 @@ int64_t elem_bytes(int e) { return e == FP8MOT_ELEM_F32 ? 4 : 2; }
 
 // A tensor of a call.  An output must lie apart from every other tensor of the
 // call, but for the inputs that it may be itself: kernels read those before
-// they write the same elements, of the same size.
+// they write the same elements, of the same size.  What a call uses of its
+// workspace must lie apart from all of them.
 struct Span {
   const void* p;
   int64_t bytes;
@@ -302,7 +303,8 @@ int fp8_linear_act(const uint8_t* qx, const uint8_t* qw, void* y, int64_t M, int
     const Span x = {qx, M * K}, w = {qw, N * K}, px = {d_sx, row_scales ? M * 4 : 4}, pw = {d_sw, row_scales ? N * 4 : 4};
     const Span scale = {out_kind == FP8MOT_OUT_FP8 ? d_sy : nullptr, 4};
     if (!apart(sy, {sp, sb, x, w, px, pw, scale}) || !same_or_apart(sy, sr) ||
-        !apart(sp, {sr, sb, x, w, px, pw, scale}))
+        !apart(sp, {sr, sb, x, w, px, pw, scale}) ||
+        !apart({ws, (int64_t)need}, {sy, sp, sr, sb, x, w, px, pw, scale}))
       return FP8MOT_ERR_INVALID_ARG;
   }
   int cus = 0;
@@ -336,7 +338,8 @@ int fp8_linear_act_backward(const uint16_t* dy, const uint16_t* pre, int act, ui
   if (need > 0 && (ws == nullptr || !aligned16(ws) || ws_bytes < need)) return FP8MOT_ERR_WORKSPACE;
   if (dbias == nullptr && (dz == nullptr || M == 0)) return FP8MOT_OK;
   const Span sy = {dy, M * N * 2}, sp = {act == FP8MOT_ACT_NONE ? nullptr : pre, M * N * 2}, sz = {dz, M * N * 2};
-  if (!same_or_apart(sz, sy) || !same_or_apart(sz, sp) || !apart({dbias, N * 4}, {sy, sp, sz}))
+  if (!same_or_apart(sz, sy) || !same_or_apart(sz, sp) || !apart({dbias, N * 4}, {sy, sp, sz}) ||
+      !apart({ws, (int64_t)need}, {sy, sp, sz, {dbias, N * 4}}))
     return FP8MOT_ERR_INVALID_ARG;
   int cus = 0;
   int st = current_device(&cus);
@@ -401,7 +404,8 @@ int fp8_layer_norm_backward(const void* dy, int dy_elem, const void* x, int x_el
     const Span sr = {dres, sx.bytes}, sd = {dx, sx.bytes}, sw = {weight, H * elem_bytes(w_elem)};
     const Span mu = {mean, rows * 4}, rs = {rstd, rows * 4}, dw = {dweight, H * 4}, db = {dbias, H * 4};
     if (!same_or_apart(sd, sy) || !same_or_apart(sd, sx) || !same_or_apart(sd, sr) || !apart(sd, {sw, mu, rs, dw, db}) ||
-        !apart(dw, {sy, sx, sr, sw, mu, rs, db}) || !apart(db, {sy, sx, sr, sw, mu, rs}))
+        !apart(dw, {sy, sx, sr, sw, mu, rs, db}) || !apart(db, {sy, sx, sr, sw, mu, rs}) ||
+        !apart({ws, (int64_t)need}, {sy, sx, sr, sd, sw, mu, rs, dw, db}))
       return FP8MOT_ERR_INVALID_ARG;
   }
   int cus = 0;
