@@ -14,6 +14,7 @@ are ``torch.uint8`` holding E4M3FN codes; scales are one-element
 import ctypes
 import functools
 import math
+import warnings
 
 import torch
 
@@ -173,19 +174,26 @@ def fp8_linear_rowwise(qx, qw, sx, sw, out_kind=OUT_BF16, out=None, accum=ACC_EX
 # training step.  Their common case -- plain contiguous tensors that fit, on
 # the current device -- is marshalled natively (csrc/binding.cpp), which
 # returns None for anything else and the status where the library refuses;
-# what follows the native call is every check and its message.
+# what follows the native call is every check and its message, and all there
+# is where the native front is not built (about 5 us more a call).
 _native = None
+NO_FRONT = ("the native front of the binding is missing or does not load: fp8_linear_act, fp8_layer_norm and their "
+            "backward passes take longer on the host (build it with `python -m mlp_fp8_quant_amd.build`)")
+
+
+class _PythonOnly:
+    linear_act = linear_act_backward = layer_norm = layer_norm_backward = staticmethod(lambda *args: None)
 
 
 def _load_native():
     global _native
     try:
         from . import _binding
-    except ImportError as e:
-        raise RuntimeError("the native binding is missing or does not load: build it with "
-                           "`python -m mlp_fp8_quant_amd.build`") from e
-    _native = _binding
-    return _binding
+        _native = _binding
+    except ImportError:
+        warnings.warn(NO_FRONT)
+        _native = _PythonOnly
+    return _native
 
 
 _Tensor = torch.Tensor

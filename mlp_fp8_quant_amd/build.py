@@ -15,6 +15,7 @@ Compiler flags:
 import os
 import subprocess
 import sys
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -63,8 +64,21 @@ def build(verbose=False, jobs=4) -> str:
     tmp = LIB_PATH + ".tmp"
     _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp])
     os.replace(tmp, LIB_PATH)
-    build_binding(verbose)
+    build_front(verbose)
     return LIB_PATH
+
+
+def build_front(verbose=False):
+    """build_binding, or where that is not possible (no g++, no torch headers)
+    no front at all, with a warning: the binding then runs its checks in
+    Python, and a front of another library's build must not stay beside this
+    one."""
+    try:
+        build_binding(verbose)
+    except (ImportError, OSError, RuntimeError) as e:
+        if os.path.exists(BINDING_PATH):
+            os.remove(BINDING_PATH)
+        warnings.warn(f"the native front of the binding was not built: {e}")
 
 
 def build_binding(verbose=False) -> str:
