@@ -1,7 +1,7 @@
 """GPU: the layer norm and its backward pass where range and rounding bite:
-rows whose mean is far above their spread, backward passes whose statistics
-leave FP32's range in columns past the row's end.  References are 64-bit, from
-the formulas."""
+rows whose mean is far above their spread, wide FP32 rows, backward passes
+whose statistics leave FP32's range in columns past the row's end.  References
+are 64-bit, from the formulas."""
 
 import pytest
 import torch
@@ -88,6 +88,30 @@ def test_norm_of_constant_rows_with_tiny_eps():
         x = torch.full((600, H), 777.7, device=device())
         y, mean, rstd = fp8.fp8_layer_norm(x, None, None, 1e-20, fp8.OUT_F32, stats=True)
         assert bool(torch.isfinite(rstd).all()) and torch.equal(mean, x[:, 0])
+
+
+# ---------------------------------------------------------------------------
+# Wide FP32 rows
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("rows,H", [(513, 4104), (700, 5120), (900, 6144), (600, 8200), (700, 9001), (520, 12288)])
+def test_norm_of_wide_fp32_rows(rows, H):
+    # FP32 rows of three groups per thread, with weight and bias of either type
+    g = torch.Generator().manual_seed(rows)
+    x = (torch.randn(rows, H, generator=g) + 0.3).to(device())
+    sy = torch.tensor([0.02], device=device())
+    for wt in (BF16, F32):
+        w, b = ((k + 0.2 * torch.randn(H, generator=g)).to(wt).to(device()) for k in (1.0, 0.0))
+        y64, mean64, rstd64, err = ref.norm(x, w, b, 1e-5)
+        for out in (fp8.OUT_BF16, fp8.OUT_F32, fp8.OUT_FP8):
+            y, mean, rstd = fp8.fp8_layer_norm(x, w, b, 1e-5, out, sy, stats=True)
+            if out == fp8.OUT_FP8:
+                ref.check_fp8(y, y64, err, sy, "y")
+            else:
+                ref.check(y, y64, err, "y")
+        e_mean, e_rstd = ref.norm_errors(x.cpu().double(), 1e-5)
+        ref.check(mean, mean64, e_mean, "mean")
+        ref.check(rstd, rstd64, rstd64 * e_rstd, "rstd")
 
 
 # ---------------------------------------------------------------------------
