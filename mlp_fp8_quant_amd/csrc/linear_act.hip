@@ -27,7 +27,7 @@ using tile::v4i;
 
 // Products of few rows.  A workgroup computes 16 * MB rows of X against 16 * NB
 // rows of W; its NW waves take the 128-K stages of K in turn, each through a
-// ring of D stages of its own in LDS that the buffer unit fills (rows of 128
+// ring of two stages of its own in LDS that the buffer unit fills (rows of 128
 // codes, swizzled as in the tiled kernel), so no wave waits for another until
 // their sums are added in wave order at the end.  A lane reads 16-byte chunks
 // lane / 16 and lane / 16 + 4 of row lane % 16 of each 16-row block and feeds
@@ -44,11 +44,12 @@ using tile::v4i;
 // one after another (512x4096x12288 52 us, 0.99 PFLOP/s).
 constexpr int kStageK = 128;
 
-template <int MB, int NB, int NW, int D>
+template <int MB, int NB, int NW>
 __global__ __launch_bounds__(NW * 64, 1) void linear_rows_kernel(LinearActArgs g) {
   constexpr int RB = MB + NB, COPIES = 2 * RB, STAGE = RB * 2048;
+  constexpr int D = 2;   // stages of a wave's ring
   static_assert(NW * D * STAGE <= 160 * 1024 && NW * MB * NB * 1024 <= NW * D * STAGE, "LDS");
-  static_assert(D >= 2 && D <= 4 && D * COPIES < 64, "wait_copies");
+  static_assert(D * COPIES < 64, "wait_copies");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[NW * D * STAGE];
   // Epilogue: a wave takes G 16-row blocks of the same 16 columns at once
   // (their operands in flight together), ROUNDS times; one copy of the code,
@@ -127,11 +128,10 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_rows_kernel(LinearActArgs g
       }
     }
   };
-  // at most n copies of this wave in flight (vmcnt alone: gfx9 encoding)
-  auto wait_copies = [&](int n) {
-    if (D > 3 && n >= 3 * COPIES) __builtin_amdgcn_s_waitcnt(0x0F70 | ((3 * COPIES) & 15) | (((3 * COPIES) >> 4) << 14));
-    else if (D > 2 && n >= 2 * COPIES) __builtin_amdgcn_s_waitcnt(0x0F70 | ((2 * COPIES) & 15) | (((2 * COPIES) >> 4) << 14));
-    else if (n >= COPIES) __builtin_amdgcn_s_waitcnt(0x0F70 | (COPIES & 15) | ((COPIES >> 4) << 14));
+  // at most one stage's copies of this wave in flight, or none (vmcnt alone:
+  // gfx9 encoding)
+  auto wait_copies = [&](bool one) {
+    if (one) __builtin_amdgcn_s_waitcnt(0x0F70 | (COPIES & 15) | ((COPIES >> 4) << 14));
     else __builtin_amdgcn_s_waitcnt(0x0F70);
   };
   const int stages = (K + kStageK - 1) / kStageK;
@@ -148,7 +148,7 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_rows_kernel(LinearActArgs g
   const int rd0 = l15 * 128 + ((kq ^ (l15 >> 1)) << 4), rd1 = l15 * 128 + (((kq + 4) ^ (l15 >> 1)) << 4);
   int slot = 0;
   for (int i = 0; i < mine; ++i) {
-    wait_copies(COPIES * (min(D, mine - i) - 1));
+    wait_copies(i + 1 < mine);
     asm volatile("" ::: "memory");
     const uint8_t* st = ring + slot * STAGE;
     v4i f[RB][2];
@@ -218,9 +218,9 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_rows_kernel(LinearActArgs g
   }
 }
 
-template <int MB, int NB, int NW, int D>
+template <int MB, int NB, int NW>
 hipError_t launch_rows(const LinearActArgs& g, hipStream_t stream) {
-  hipLaunchKernelGGL((linear_rows_kernel<MB, NB, NW, D>),
+  hipLaunchKernelGGL((linear_rows_kernel<MB, NB, NW>),
                      dim3((unsigned)((g.N + 16 * NB - 1) / (16 * NB)), (unsigned)((g.M + 16 * MB - 1) / (16 * MB))),
                      dim3(NW * 64), 0, stream, g);
   return hipGetLastError();
@@ -410,16 +410,16 @@ size_t linear_act_workspace(int64_t M, int64_t N, int64_t K) {
 hipError_t launch_linear_act(const LinearActArgs& g, int accum, float* ws, int num_cus, hipStream_t stream) {
   const LinearPlan p = linear_plan(g.M, g.N, g.K);
   switch (p.tile) {
-    case kRows1x1: return launch_rows<1, 1, 16, 2>(g, stream);
-    case kRows1x2: return launch_rows<1, 2, 8, 2>(g, stream);
-    case kRows1x4: return launch_rows<1, 4, 4, 2>(g, stream);
-    case kRows2x1: return launch_rows<2, 1, 8, 2>(g, stream);
-    case kRows2x2: return launch_rows<2, 2, 8, 2>(g, stream);
-    case kRows2x4: return launch_rows<2, 4, 4, 2>(g, stream);
-    case kRows4x2: return launch_rows<4, 2, 4, 2>(g, stream);
-    case kRows4x4: return launch_rows<4, 4, 4, 2>(g, stream);
-    case kRows4x6: return launch_rows<4, 6, 4, 2>(g, stream);
-    case kRows4x4Pair: return launch_rows<4, 4, 2, 2>(g, stream);
+    case kRows1x1: return launch_rows<1, 1, 16>(g, stream);
+    case kRows1x2: return launch_rows<1, 2, 8>(g, stream);
+    case kRows1x4: return launch_rows<1, 4, 4>(g, stream);
+    case kRows2x1: return launch_rows<2, 1, 8>(g, stream);
+    case kRows2x2: return launch_rows<2, 2, 8>(g, stream);
+    case kRows2x4: return launch_rows<2, 4, 4>(g, stream);
+    case kRows4x2: return launch_rows<4, 2, 4>(g, stream);
+    case kRows4x4: return launch_rows<4, 4, 4>(g, stream);
+    case kRows4x6: return launch_rows<4, 6, 4>(g, stream);
+    case kRows4x4Pair: return launch_rows<4, 4, 2>(g, stream);
     default: break;
   }
   const hipError_t e = launch_linear_tile(g, p, accum, ws, num_cus, stream);
