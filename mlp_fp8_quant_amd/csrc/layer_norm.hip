@@ -172,10 +172,11 @@ __global__ __launch_bounds__(TC > 0 ? 256 : 1024) void layer_norm_kernel(LayerNo
       const float off = __fmul_rn(row_sum<TC>(c, red[2]), inv_h);
       var = centred(var, off);
       mean = __fadd_rn(mean, off);
+      const bool flat = __fadd_rn(var, g.eps) == 0.0f;   // 0 * Inf below, whatever off's roundings left
 #pragma unroll
       for (int j = 0; j < U; ++j)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[j][k] = __fadd_rn(x[j][k], -off);
+        for (int k = 0; k < 8; ++k) x[j][k] = flat ? 0.0f : __fadd_rn(x[j][k], -off);
     }
     const float rstd = 1.0f / __fsqrt_rn(__fadd_rn(var, g.eps));
     if (t == 0) {
@@ -236,6 +237,7 @@ __global__ __launch_bounds__(1024) void layer_norm_long_kernel(LayerNormArgs g) 
     var = centred(var, off);
   }
   const float rstd = 1.0f / __fsqrt_rn(__fadd_rn(var, g.eps));
+  const bool flat = off != 0.0f && __fadd_rn(var, g.eps) == 0.0f;   // 0 * Inf below, whatever off's roundings left
   if (threadIdx.x == 0) {
     if (g.mean != nullptr) g.mean[r] = __fadd_rn(mean, off);
     if (g.rstd != nullptr) g.rstd[r] = rstd;
@@ -247,7 +249,10 @@ __global__ __launch_bounds__(1024) void layer_norm_long_kernel(LayerNormArgs g) 
     float w[8], b[8];
     affine8(g, i, w, b);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = __builtin_fmaf(__fmul_rn(__fadd_rn(__fadd_rn(f[k], -mean), -off), rstd), w[k], b[k]);
+    for (int k = 0; k < 8; ++k) {
+      const float d = flat ? 0.0f : __fadd_rn(__fadd_rn(f[k], -mean), -off);
+      f[k] = __builtin_fmaf(__fmul_rn(d, rstd), w[k], b[k]);
+    }
     emit8(g, base, i, rs, f);
   }
   }

@@ -90,6 +90,18 @@ def test_norm_of_constant_rows_with_tiny_eps():
         assert bool(torch.isfinite(rstd).all()) and torch.equal(mean, x[:, 0])
 
 
+def test_norm_of_constant_rows_without_eps():
+    # 0 / 0: NaN, or a quotient of what the roundings leave, never an infinity,
+    # which an FP8 output would show as its largest value.  With all differences
+    # d, |d - off| is within DEPTH d, and a variance d^2 - off^2 above 0 at least
+    # 2^-48 d^2 (off^2 has 48 bits): 60 at most
+    for H in (7, 96, 300, 1027, 5120, 9001, 20000, 40001):
+        x = (500 + 1000 * torch.rand(600, 1, generator=torch.Generator().manual_seed(H))).expand(600, H).contiguous()
+        y = fp8.fp8_layer_norm(x.to(device()), None, None, 0.0, fp8.OUT_F32)
+        assert not bool(torch.isinf(y).any())
+        assert bool((torch.isnan(y) | (y.abs() <= 60)).all())
+
+
 # ---------------------------------------------------------------------------
 # Wide FP32 rows
 # ---------------------------------------------------------------------------
