@@ -60,16 +60,123 @@
 #include <type_traits>
 
 #include "device_common.h"
-#include "gemm_parts.h"
 #include "kernels.h"
 
 namespace fp8mot {
 
 namespace {
 
-using namespace tile;
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef float v4f __attribute__((ext_vector_type(4)));
 
+constexpr int kNumXcd = 8;      // MI355X: 8 XCDs
 constexpr int kGroupM = 8;      // tile rows per band
+
+// Workgroup id -> (tile_m, tile_n).
+__device__ __forceinline__ void tile_of(int bid, int tiles_m, int tiles_n,
+                                        int& tm, int& tn) {
+  const int nb = tiles_m * tiles_n;
+  // undo the round-robin XCD dealing: blocks of one XCD become contiguous
+  const int xcd = bid % kNumXcd, idx = bid / kNumXcd;
+  const int q = nb / kNumXcd, r = nb % kNumXcd;
+  const int t = (xcd < r ? xcd * (q + 1) : r * (q + 1) + (xcd - r) * q) + idx;
+  // banded order: kGroupM tile rows advance together along N
+  const int per_band = kGroupM * tiles_n;
+  const int band = t / per_band;
+  const int first_m = band * kGroupM;
+  const int rows = min(tiles_m - first_m, kGroupM);
+  const int in_band = t - band * per_band;
+  tm = first_m + in_band % rows;
+  tn = in_band / rows;
+}
+
+// Two E4M3 codes (the low or high half of a dword) -> two F16 values with the gfx950
+// packed conversion at scale 1.0.  Every finite E4M3 value is exactly an F16
+// value (max 448, smallest subnormal 2^-9 is an F16 normal) and the NaN codes
+// become an F16 NaN; all 256 codes were checked on the hardware.
+template <bool HIGH>
+__device__ __forceinline__ int e4m3x2_to_f16x2(uint32_t x) {
+  return __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x, 1.0f, HIGH));
+}
+
+// Buffer resource over [base, base + bytes): loads beyond it return 0 and
+// stores beyond it are dropped, which is how every bound below is enforced
+// without a branch.  The third-dword value is the standard gfx9 raw-buffer
+// configuration.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base,
+                                                           int64_t bytes) {
+  const int n = bytes > 0x7FFFFFF0LL ? 0x7FFFFFF0 : (int)bytes;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, n,
+                                           0x00020000);
+}
+
+constexpr int kOOB = 0x7FFFFFF0;  // a byte offset past every buffer
+
+// The same raw-buffer descriptor as four dwords (base address, stride 0,
+// size in bytes, the configuration dword) for the inline-assembly copy below.
+__device__ __forceinline__ v4i make_rsrc_words(const void* base, int64_t bytes) {
+  const int n = bytes > 0x7FFFFFF0LL ? 0x7FFFFFF0 : (int)bytes;
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  return (v4i){(int)(uint32_t)a, (int)(uint32_t)((a >> 32) & 0xFFFF), n, 0x00020000};
+}
+
+// One wave-wide 16-byte-per-lane copy from a buffer straight into LDS
+// (buffer_load_dwordx4 ... lds): lane i's bytes land at lds_addr + 16 * i,
+// out-of-range lanes write zeros.  Written as assembly so that the compiler,
+// which cannot tell which stage buffer a copy writes, does not make every
+// LDS read wait for every copy; the kernel waits for its copies itself
+// (s_waitcnt vmcnt) before the barrier that publishes a stage.  M0 holds the
+// LDS address; one wait state separates its write from the copy.  The
+// memory address is the descriptor's base + soff (one value for the wave)
+// + voff (per lane).
+__device__ __forceinline__ void copy_to_lds(v4i rsrc, uint32_t lds_addr, int voff, int soff) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dwordx4 %1, %2, %3 offen lds"
+      :
+      : "s"(lds_addr), "v"(voff), "s"(rsrc), "s"(soff)
+      : "memory", "m0");
+}
+
+typedef unsigned v2u __attribute__((ext_vector_type(2)));
+
+// Lane t of a quad holds byte e = row e of column t; afterwards it holds
+// byte e = column e of row t (a 4x4 byte transpose across the quad).
+__device__ __forceinline__ uint32_t quad_transpose_bytes(uint32_t x, int t) {
+  // exchange 16-bit halves with lane t ^ 2, then bytes with lane t ^ 1
+  const uint32_t p = (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x4E, 0xF, 0xF, true);   // quad_perm [2,3,0,1]
+  const uint32_t z = __builtin_amdgcn_perm(p, x, t < 2 ? 0x05040100u : 0x03020706u);
+  const uint32_t r = (uint32_t)__builtin_amdgcn_mov_dpp((int)z, 0xB1, 0xF, 0xF, true);   // quad_perm [1,0,3,2]
+  return __builtin_amdgcn_perm(r, z, (t & 1) ? 0x03070105u : 0x06020400u);
+}
+
+// Lane t of a quad holds four 16-bit values of column t, rows 0..3, as
+// a = row0 | row1 << 16 and b = row2 | row3 << 16; afterwards d0, d1 hold
+// row t, columns 0..3 (d0 = col0 | col1 << 16, d1 = col2 | col3 << 16).
+__device__ __forceinline__ void quad_transpose_halves(uint32_t a, uint32_t b, int t,
+                                                      uint32_t& d0, uint32_t& d1) {
+  // lanes 0, 1 keep rows 0-1 and take those of columns t + 2; lanes 2, 3
+  // keep rows 2-3 and take those of columns t - 2
+  const uint32_t send = t < 2 ? b : a;
+  const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)send, 0x4E, 0xF, 0xF, true);
+  const uint32_t u = t < 2 ? a : got;    // rows ra, ra+1 of column t & 1
+  const uint32_t v = t < 2 ? got : b;    // rows ra, ra+1 of column (t & 1) + 2
+  // even lanes keep row ra and send row ra+1; odd lanes the reverse
+  const uint32_t s2 = (t & 1) ? __builtin_amdgcn_perm(v, u, 0x05040100u)    // u.lo | v.lo << 16
+                              : __builtin_amdgcn_perm(v, u, 0x07060302u);   // u.hi | v.hi << 16
+  const uint32_t r2 = (uint32_t)__builtin_amdgcn_mov_dpp((int)s2, 0xB1, 0xF, 0xF, true);
+  if (t & 1) {
+    d0 = __builtin_amdgcn_perm(u, r2, 0x07060100u);   // r2.lo | u.hi << 16
+    d1 = __builtin_amdgcn_perm(v, r2, 0x07060302u);   // r2.hi | v.hi << 16
+  } else {
+    d0 = __builtin_amdgcn_perm(r2, u, 0x05040100u);   // u.lo | r2.lo << 16
+    d1 = __builtin_amdgcn_perm(r2, v, 0x07060100u);   // v.lo | r2.hi << 16
+  }
+}
 
 // Operand staging: a stage covers KS = 128 of K.  Its LDS rows hold the 128
 // FP8 codes of one A or B row, and NB stages live in LDS at once (two, or
@@ -121,6 +228,8 @@ struct GemmArgs {
   int gN[3];
   int gtiles_n[3];
 };
+
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 // OUT: 0 BF16, 1 FP8, 2 FP32 with per-tensor scales; 3 BF16, 4 FP32 with a
 // scale per row of A and per row of B (per-token / per-channel).  FUSED: gate and up GEMMs of a gated MLP in one
@@ -178,7 +287,7 @@ __global__ __launch_bounds__(WM* WN * 64 * KSPL, 1) void gemm_kernel(GemmArgs g)
   };
   auto tile_info = [&](int tile) -> TileInfo {
     int tm, tn;
-    tile_of(tile, g.tiles_m, g.tiles_n, kGroupM, tm, tn);
+    tile_of(tile, g.tiles_m, g.tiles_n, tm, tn);
     TileInfo t{0, 0, g.N, g.ldc, g.B, g.C, g.sw};
     if (g.groups > 1) {
       int p = 0;
@@ -372,14 +481,18 @@ __global__ __launch_bounds__(WM* WN * 64 * KSPL, 1) void gemm_kernel(GemmArgs g)
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         const v4i v = fa[slot][i];
-        a0[i] = decode8(v[0], v[1]);
-        a1[i] = decode8(v[2], v[3]);
+        a0[i] = __builtin_bit_cast(f16x8, (v4i){e4m3x2_to_f16x2<false>(v[0]), e4m3x2_to_f16x2<true>(v[0]),
+                                                e4m3x2_to_f16x2<false>(v[1]), e4m3x2_to_f16x2<true>(v[1])});
+        a1[i] = __builtin_bit_cast(f16x8, (v4i){e4m3x2_to_f16x2<false>(v[2]), e4m3x2_to_f16x2<true>(v[2]),
+                                                e4m3x2_to_f16x2<false>(v[3]), e4m3x2_to_f16x2<true>(v[3])});
       }
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
         const v4i v = fb[slot][j];
-        b0[j] = decode8(v[0], v[1]);
-        b1[j] = decode8(v[2], v[3]);
+        b0[j] = __builtin_bit_cast(f16x8, (v4i){e4m3x2_to_f16x2<false>(v[0]), e4m3x2_to_f16x2<true>(v[0]),
+                                                e4m3x2_to_f16x2<false>(v[1]), e4m3x2_to_f16x2<true>(v[1])});
+        b1[j] = __builtin_bit_cast(f16x8, (v4i){e4m3x2_to_f16x2<false>(v[2]), e4m3x2_to_f16x2<true>(v[2]),
+                                                e4m3x2_to_f16x2<false>(v[3]), e4m3x2_to_f16x2<true>(v[3])});
       }
 #pragma unroll
       for (int i = 0; i < FM; ++i) {

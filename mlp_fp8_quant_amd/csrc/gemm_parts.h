@@ -1,6 +1,6 @@
-// Device pieces that the FP8 x FP8 products share (gfx950; gemm.hip,
-// linear_act.hip, linear_act_tile.hip): the tile order, exact decode, operand
-// windows, copies into LDS and the quad transposes of gemm.hip's epilogues.
+// Device pieces of the tiled FP8 x FP8 products (gfx950): operand windows,
+// copies into LDS, the LDS swizzle, exact decode and the quad transposes of
+// the epilogues.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -40,8 +40,7 @@ __device__ __forceinline__ void tile_of(int bid, int tiles_m, int tiles_n, int b
 
 // Eight E4M3 codes (two dwords) -> eight F16 values with the gfx950 packed
 // conversion at scale 1.0: every E4M3 value is exactly an F16 value (max 448,
-// smallest subnormal 2^-9 is an F16 normal) and the NaN codes become a NaN;
-// all 256 codes were checked on the hardware.
+// smallest subnormal 2^-9 is an F16 normal) and the NaN codes become a NaN.
 __device__ __forceinline__ f16x8 decode8(int lo, int hi) {
   return __builtin_bit_cast(
       f16x8, (v4i){__builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((uint32_t)lo, 1.0f, false)),
@@ -50,11 +49,11 @@ __device__ __forceinline__ f16x8 decode8(int lo, int hi) {
                    __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((uint32_t)hi, 1.0f, true))});
 }
 
-// Buffer resource over [base, base + bytes), bytes >= 0: loads beyond it return
-// 0 and stores beyond it are dropped, which is how bounds are enforced without a
-// branch.  The third-dword value is the standard gfx9 raw-buffer configuration.
+// Buffer resource over [base, base + bytes): loads beyond it return 0 and
+// stores beyond it are dropped.  The third-dword value is the standard gfx9
+// raw-buffer configuration.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
-  const int n = bytes > 0x7FFFFFF0LL ? 0x7FFFFFF0 : (int)bytes;
+  const int n = bytes > 0x7FFFFFF0LL ? 0x7FFFFFF0 : (bytes > 0 ? (int)bytes : 0);
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, n, 0x00020000);
 }
 
@@ -65,14 +64,12 @@ __device__ __forceinline__ v4i make_rsrc_words(const void* base, int64_t bytes) 
   return (v4i){(int)(uint32_t)a, (int)(uint32_t)((a >> 32) & 0xFFFF), n, 0x00020000};
 }
 
-// One wave-wide copy from a buffer straight into LDS (buffer_load_dwordx4 ...
-// lds): lane i's 16 bytes land at lds_addr + 16 * i, out-of-range lanes write
-// zeros.  Written as assembly so that the compiler, which cannot tell which
-// stage buffer a copy writes, does not make every LDS read wait for every
-// copy; the kernel waits for its copies itself (s_waitcnt vmcnt) before it
-// reads a stage.  M0 holds the LDS address; one wait state separates its write
-// from the copy.  The memory address is the descriptor's base + soff (one value
-// for the wave) + voff (per lane).
+// One wave-wide 16-byte-per-lane copy from a buffer straight into LDS: lane
+// i's bytes land at lds_addr + 16 * i, out-of-range lanes write zeros.  As
+// assembly, so that the compiler does not make every LDS read wait for every
+// copy; the kernel waits for its copies itself before the barrier that
+// publishes a stage.  M0 holds the LDS address; one wait state separates its
+// write from the copy.
 __device__ __forceinline__ void copy_to_lds(v4i rsrc, uint32_t lds_addr, int voff, int soff) {
   asm volatile(
       "s_mov_b32 m0, %0\n\t"
@@ -83,28 +80,24 @@ __device__ __forceinline__ void copy_to_lds(v4i rsrc, uint32_t lds_addr, int vof
       : "memory", "m0");
 }
 
-// Lane t of a quad holds byte e = row e of column t; afterwards it holds
-// byte e = column e of row t (a 4x4 byte transpose across the quad).
+// Lane t of a quad holds byte e = row e of column t; afterwards it holds byte
+// e = column e of row t.
 __device__ __forceinline__ uint32_t quad_transpose_bytes(uint32_t x, int t) {
-  // exchange 16-bit halves with lane t ^ 2, then bytes with lane t ^ 1
-  const uint32_t p = (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x4E, 0xF, 0xF, true);   // quad_perm [2,3,0,1]
+  const uint32_t p = (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x4E, 0xF, 0xF, true);   // lane t ^ 2
   const uint32_t z = __builtin_amdgcn_perm(p, x, t < 2 ? 0x05040100u : 0x03020706u);
-  const uint32_t r = (uint32_t)__builtin_amdgcn_mov_dpp((int)z, 0xB1, 0xF, 0xF, true);   // quad_perm [1,0,3,2]
+  const uint32_t r = (uint32_t)__builtin_amdgcn_mov_dpp((int)z, 0xB1, 0xF, 0xF, true);   // lane t ^ 1
   return __builtin_amdgcn_perm(r, z, (t & 1) ? 0x03070105u : 0x06020400u);
 }
 
 // Lane t of a quad holds four 16-bit values of column t, rows 0..3, as
-// a = row0 | row1 << 16 and b = row2 | row3 << 16; afterwards d0, d1 hold
-// row t, columns 0..3 (d0 = col0 | col1 << 16, d1 = col2 | col3 << 16).
+// a = row0 | row1 << 16 and b = row2 | row3 << 16; afterwards d0, d1 hold row
+// t, columns 0..3.  Its own inverse: rows in, columns out.
 __device__ __forceinline__ void quad_transpose_halves(uint32_t a, uint32_t b, int t, uint32_t& d0,
                                                       uint32_t& d1) {
-  // lanes 0, 1 keep rows 0-1 and take those of columns t + 2; lanes 2, 3
-  // keep rows 2-3 and take those of columns t - 2
   const uint32_t send = t < 2 ? b : a;
   const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)send, 0x4E, 0xF, 0xF, true);
   const uint32_t u = t < 2 ? a : got;    // rows ra, ra+1 of column t & 1
   const uint32_t v = t < 2 ? got : b;    // rows ra, ra+1 of column (t & 1) + 2
-  // even lanes keep row ra and send row ra+1; odd lanes the reverse
   const uint32_t s2 = (t & 1) ? __builtin_amdgcn_perm(v, u, 0x05040100u)    // u.lo | v.lo << 16
                               : __builtin_amdgcn_perm(v, u, 0x07060302u);   // u.hi | v.hi << 16
   const uint32_t r2 = (uint32_t)__builtin_amdgcn_mov_dpp((int)s2, 0xB1, 0xF, 0xF, true);
