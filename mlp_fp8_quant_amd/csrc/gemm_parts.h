@@ -1,6 +1,7 @@
-// Device pieces of the tiled FP8 x FP8 products (gfx950): operand windows,
-// copies into LDS, the LDS swizzle, exact decode and the quad transposes of
-// the epilogues.
+// Device pieces of the Linear epilogue's FP8 x FP8 products (gfx950): tile
+// order, exact decode, operand windows and copies into LDS.  gemm.hip, whose
+// recorded counters are tied to its own text, holds the same pieces itself: a
+// change to one belongs in the other too.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -78,36 +79,6 @@ __device__ __forceinline__ void copy_to_lds(v4i rsrc, uint32_t lds_addr, int vof
       :
       : "s"(lds_addr), "v"(voff), "s"(rsrc), "s"(soff)
       : "memory", "m0");
-}
-
-// Lane t of a quad holds byte e = row e of column t; afterwards it holds byte
-// e = column e of row t.
-__device__ __forceinline__ uint32_t quad_transpose_bytes(uint32_t x, int t) {
-  const uint32_t p = (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x4E, 0xF, 0xF, true);   // lane t ^ 2
-  const uint32_t z = __builtin_amdgcn_perm(p, x, t < 2 ? 0x05040100u : 0x03020706u);
-  const uint32_t r = (uint32_t)__builtin_amdgcn_mov_dpp((int)z, 0xB1, 0xF, 0xF, true);   // lane t ^ 1
-  return __builtin_amdgcn_perm(r, z, (t & 1) ? 0x03070105u : 0x06020400u);
-}
-
-// Lane t of a quad holds four 16-bit values of column t, rows 0..3, as
-// a = row0 | row1 << 16 and b = row2 | row3 << 16; afterwards d0, d1 hold row
-// t, columns 0..3.  Its own inverse: rows in, columns out.
-__device__ __forceinline__ void quad_transpose_halves(uint32_t a, uint32_t b, int t, uint32_t& d0,
-                                                      uint32_t& d1) {
-  const uint32_t send = t < 2 ? b : a;
-  const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)send, 0x4E, 0xF, 0xF, true);
-  const uint32_t u = t < 2 ? a : got;    // rows ra, ra+1 of column t & 1
-  const uint32_t v = t < 2 ? got : b;    // rows ra, ra+1 of column (t & 1) + 2
-  const uint32_t s2 = (t & 1) ? __builtin_amdgcn_perm(v, u, 0x05040100u)    // u.lo | v.lo << 16
-                              : __builtin_amdgcn_perm(v, u, 0x07060302u);   // u.hi | v.hi << 16
-  const uint32_t r2 = (uint32_t)__builtin_amdgcn_mov_dpp((int)s2, 0xB1, 0xF, 0xF, true);
-  if (t & 1) {
-    d0 = __builtin_amdgcn_perm(u, r2, 0x07060100u);   // r2.lo | u.hi << 16
-    d1 = __builtin_amdgcn_perm(v, r2, 0x07060302u);   // r2.hi | v.hi << 16
-  } else {
-    d0 = __builtin_amdgcn_perm(r2, u, 0x05040100u);   // u.lo | r2.lo << 16
-    d1 = __builtin_amdgcn_perm(r2, v, 0x07060100u);   // v.lo | r2.hi << 16
-  }
 }
 
 }  // namespace tile
