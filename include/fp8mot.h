@@ -320,8 +320,11 @@ int fp8_linear_rowwise(const uint8_t* qx, const uint8_t* qw, void* y, int64_t M,
 /* ------------------------------------------------------------------ */
 
 /* Bytes of workspace fp8_linear_act needs: 0 for most shapes, FP32 partial
- * sums where K is split over workgroups (few outputs, long K).  Depends on
- * (M, N, K) only.  Returns 0 for sizes that fp8_linear_act refuses. */
+ * sums where K is split over workgroups (more than about two million outputs,
+ * rows and columns counted in whole sixteens, whose tiles leave CUs idle, and
+ * K of about 2000 or more).  Depends on (M, N, K) only: tiles and splits are
+ * chosen for 256 CUs, whatever the device has.  Returns 0 for sizes that
+ * fp8_linear_act refuses. */
 size_t fp8_linear_act_workspace(int64_t M, int64_t N, int64_t K);
 
 /* FP8 Linear with bias, activation and residual in its epilogue:
@@ -371,7 +374,9 @@ size_t fp8_linear_act_backward_workspace(int64_t M, int64_t N);
  * fp8_quant_per_row and fp8_linear_rowwise on the transposed codes.
  * dy, pre, dz: BF16 [M, N]; dbias: FP32 [N]; all 16-byte aligned.  dz or
  * dbias may be NULL (not computed), and with FP8MOT_ACT_NONE pre too.  dz may
- * be dy or pre itself; any other overlap is refused.  relu's slope at 0 is 0.  M == 0 writes dbias = 0.
+ * be dy or pre itself; any other overlap is refused.  relu's slope at 0 is 0;
+ * gelu's and silu's at an infinite argument are the NaN of Inf * 0.  M == 0
+ * writes dbias = 0.
  * M up to INT32_MAX, N up to 2^26.
  * ws: 16-byte aligned, at least fp8_linear_act_backward_workspace(M, N)
  * bytes, apart from every tensor of the call; unused where dbias is NULL. */
@@ -387,7 +392,8 @@ int fp8_linear_act_backward(const uint16_t* dy, const uint16_t* pre, int act, ui
  * that read it (one quantized tensor for a group that shares its input scale,
  * as silu_mul_2in_fp8 emits the down projection's input):
  *   mean = sum_i x[i] / H,   var = sum_i (x[i] - mean)^2 / H
- *   rstd = 1 / sqrt(var + eps)
+ *   rstd = 1 / sqrt(var + eps)             (where |mean| > 4 / rstd, both are
+ *          corrected by the mean of the differences x[i] - mean)
  *   v    = fma((x[i] - mean) * rstd, weight[i], bias[i])       (FP32)
  *   y[i] = bf16_rne(v) | e4m3(v * r) | v    per out_kind, r = fp32(1 / *d_sy)
  * x: [rows, H] of x_elem (fp8mot_elem); weight, bias: [H] of wb_elem, either

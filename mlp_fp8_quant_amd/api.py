@@ -3,7 +3,9 @@
 Torch provides device memory and the current stream; every computation runs
 in libfp8mot's HIP kernels.  Each wrapper checks dtype, device and
 contiguity and refuses anything else (a strided tensor is rejected, never
-copied), flattens rank-N ``[..., H]`` activations to ``[M, H]``, and maps a
+copied), computes outside autograd (results carry no graph, also of inputs
+that require gradients: a training loop calls the ``*_backward`` functions
+itself), flattens rank-N ``[..., H]`` activations to ``[M, H]``, and maps a
 non-OK status to ``Fp8motError``.
 
 Dtypes at this boundary: BF16 tensors are ``torch.bfloat16``; FP8 tensors

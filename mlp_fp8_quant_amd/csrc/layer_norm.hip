@@ -106,6 +106,9 @@ __device__ __forceinline__ void affine8(const LayerNormArgs& g, int64_t i, float
 // BF16 -> E4M3 4.1 us with its loads unguarded, 4.4 with the guards).
 // 16384x5120 BF16 -> BF16 67 us, 5.0 TB/s, bound by memory; -> E4M3 60 us, 4.2
 // TB/s, by the arithmetic between the row's sums (loads two rows ahead: slower).
+// The bound of 1024 threads holds every whole-workgroup kernel to 128 registers;
+// that of three FP32 groups spills 32, which does not show: 16384x5120 FP32 ->
+// BF16 97 us, 8000x12288 113, both 5.2 TB/s.
 template <bool F32, int TC, int U, bool FULL>
 __global__ __launch_bounds__(TC > 0 ? 256 : 1024) void layer_norm_kernel(LayerNormArgs g) {
   __shared__ float red[3][16];

@@ -41,7 +41,7 @@ using tile::v4i;
 // operands from L2, about 50 bytes a clock with copies of whole 128-byte row
 // pieces (fragments of 64 bytes straight to registers, half of that: 64x4096
 // x4096 16.5 us, 7.9 so), and with two workgroups per CU by decodes and MFMAs
-// one after another (512x4096x12288 52 us, 0.99 PFLOP/s).
+// one after another (512x4096x12288 52 to 56 us, 0.92 to 0.99 PFLOP/s).
 constexpr int kStageK = 128;
 
 template <int MB, int NB, int NW>
@@ -353,8 +353,8 @@ hipError_t run_act_backward(const uint16_t* dy, const uint16_t* pre, int act, ui
 // 32x16 8.2), 256x4096x4096 15.4 with 64x64 (64x32 19.3; 128x128 tiles split
 // four ways over K 23.1), 128x12288x4096 22.0 with 64x96 (64x64 in pairs 24.2),
 // 500x3000x3008 18.6 (24.8; but 128x12288x512 10.3, in pairs 9.0).  Above that, up to two workgroups per CU (64x64,
-// two waves): 512x4096x2048 16.1 (128x128 tiles 23.0), 512x4096x12288 55
-// (128x128 split in two 54.7), 777x2053x2064 20.0 (27.1).
+// two waves): 512x4096x2048 16.1 (128x128 tiles 23.0), 512x4096x12288 as
+// long as 128x128 split in two, 777x2053x2064 20.0 (27.1).
 //
 // More outputs: the cheapest of the tiles and splits by an estimate of rounds
 // of workgroups times (rate * K + what a tile costs besides), plus the second
