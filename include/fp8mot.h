@@ -82,7 +82,9 @@ typedef enum {
 typedef enum {
   FP8MOT_OUT_BF16 = 0, /* y = bf16_rne(acc * (s_x * s_w)), uint16_t [M, N] */
   FP8MOT_OUT_FP8 = 1,  /* y = e4m3(acc * (s_x * s_w) / s_y), uint8_t [M, N] */
-  FP8MOT_OUT_F32 = 2   /* y = acc * (s_x * s_w) before any output rounding, float [M, N] */
+  FP8MOT_OUT_F32 = 2,  /* y = acc * (s_x * s_w) before any output rounding, float [M, N] */
+  FP8MOT_OUT_FP8_BLOCK = 3 /* fp8_residual_norm alone: codes with an FP32 scale for each
+                              128 columns of a row, as fp8_quant_block gives them */
 } fp8mot_out;
 
 /* Accumulation engine of the FP8 GEMMs (fp8_linear and the composites).
@@ -316,6 +318,67 @@ int fp8_linear_rowwise(const uint8_t* qx, const uint8_t* qw, void* y, int64_t M,
                        int out_kind, int accum, hipStream_t stream);
 
 /* ------------------------------------------------------------------ */
+/* FP8 with a scale for each block of 128                              */
+/* ------------------------------------------------------------------ */
+
+/* Dynamic quantization with an FP32 scale for each block of 128, finer than
+ * fp8_quant_per_row's: an outlier costs precision in its block alone.
+ *   scale = fp32(amax of the block) / 448,  q = e4m3(fp32(x) / scale)
+ * (IEEE FP32 divisions) for blocks of x [M, K] (of x_elem, fp8mot_elem) that are
+ *   tile 0: 128 columns of a row (the last one K's remainder)
+ *   tile 1: 128 x 128 tiles (the last ones the remainders)
+ * and with transpose 1 the same of x^T, whose codes and scales are written
+ * as those of a [K, M] tensor:
+ *   transpose 0: q [M, ld(K)], scales [M, nb(K)], or with tile [nb(M), nb(K)]
+ *   transpose 1: q [K, ld(M)], scales [K, nb(M)], or with tile [nb(K), nb(M)]
+ * with nb(n) = ceil(n / 128) and ld(n) = n rounded up to a multiple of 16, the
+ * codes from n on being those of zeros: rows of codes of any length are
+ * operands of fp8_linear_block.  Activations and gradients have blocks of a
+ * row, weights tiles; a product's backward pass takes the transposed forms:
+ *   dx = dy w     fp8_linear_block of dy's rows and w's transposed tiles
+ *   dw = dy^T x   fp8_linear_block of dy's and x's transposed rows, FP32 out
+ * A zero block gets scale 0 and keeps its signed zeros; one that holds a NaN
+ * gets a NaN scale and NaN codes (its padding too), one with an infinity an
+ * infinite scale, zeros and, for the infinity, a NaN code.
+ * M up to INT32_MAX and K up to 2^26; x, q 16-byte aligned.  q and scales lie
+ * apart from x and from each other.  M == 0 or K == 0 does nothing. */
+int fp8_quant_block(const void* x, int x_elem, uint8_t* q, float* d_scales, int64_t M,
+                    int64_t K, int tile, int transpose, hipStream_t stream);
+
+/* silu_mul_2in_fp8 with a scale for each 128 columns of a row, taken from the
+ * values themselves instead of calibrated:
+ *   v = g / (1 + exp(-g)) * u            (FP32, within about 2 ulp)
+ *   q, scales = fp8_quant_block of v [M, K]  (tile 0, transpose 0)
+ * g, u: BF16 [M, K], 16-byte aligned like q [M, ld(K)]; limits as there. */
+int silu_mul_2in_block(const uint16_t* g, const uint16_t* u, uint8_t* q, float* d_scales,
+                       int64_t M, int64_t K, hipStream_t stream);
+
+/* FP8 Linear of operands that have a scale for each block of 128 of K, with
+ * fp8_linear_act's epilogue:
+ *   P[m,n,b] = sum_{k in block b} e4m3_value(qx[m,k]) * e4m3_value(qw[n,k])
+ *   acc[m,n] = sum_b fp32(d_sx[m,b] * d_sw[n',b]) * P[m,n,b]
+ *   z = acc + bias[n],  v = act(z) + residual[m,n],  y per out_kind
+ * d_sx: FP32 [M, nb(K)]; d_sw: with w_rows 0 FP32 [nb(N), nb(K)] and n' = n / 128
+ * (weights), with w_rows 1 FP32 [N, nb(K)] and n' = n (a weight's gradient,
+ * whose operands are both quantized along the rows summed over).  The sums are
+ * FP32 on the exact engine (codes decoded to F16, see FP8MOT_ACC_EXACT): each
+ * block's products are summed by themselves and added by one FMA, along K in
+ * turns or strided over the waves of a workgroup; the order depends on
+ * (M, N, K) only.  The scales may differ widely, between blocks too; a product
+ * of two scales below FP32's range is 0, above it infinite.
+ * bias, act, residual, pre, out_kind (BF16, FP8 at d_sy, FP32), d_sy and the
+ * overlaps that are allowed: as fp8_linear_act (y may be the residual: a
+ * weight's gradient is added to in place).  No workspace.  K == 0 gives
+ * act(bias) + residual.  K must be a multiple of 16 (pad codes with zeros, as
+ * fp8_quant_block does); M, N, K as in fp8_linear; qx, qw, y, bias, residual,
+ * pre 16-byte aligned. */
+int fp8_linear_block(const uint8_t* qx, const uint8_t* qw, void* y, int64_t M, int64_t N,
+                     int64_t K, const float* d_sx, const float* d_sw, int w_rows,
+                     const void* bias, int bias_elem, int act, const void* residual,
+                     int residual_elem, uint16_t* pre, int out_kind, const float* d_sy,
+                     hipStream_t stream);
+
+/* ------------------------------------------------------------------ */
 /* Linear epilogue: bias, activation, residual                         */
 /* ------------------------------------------------------------------ */
 
@@ -433,6 +496,75 @@ int fp8_layer_norm_backward(const void* dy, int dy_elem, const void* x, int x_el
                             const float* rstd, const void* dres, void* dx, float* dweight,
                             float* dbias, int64_t rows, int64_t H, void* ws, size_t ws_bytes,
                             hipStream_t stream);
+
+/* ------------------------------------------------------------------ */
+/* Norms before and after a block, its gate and residual scale         */
+/* ------------------------------------------------------------------ */
+
+/* What stands between two blocks of a decoder layer, in one pass: the norm
+ * after the block's last projection, the block's gate, the residual addition
+ * with its scale, and the norm before the next block with direct FP8 emission
+ * for the projections that read it (root mean square norms):
+ *   post_rstd = 1 / sqrt(sum_i hidden[i]^2 / H + eps)
+ *   v    = hidden[i] * post_rstd * post_weight[i]  (hidden[i] without post_weight)
+ *   r[i] = fma(alpha, v * gate[i], x[i])           the residual stream, x's type
+ *   rstd = 1 / sqrt(sum_i r[i]^2 / H + eps)
+ *   w    = r[i] * rstd * weight[i]
+ *   y[i] = bf16_rne(w) | e4m3(w / *d_sy) (times fp32(1 / *d_sy)) | w, or with
+ *          FP8MOT_OUT_FP8_BLOCK codes [rows, ld(H)] and d_scales [rows, nb(H)]
+ *          as fp8_quant_block gives them of w
+ * in FP32; rstd and w are taken from r before its rounding to x's type.
+ *  - x, r: [rows, H] of x_elem; hidden: [rows, H] of h_elem, or NULL for the
+ *    norm alone (r, gate and post_weight then have to be NULL: y of x).
+ *  - gate: NULL, or [gates, H] of gate_elem, each row the gate of rows / gates
+ *    rows one after another (one for all, one for each sample of a batch of
+ *    equal lengths, one for each row); gates has to divide rows.
+ *  - post_weight, weight: [H] of w_elem; weight NULL: ones.  alpha finite.
+ *  - rstd, post_rstd: FP32 [rows] for the backward pass, or NULL.
+ *  - r may be x itself (the stream is then updated in place), and y x without
+ *    hidden, where the element types agree; any other overlap of an output is refused.
+ * eps finite and >= 0; H up to 2^26, rows up to INT32_MAX; tensors 16-byte
+ * aligned but d_scales, rstd and post_rstd.  A row of zeros with eps 0 is NaN
+ * (0 * Inf); a NaN or an infinity, or squares beyond FP32's range, make of
+ * their row what the formulas do. */
+int fp8_residual_norm(const void* x, int x_elem, const void* hidden, int h_elem,
+                      const void* gate, int gate_elem, int64_t gates,
+                      const void* post_weight, const void* weight, int w_elem, void* r,
+                      void* y, int out_kind, const float* d_sy, float* d_scales, float* rstd,
+                      float* post_rstd, int64_t rows, int64_t H, float alpha, float eps,
+                      hipStream_t stream);
+
+/* Bytes of workspace fp8_residual_norm_backward needs (column sums over slabs
+ * of rows; gates 1 without a gate).  Returns 0 for sizes that it refuses. */
+size_t fp8_residual_norm_backward_workspace(int64_t rows, int64_t H, int64_t gates);
+
+/* Backward pass of fp8_residual_norm, for the gradients dy of y (an FP8 y
+ * passes its gradient straight through) and dr, what reaches r past the norm:
+ *   n = r * rstd,  g = dy * weight,  z = hidden * post_rstd (hidden without post_weight)
+ *   dx = rstd * (g - n * sum_i(g * n) / H) + dr
+ *   p  = dx * (alpha * gate * post_weight)
+ *   dhidden = post_rstd * (p - z * sum_i(p * z) / H)  (p without post_weight)
+ *   dweight = sum_rows dy * n,   dpost_weight = sum_rows alpha * gate * dx * z
+ *   dgate   = alpha * post_weight * the sum of dx * z over the gate's rows
+ * in FP32, dx not yet rounded where it is used again.  r, rstd, post_rstd:
+ * what fp8_residual_norm wrote (r as stored).  dy, hidden, dhidden: of h_elem;
+ * r, dr, dx: of r_elem.  Without hidden gate, post_weight, dhidden, dgate and
+ * dpost_weight have to be NULL; dr NULL: no such gradient.  dweight,
+ * dpost_weight FP32 [H], dgate FP32 [gates, H]: each may be NULL (not
+ * computed), and without gate or post_weight has to be.  dx may be dy, r or dr
+ * itself and dhidden dy or hidden, where the element types agree; any other
+ * overlap of an output is refused.  rows == 0 writes zeros to the parameters'
+ * gradients.  The sums over rows take an order that depends on (rows, H,
+ * gates) only.  Sizes and alignment as there; ws: 16-byte aligned, at least
+ * fp8_residual_norm_backward_workspace(rows, H, gates) bytes, apart from every
+ * tensor of the call. */
+int fp8_residual_norm_backward(const void* dy, const void* r, int r_elem, const void* hidden,
+                               int h_elem, const void* gate, int gate_elem, int64_t gates,
+                               const void* post_weight, const void* weight, int w_elem,
+                               const float* rstd, const float* post_rstd, const void* dr,
+                               void* dx, void* dhidden, float* dgate, float* dpost_weight,
+                               float* dweight, int64_t rows, int64_t H, float alpha, void* ws,
+                               size_t ws_bytes, hipStream_t stream);
 
 /* ------------------------------------------------------------------ */
 /* Fused-topology comparison (what the split path avoids)              */

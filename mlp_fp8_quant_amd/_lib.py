@@ -46,6 +46,22 @@ SIGNATURES = {
                                         c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                         c_void_p, c_i64, c_i64, c_void_p, c_size_t,
                                         c_void_p]),
+    "fp8_quant_block": (c_int, [c_void_p, c_int, c_void_p, c_void_p, c_i64, c_i64, c_int, c_int,
+                                c_void_p]),
+    "silu_mul_2in_block": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_i64, c_i64, c_void_p]),
+    "fp8_linear_block": (c_int, [c_void_p, c_void_p, c_void_p, c_i64, c_i64, c_i64, c_void_p,
+                                 c_void_p, c_int, c_void_p, c_int, c_int, c_void_p, c_int,
+                                 c_void_p, c_int, c_void_p, c_void_p]),
+    "fp8_residual_norm": (c_int, [c_void_p, c_int, c_void_p, c_int, c_void_p, c_int, c_i64,
+                                  c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_int, c_void_p,
+                                  c_void_p, c_void_p, c_void_p, c_i64, c_i64, c_float, c_float,
+                                  c_void_p]),
+    "fp8_residual_norm_backward_workspace": (c_size_t, [c_i64, c_i64, c_i64]),
+    "fp8_residual_norm_backward": (c_int, [c_void_p, c_void_p, c_int, c_void_p, c_int, c_void_p,
+                                           c_int, c_i64, c_void_p, c_void_p, c_int, c_void_p,
+                                           c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                           c_void_p, c_void_p, c_i64, c_i64, c_float, c_void_p,
+                                           c_size_t, c_void_p]),
     "fp8_linear_ldc": (c_int, [c_void_p, c_void_p, c_void_p, c_i64, c_i64, c_i64, c_i64,
                                c_void_p, c_void_p, c_int, c_void_p, c_int, c_void_p]),
     "fp8_requantize_onto_max": (c_int, [c_void_p, c_void_p, c_i64, c_void_p, c_void_p,

@@ -23,7 +23,8 @@ import torch
 from . import _lib
 from ._lib import Fp8motError  # noqa: F401
 
-OUT_BF16, OUT_FP8, OUT_F32 = 0, 1, 2
+OUT_BF16, OUT_FP8, OUT_F32, OUT_FP8_BLOCK = 0, 1, 2, 3
+BLOCK = 128   # elements that share a scale in the *_block calls
 ACC_EXACT, ACC_FP8_MFMA = 0, 1
 ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
 OBS_MAX, OBS_MOVING_AVG = 0, 1
@@ -172,19 +173,21 @@ def fp8_linear_rowwise(qx, qw, sx, sw, out_kind=OUT_BF16, out=None, accum=ACC_EX
     return out
 
 
-# The four calls below take many tensors and are made once per token or
-# training step.  Their common case -- plain contiguous tensors that fit, on
+# The calls below take many tensors and are made once per token or training
+# step.  Their common case -- plain contiguous tensors that fit, on
 # the current device -- is marshalled natively (csrc/binding.cpp), which
 # returns None for anything else and the status where the library refuses;
 # what follows the native call is every check and its message, and all there
 # is where the native front is not built (about 5 us more a call).
 _native = None
-NO_FRONT = ("the native front of the binding is missing or does not load: fp8_linear_act, fp8_layer_norm and their "
-            "backward passes take longer on the host (build it with `python -m mlp_fp8_quant_amd.build`)")
+NO_FRONT = ("the native front of the binding is missing or does not load: fp8_linear_act, fp8_layer_norm, the calls "
+            "with a scale for each block, fp8_residual_norm and the backward passes take longer on the host (build it "
+            "with `python -m mlp_fp8_quant_amd.build`)")
 
 
 class _PythonOnly:
-    linear_act = linear_act_backward = layer_norm = layer_norm_backward = staticmethod(lambda *args: None)
+    linear_act = linear_act_backward = layer_norm = layer_norm_backward = quant_block = silu_mul_block = \
+        linear_block = residual_norm = residual_norm_backward = staticmethod(lambda *args: None)
 
 
 def _load_native():
@@ -438,6 +441,254 @@ def fp8_layer_norm_backward(dy, x, weight, mean, rstd, dres=None, dx=None, dweig
               w_elem, mean.data_ptr(), rstd.data_ptr(), _ptr(dres), dx.data_ptr(), dweight.data_ptr(),
               dbias.data_ptr(), rows, H, ws_ptr, ws_bytes, _stream(x))
     return dx, dweight, dbias
+
+
+def _up(n, to):
+    return (n + to - 1) // to * to
+
+
+def _blocks(n):
+    return (n + BLOCK - 1) // BLOCK
+
+
+def _codes(like, lead, cols, out, scales, lead_scales=None):
+    """Codes [*lead, cols up to a multiple of 16] and scales [*lead_scales, blocks of cols]
+    of a block-scaled result: the caller's or new ones."""
+    dev = like.get_device()
+    shape, sshape = (*lead, _up(cols, 16)), (*(lead if lead_scales is None else lead_scales), _blocks(cols))
+    if out is None:
+        out = like.new_empty(shape, dtype=_U8)
+    else:
+        _fit(out, "out", _U8, dev, math.prod(shape), "rows of codes padded to a multiple of 16")
+    if scales is None:
+        scales = like.new_empty(sshape, dtype=_F32)
+    else:
+        _fit(scales, "scales", _F32, dev, math.prod(sshape), "one scale per block of 128")
+    return out, scales
+
+
+def fp8_quant_block(x, tile=False, transpose=False, out=None, scales=None):
+    """E4M3 codes of x [..., K] (BF16 or FP32) with an FP32 scale, amax / 448,
+    for each block of 128 columns of a row -- or, ``tile``, for each 128 x 128
+    tile of a 2-D x.  ``transpose``: of the transposed x [M, K], whose rows then
+    are x's columns (a product's backward pass needs them).  Returns (codes,
+    scales): codes [..., ld(K)] and scales [..., nb(K)], transposed [K, ld(M)]
+    and [K, nb(M)], tiles [nb(rows), nb(columns)], with nb(n) = ceil(n / 128) and
+    ld(n) = n up to a multiple of 16; the codes past n are zeros', so that
+    fp8_linear_block takes them as they are."""
+    r = (_native or _load_native()).quant_block(x, tile, transpose, out, scales)
+    if r is not None:
+        return r if type(r) is not int else _lib.fail("fp8_quant_block", r)
+    dev = _on_gpu(x, "x")
+    if (tile or transpose) and x.dim() != 2:
+        raise ValueError("x must be 2-D for tiles and for the transposed codes")
+    K = x.shape[-1]
+    M = math.prod(x.shape[:-1])
+    lead, cols = ((K,), M) if transpose else (x.shape[:-1], K)
+    out, scales = _codes(x, lead, cols, out, scales, (_blocks(lead[0]),) if tile else None)
+    _lib.call("fp8_quant_block", x.data_ptr(), 1 if x.dtype is _F32 else 0, out.data_ptr(), scales.data_ptr(), M, K,
+              1 if tile else 0, 1 if transpose else 0, _stream(x))
+    return out, scales
+
+
+def silu_mul_2in_block(g, u, out=None, scales=None):
+    """silu(g) * u of two BF16 tensors [..., K] as E4M3 codes with an FP32 scale
+    for each 128 columns: (codes [..., ld(K)], scales [..., nb(K)]), see
+    fp8_quant_block."""
+    r = (_native or _load_native()).silu_mul_block(g, u, out, scales)
+    if r is not None:
+        return r if type(r) is not int else _lib.fail("silu_mul_2in_block", r)
+    dev = _on_gpu(g, "g", _BF16)
+    _fit(u, "u", _BF16, dev)
+    if g.shape != u.shape:
+        raise ValueError("g and u must have the same shape")
+    K = g.shape[-1]
+    out, scales = _codes(g, g.shape[:-1], K, out, scales)
+    _lib.call("silu_mul_2in_block", g.data_ptr(), u.data_ptr(), out.data_ptr(), scales.data_ptr(),
+              math.prod(g.shape[:-1]), K, _stream(g))
+    return out, scales
+
+
+def fp8_linear_block(qx, qw, sx, sw, bias=None, act=ACT_NONE, residual=None, out_kind=OUT_BF16, sy=None, pre=False,
+                     out=None):
+    """fp8_linear_act for operands with a scale for each block of 128 of K:
+    qx [..., K] and qw [N, K] E4M3 (K a multiple of 16, as fp8_quant_block pads
+    it), sx [..., nb(K)], and sw [nb(N), nb(K)] for 128 x 128 tiles of a weight or
+    [N, nb(K)] for its rows (a weight's gradient: dy's and x's transposed codes).
+    bias, act, residual, out_kind, sy, pre and out as there; no workspace."""
+    r = (_native or _load_native()).linear_block(qx, qw, sx, sw, bias, act, residual, out_kind, sy, pre, out)
+    if r is not None:
+        return r if type(r) is not int else _lib.fail("fp8_linear_block", r)
+    dev = _on_gpu(qx, "qx", _U8)
+    _fit(qw, "qw", _U8, dev)
+    shape = qx.shape
+    if qw.dim() != 2 or shape[-1] != qw.shape[1]:
+        raise ValueError("shapes: qx [..., K], qw [N, K]")
+    N, K = qw.shape
+    M = math.prod(shape[:-1])
+    kb = _blocks(K)
+    _fit(sx, "sx", _F32, dev, M * kb, "one scale per row and block of 128 of qx")
+    _fit(sw, "sw", _F32, dev)
+    if sw.numel() not in (N * kb, _blocks(N) * kb):
+        raise ValueError("sw must hold one scale per row (or 128 rows) and block of 128 of qw")
+    w_rows = sw.numel() != _blocks(N) * kb
+    dtype = _out_dtype(out_kind)
+    sy_ptr = None
+    if out_kind == OUT_FP8 and sy is not None:
+        _fit(sy, "sy", _F32, dev, 1, "exactly one float32")
+        sy_ptr = sy.data_ptr()
+    bias_elem = _fit_float(bias, "bias", dev, N, "N elements")
+    res_elem = _fit_float(residual, "residual", dev, M * N, "M * N elements")
+    out_shape = (*shape[:-1], N)
+    if out is None:
+        out = qx.new_empty(out_shape, dtype=dtype)
+    else:
+        _fit(out, "out", dtype, dev, M * N, "M * N elements")
+    keep = None
+    if pre is not False and pre is not None:
+        if pre is True:
+            keep = qx.new_empty(out_shape, dtype=_BF16)
+        else:
+            keep = pre
+            _fit(keep, "pre", _BF16, dev, M * N, "M * N elements")
+    _lib.call("fp8_linear_block", qx.data_ptr(), qw.data_ptr(), out.data_ptr(), M, N, K, sx.data_ptr(), sw.data_ptr(),
+              1 if w_rows else 0, _ptr(bias), bias_elem, act, _ptr(residual), res_elem, _ptr(keep), out_kind, sy_ptr,
+              _stream(qx))
+    return out if keep is None else (out, keep)
+
+
+def _gates(gate, dev, rows, H):
+    """(number of gates, FP8MOT_ELEM code) of gate [H] or [gates, H]."""
+    if gate is None:
+        return 1, 0
+    elem = _fit_float(gate, "gate", dev, None, None)
+    if gate.dim() not in (1, 2) or gate.shape[-1] != H:
+        raise ValueError("gate must be [H] or [gates, H]")
+    gates = gate.shape[0] if gate.dim() == 2 else 1
+    if gates < 1 or rows % gates:
+        raise ValueError("the number of gates must divide the number of rows")
+    return gates, elem
+
+
+def fp8_residual_norm(x, weight=None, hidden=None, gate=None, post_weight=None, alpha=1.0, eps=1e-6,
+                      out_kind=OUT_BF16, sy=None, stats=False, out=None, stream_out=None):
+    """What stands between two blocks, in one pass over x and hidden [..., H]
+    (BF16 or FP32 each): the root-mean-square norm of the block's output hidden
+    (with ``post_weight``), its gate, the residual addition and the norm before
+    the next block:
+
+        v = hidden * rsqrt(mean(hidden^2) + eps) * post_weight    (or hidden)
+        r = x + alpha * gate * v
+        y = r * rsqrt(mean(r^2) + eps) * weight
+
+    ``gate`` [H], or [gates, H] with a gate for each rows / gates rows.  Returns
+    (y, r): y BF16, FP32 or (at the scale ``sy``) E4M3 codes, or with
+    OUT_FP8_BLOCK a pair (codes, scales) as fp8_quant_block gives; r has x's type
+    and is written to ``stream_out`` (which may be x itself) where that is given.
+    ``stats``: (y, r, rstd, post_rstd), FP32 [...] for the backward pass.
+    Without ``hidden`` it is the norm of x alone, and r None."""
+    if hidden is None and (gate is not None or post_weight is not None or stream_out is not None):
+        raise ValueError("gate, post_weight and stream_out go with hidden")
+    r = (_native or _load_native()).residual_norm(x, weight, hidden, gate, post_weight, alpha, eps, out_kind, sy, stats,
+                                                  out, stream_out)
+    if r is not None:
+        return r if type(r) is not int else _lib.fail("fp8_residual_norm", r)
+    dev = _on_gpu(x, "x")
+    xt = x.dtype
+    n, H = x.numel(), x.shape[-1]
+    rows = n // H if H else 0
+    h_elem = _fit_float(hidden, "hidden", dev, n, "as many elements as x")
+    w_elem = _fit_float(weight, "weight", dev, H, "H elements")
+    p_elem = _fit_float(post_weight, "post_weight", dev, H, "H elements", None if weight is None else weight.dtype)
+    gates, g_elem = _gates(gate, dev, rows, H)
+    scales = sy_ptr = None
+    if out_kind == OUT_FP8_BLOCK:
+        out, scales = _codes(x, x.shape[:-1], H, *((None, None) if out is None else out))
+    else:
+        dtype = _out_dtype(out_kind)
+        if out_kind == OUT_FP8 and sy is not None:
+            _fit(sy, "sy", _F32, dev, 1, "exactly one float32")
+            sy_ptr = sy.data_ptr()
+        if out is None:
+            out = x.new_empty(x.shape, dtype=dtype)
+        else:
+            _fit(out, "out", dtype, dev, n, "as many elements as x")
+    if hidden is not None:
+        if stream_out is None:
+            stream_out = torch.empty_like(x)
+        else:
+            _fit(stream_out, "stream_out", xt, dev, n, "as many elements as x")
+    rstd = post_rstd = None
+    if stats:
+        rstd = x.new_empty(x.shape[:-1], dtype=_F32)
+        if post_weight is not None:
+            post_rstd = torch.empty_like(rstd)
+    _lib.call("fp8_residual_norm", x.data_ptr(), 1 if xt is _F32 else 0, _ptr(hidden), h_elem, _ptr(gate), g_elem,
+              gates, _ptr(post_weight), _ptr(weight), w_elem if weight is not None else p_elem, _ptr(stream_out),
+              out.data_ptr(), out_kind, sy_ptr, _ptr(scales), _ptr(rstd), _ptr(post_rstd), rows, H, alpha, eps,
+              _stream(x))
+    y = out if scales is None else (out, scales)
+    return (y, stream_out, rstd, post_rstd) if stats else (y, stream_out)
+
+
+def fp8_residual_norm_backward_workspace(rows, H, gates=1):
+    return _workspace_bytes("fp8_residual_norm_backward_workspace", rows, H, gates)
+
+
+def fp8_residual_norm_backward(dy, r, weight, rstd, hidden=None, gate=None, post_weight=None, post_rstd=None, alpha=1.0,
+                               dr=None, dx=None, dhidden=None, dweight=None, dgate=None, dpost_weight=None,
+                               workspace=None):
+    """Backward pass of fp8_residual_norm: (dx, dhidden, dweight, dgate,
+    dpost_weight) for the gradients dy [..., H] of y and ``dr`` (r's type) of r.
+    r, rstd and post_rstd are what the forward pass returned with ``stats``
+    (r is x where there was no hidden).  dx has r's type, dhidden hidden's, which
+    dy has to have too; dweight and dpost_weight are FP32 [H], dgate FP32 shaped
+    as gate.  What has no input (dhidden without hidden, ...) is None."""
+    if hidden is None and (gate is not None or post_weight is not None):
+        raise ValueError("gate and post_weight go with hidden")
+    res = (_native or _load_native()).residual_norm_backward(dy, r, weight, rstd, hidden, gate, post_weight, post_rstd,
+                                                             alpha, dr, dx, dhidden, dweight, dgate, dpost_weight,
+                                                             workspace)
+    if res is not None:
+        return res if type(res) is not int else _lib.fail("fp8_residual_norm_backward", res)
+    dev = _on_gpu(r, "r")
+    rt = r.dtype
+    n, H = r.numel(), r.shape[-1]
+    rows = n // H if H else 0
+    if dy is None:
+        raise ValueError("dy must be a tensor")
+    h_elem = _fit_float(dy, "dy", dev, n, "as many elements as r")
+    _fit_float(hidden, "hidden", dev, n, "as many elements as r", dy.dtype)
+    w_elem = _fit_float(weight, "weight", dev, H, "H elements")
+    p_elem = _fit_float(post_weight, "post_weight", dev, H, "H elements", None if weight is None else weight.dtype)
+    gates, g_elem = _gates(gate, dev, rows, H)
+    _fit_float(dr, "dr", dev, n, "as many elements as r", rt)
+    _fit(rstd, "rstd", _F32, dev, rows, "one value per row")
+    if post_weight is not None:
+        _fit(post_rstd, "post_rstd", _F32, dev, rows, "one value per row")
+
+    def made(t, name, there, shape, dtype, what):
+        if not there:
+            if t is not None:
+                raise ValueError(f"{name} has no input whose gradient it could be")
+            return None
+        if t is None:
+            return r.new_empty(shape, dtype=dtype)
+        _fit(t, name, dtype, dev, math.prod(shape), what)
+        return t
+
+    dx = made(dx, "dx", True, r.shape, rt, "as many elements as r")
+    dhidden = made(dhidden, "dhidden", hidden is not None, r.shape, dy.dtype, "as many elements as r")
+    dweight = made(dweight, "dweight", weight is not None, (H,), _F32, "H elements")
+    dgate = made(dgate, "dgate", gate is not None, () if gate is None else gate.shape, _F32, "as many elements as gate")
+    dpost_weight = made(dpost_weight, "dpost_weight", post_weight is not None, (H,), _F32, "H elements")
+    _ws, ws_ptr, ws_bytes = _scratch("fp8_residual_norm_backward_workspace", (rows, H, gates), r, workspace)
+    _lib.call("fp8_residual_norm_backward", dy.data_ptr(), r.data_ptr(), 1 if rt is _F32 else 0, _ptr(hidden), h_elem,
+              _ptr(gate), g_elem, gates, _ptr(post_weight), _ptr(weight), w_elem if weight is not None else p_elem,
+              rstd.data_ptr(), _ptr(post_rstd) if post_weight is not None else None, _ptr(dr), dx.data_ptr(),
+              _ptr(dhidden), _ptr(dgate), _ptr(dpost_weight), _ptr(dweight), rows, H, alpha, ws_ptr, ws_bytes,
+              _stream(r))
+    return dx, dhidden, dweight, dgate, dpost_weight
 
 
 def fp8_linear_into(qx, qw, sx, sw, out, col0=0, out_kind=OUT_BF16, sy=None,

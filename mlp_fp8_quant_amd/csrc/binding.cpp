@@ -1,6 +1,6 @@
 // Native front of the calls that are made once per token or per training
-// step: fp8_linear_act, fp8_linear_act_backward, fp8_layer_norm and
-// fp8_layer_norm_backward.  Marshalling only, like the Python binding
+// step: fp8_linear_act, fp8_layer_norm, the calls with a scale for each block of
+// 128, fp8_residual_norm and the backward passes.  Marshalling only, like the Python binding
 // (api.py), which stays the place of every check and message: a function here
 // takes the common case -- plain contiguous tensors of the right types and
 // sizes on the current device -- and returns None for anything else, which
@@ -267,11 +267,247 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+int64_t blocks128(int64_t n) { return (n + 127) / 128; }
+int64_t code_columns(int64_t n) { return (n + 15) / 16 * 16; }
+
+// Codes and scales of a block-scaled result of `cols` columns, as api.py's
+// _codes: lead's rows of codes, lead_scales' of scales.
+void block_codes(Call& c, PyObject* out, PyObject* scales, at::DimVector lead, at::DimVector lead_scales,
+                 int64_t cols, const at::Tensor& like, at::Tensor* q, at::Tensor* s) {
+  lead.push_back(code_columns(cols));
+  lead_scales.push_back(blocks128(cols));
+  *q = c.output(out, lead, at::kByte, like);
+  *s = c.output(scales, lead_scales, at::kFloat, like);
+}
+
+// (x, tile, transpose, out, scales)
+PyObject* quant_block(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 5) throw Skip();
+    Call c;
+    const at::Tensor& x = c.plain(a[0]);
+    const int elem = Call::elem_of(x);
+    const bool tile = flag(a[1]), transpose = flag(a[2]);
+    if (x.dim() == 0 || x.size(-1) == 0 || ((tile || transpose) && x.dim() != 2)) throw Skip();
+    const int64_t K = x.size(-1), M = x.numel() / K;
+    at::DimVector lead(x.sizes().slice(0, x.dim() - 1));
+    if (transpose) lead = {K};
+    at::DimVector lead_scales(lead);
+    if (tile) lead_scales = {blocks128(lead[0])};
+    at::Tensor q, s;
+    block_codes(c, a[3], a[4], lead, lead_scales, transpose ? M : K, x, &q, &s);
+    const hipStream_t stream = c.stream();
+    const int st = without_gil([&] {
+      return fp8_quant_block(data(x), elem, static_cast<uint8_t*>(data(q)), static_cast<float*>(data(s)), M, K, tile,
+                             transpose, stream);
+    });
+    if (st != FP8MOT_OK) return PyLong_FromLong(st);
+    return tuple_of({q, s});
+  });
+}
+
+// (g, u, out, scales)
+PyObject* silu_mul_block(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 4) throw Skip();
+    Call c;
+    const at::Tensor& g = c.of(a[0], at::kBFloat16);
+    const at::Tensor& u = c.of(a[1], at::kBFloat16);
+    if (g.dim() == 0 || g.size(-1) == 0 || g.sizes() != u.sizes()) throw Skip();
+    const int64_t K = g.size(-1), M = g.numel() / K;
+    const at::DimVector lead(g.sizes().slice(0, g.dim() - 1));
+    at::Tensor q, s;
+    block_codes(c, a[2], a[3], lead, lead, K, g, &q, &s);
+    const hipStream_t stream = c.stream();
+    const int st = without_gil([&] {
+      return silu_mul_2in_block(static_cast<const uint16_t*>(data(g)), static_cast<const uint16_t*>(data(u)),
+                                static_cast<uint8_t*>(data(q)), static_cast<float*>(data(s)), M, K, stream);
+    });
+    if (st != FP8MOT_OK) return PyLong_FromLong(st);
+    return tuple_of({q, s});
+  });
+}
+
+// (qx, qw, sx, sw, bias, act, residual, out_kind, sy, pre, out)
+PyObject* linear_block(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 11) throw Skip();
+    Call c;
+    const at::Tensor& qx = c.of(a[0], at::kByte);
+    const at::Tensor& qw = c.of(a[1], at::kByte);
+    if (qw.dim() != 2 || qx.dim() < 1 || qx.size(-1) != qw.size(1)) throw Skip();
+    const int64_t N = qw.size(0), K = qw.size(1);
+    if (K == 0) throw Skip();
+    const int64_t M = qx.numel() / K, kb = blocks128(K);
+    const float* sx = c.scale(a[2], M * kb);
+    const at::Tensor& sw = c.of(a[3], at::kFloat);
+    const bool w_rows = sw.numel() != blocks128(N) * kb;
+    if (w_rows && sw.numel() != N * kb) throw Skip();
+    int bias_elem, res_elem;
+    const void* bias = c.floats(a[4], N, &bias_elem);
+    const int act = small_int(a[5]), kind = small_int(a[7]);
+    const void* residual = c.floats(a[6], M * N, &res_elem);
+    at::ScalarType type;
+    if (!out_type(kind, &type)) throw Skip();
+    const float* sy = kind == FP8MOT_OUT_FP8 ? c.scale(a[8], 1) : nullptr;
+    at::DimVector shape(qx.sizes());
+    shape.back() = N;
+    const at::Tensor out = c.output(a[10], shape, type, qx);
+    at::Tensor pre;
+    if (a[9] == Py_True) pre = at::empty(shape, qx.options().dtype(at::kBFloat16));
+    else if (a[9] != Py_False && a[9] != Py_None) pre = c.of(a[9], at::kBFloat16, M * N);
+    const hipStream_t stream = c.stream();
+    const int st = without_gil([&] {
+      return fp8_linear_block(static_cast<const uint8_t*>(data(qx)), static_cast<const uint8_t*>(data(qw)), data(out),
+                              M, N, K, sx, static_cast<const float*>(data(sw)), w_rows, bias, bias_elem, act, residual,
+                              res_elem, static_cast<uint16_t*>(data(pre)), kind, sy, stream);
+    });
+    if (st != FP8MOT_OK) return PyLong_FromLong(st);
+    return pre.defined() ? tuple_of({out, pre}) : THPVariable_Wrap(out);
+  });
+}
+
+// gate [H] or [gates, H], or None (1 gate)
+const void* gate_of(Call& c, PyObject* o, int64_t rows, int64_t H, int64_t* gates, int* elem) {
+  *gates = 1;
+  *elem = FP8MOT_ELEM_BF16;
+  if (o == Py_None) return nullptr;
+  const at::Tensor& t = c.plain(o);
+  *elem = Call::elem_of(t);
+  if ((t.dim() != 1 && t.dim() != 2) || t.size(-1) != H) throw Skip();
+  if (t.dim() == 2) *gates = t.size(0);
+  if (*gates < 1 || rows % *gates != 0) throw Skip();
+  return t.const_data_ptr();
+}
+float real(PyObject* o) {
+  if (!PyFloat_Check(o)) throw Skip();
+  return (float)PyFloat_AS_DOUBLE(o);
+}
+PyObject* wrap_or_none(const at::Tensor& t) {
+  if (t.defined()) return THPVariable_Wrap(t);
+  Py_RETURN_NONE;
+}
+
+// (x, weight, hidden, gate, post_weight, alpha, eps, out_kind, sy, stats, out, stream_out)
+PyObject* residual_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 12) throw Skip();
+    Call c;
+    const at::Tensor& x = c.plain(a[0]);
+    const int x_elem = Call::elem_of(x);
+    if (x.dim() == 0 || x.size(-1) == 0) throw Skip();
+    const int64_t H = x.size(-1), rows = x.numel() / H;
+    if (rows == 0) throw Skip();   // (a NULL pointer below is None)
+    int w_elem, h_elem, g_elem, p_elem;
+    const void* w = c.floats(a[1], H, &w_elem);
+    const void* h = c.floats(a[2], x.numel(), &h_elem);
+    int64_t gates;
+    const void* gate = gate_of(c, a[3], rows, H, &gates, &g_elem);
+    const void* post = c.floats(a[4], H, &p_elem);
+    if (w != nullptr && post != nullptr && w_elem != p_elem) throw Skip();
+    const float alpha = real(a[5]), eps = real(a[6]);
+    const int kind = small_int(a[7]);
+    const float* sy = nullptr;
+    at::Tensor y, scales, r, rstd, post_rstd;
+    const at::DimVector lead(x.sizes().slice(0, x.dim() - 1));
+    if (kind == FP8MOT_OUT_FP8_BLOCK) {
+      if (a[10] != Py_None) throw Skip();
+      block_codes(c, Py_None, Py_None, lead, lead, H, x, &y, &scales);
+    } else {
+      at::ScalarType type;
+      if (!out_type(kind, &type)) throw Skip();
+      if (kind == FP8MOT_OUT_FP8) sy = c.scale(a[8], 1);
+      y = c.output(a[10], x.sizes(), type, x);
+    }
+    if (h != nullptr) r = c.output(a[11], x.sizes(), x.scalar_type(), x);
+    const bool stats = flag(a[9]);
+    if (stats) {
+      rstd = at::empty(lead, x.options().dtype(at::kFloat));
+      if (post != nullptr) post_rstd = at::empty(lead, x.options().dtype(at::kFloat));
+    }
+    const hipStream_t stream = c.stream();
+    const int st = without_gil([&] {
+      return fp8_residual_norm(data(x), x_elem, h, h_elem, gate, g_elem, gates, post, w,
+                               w != nullptr ? w_elem : p_elem, data(r), data(y), kind, sy,
+                               static_cast<float*>(data(scales)), static_cast<float*>(data(rstd)),
+                               static_cast<float*>(data(post_rstd)), rows, H, alpha, eps, stream);
+    });
+    if (st != FP8MOT_OK) return PyLong_FromLong(st);
+    PyObject* result = PyTuple_New(stats ? 4 : 2);
+    if (result == nullptr) throw Skip();
+    PyTuple_SET_ITEM(result, 0, kind == FP8MOT_OUT_FP8_BLOCK ? tuple_of({y, scales}) : THPVariable_Wrap(y));
+    PyTuple_SET_ITEM(result, 1, wrap_or_none(r));
+    if (stats) {
+      PyTuple_SET_ITEM(result, 2, wrap_or_none(rstd));
+      PyTuple_SET_ITEM(result, 3, wrap_or_none(post_rstd));
+    }
+    return result;
+  });
+}
+
+// (dy, r, weight, rstd, hidden, gate, post_weight, post_rstd, alpha, dr, dx, dhidden, dweight, dgate, dpost_weight,
+//  workspace)
+PyObject* residual_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 16 || a[0] == Py_None) throw Skip();
+    Call c;
+    const at::Tensor& r = c.plain(a[1]);
+    const int r_elem = Call::elem_of(r);
+    if (r.dim() == 0 || r.size(-1) == 0) throw Skip();
+    const int64_t H = r.size(-1), rows = r.numel() / H;
+    if (rows == 0) throw Skip();   // (a NULL pointer below is None)
+    const at::Tensor& dy = c.plain(a[0]);
+    const int h_elem = Call::elem_of(dy);
+    if (dy.numel() != r.numel()) throw Skip();
+    int w_elem, p_elem, g_elem;
+    const void* w = c.floats(a[2], H, &w_elem);
+    const float* rstd = c.scale(a[3], rows);
+    const void* h = a[4] == Py_None ? nullptr : data(c.of(a[4], dy.scalar_type(), r.numel()));
+    int64_t gates;
+    const void* gate = gate_of(c, a[5], rows, H, &gates, &g_elem);
+    const void* post = c.floats(a[6], H, &p_elem);
+    if (w != nullptr && post != nullptr && w_elem != p_elem) throw Skip();
+    const float* post_rstd = post != nullptr ? c.scale(a[7], rows) : nullptr;
+    const float alpha = real(a[8]);
+    const void* dr = a[9] == Py_None ? nullptr : data(c.of(a[9], r.scalar_type(), r.numel()));
+    const at::Tensor dx = c.output(a[10], r.sizes(), r.scalar_type(), r);
+    at::Tensor dh, dw, dgate, dpost;
+    if (h != nullptr) dh = c.output(a[11], r.sizes(), dy.scalar_type(), r);
+    else if (a[11] != Py_None) throw Skip();
+    if (w != nullptr) dw = c.output(a[12], {H}, at::kFloat, r);
+    else if (a[12] != Py_None) throw Skip();
+    if (gate != nullptr) dgate = c.output(a[13], THPVariable_Unpack(a[5]).sizes(), at::kFloat, r);
+    else if (a[13] != Py_None) throw Skip();
+    if (post != nullptr) dpost = c.output(a[14], {H}, at::kFloat, r);
+    else if (a[14] != Py_None) throw Skip();
+    const at::Tensor ws = c.scratch(a[15], fp8_residual_norm_backward_workspace(rows, H, gates), r);
+    const hipStream_t stream = c.stream();
+    const int st = without_gil([&] {
+      return fp8_residual_norm_backward(data(dy), data(r), r_elem, h, h_elem, gate, g_elem, gates, post, w,
+                                        w != nullptr ? w_elem : p_elem, rstd, post_rstd, dr, data(dx), data(dh),
+                                        static_cast<float*>(data(dgate)), static_cast<float*>(data(dpost)),
+                                        static_cast<float*>(data(dw)), rows, H, alpha, data(ws),
+                                        ws.defined() ? (size_t)ws.numel() : 0, stream);
+    });
+    if (st != FP8MOT_OK) return PyLong_FromLong(st);
+    PyObject* result = PyTuple_New(5);
+    if (result == nullptr) throw Skip();
+    const at::Tensor* outs[5] = {&dx, &dh, &dw, &dgate, &dpost};
+    for (int i = 0; i < 5; ++i) PyTuple_SET_ITEM(result, i, wrap_or_none(*outs[i]));
+    return result;
+  });
+}
+
 PyMethodDef methods[] = {
     {"linear_act", (PyCFunction)(void (*)(void))linear_act, METH_FASTCALL, nullptr},
     {"linear_act_backward", (PyCFunction)(void (*)(void))linear_act_backward, METH_FASTCALL, nullptr},
     {"layer_norm", (PyCFunction)(void (*)(void))layer_norm, METH_FASTCALL, nullptr},
     {"layer_norm_backward", (PyCFunction)(void (*)(void))layer_norm_backward, METH_FASTCALL, nullptr},
+    {"quant_block", (PyCFunction)(void (*)(void))quant_block, METH_FASTCALL, nullptr},
+    {"silu_mul_block", (PyCFunction)(void (*)(void))silu_mul_block, METH_FASTCALL, nullptr},
+    {"linear_block", (PyCFunction)(void (*)(void))linear_block, METH_FASTCALL, nullptr},
+    {"residual_norm", (PyCFunction)(void (*)(void))residual_norm, METH_FASTCALL, nullptr},
+    {"residual_norm_backward", (PyCFunction)(void (*)(void))residual_norm_backward, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

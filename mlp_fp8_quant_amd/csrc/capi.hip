@@ -116,6 +116,9 @@ bool rows_ok(int64_t rows, int64_t cols) {
   return rows >= 0 && cols >= 0 && rows <= INT32_MAX && cols <= kMaxColumns;
 }
 int64_t elem_bytes(int e) { return e == FP8MOT_ELEM_F32 ? 4 : 2; }
+// Blocks of 128 that cover n, and the columns of a row of n codes with its padding.
+int64_t blocks128(int64_t n) { return (n + 127) / 128; }
+int64_t code_columns(int64_t n) { return (n + 15) / 16 * 16; }
 
 // A tensor of a call.  An output must lie apart from every other tensor of the
 // call, but for the inputs that it may be itself: kernels read those before
@@ -418,6 +421,195 @@ int fp8_layer_norm_backward(const void* dy, int dy_elem, const void* x, int x_el
   g.mean = mean; g.rstd = rstd; g.dres = dres; g.dx = dx;
   g.rows = rows; g.H = H;
   return hip_status(launch_layer_norm_backward(g, dweight, dbias, static_cast<float*>(ws), stream));
+}
+
+int fp8_quant_block(const void* x, int x_elem, uint8_t* q, float* d_scales, int64_t M,
+                    int64_t K, int tile, int transpose, hipStream_t stream) {
+  if (!elem_ok(x_elem) || !rows_ok(M, K) || (tile != 0 && tile != 1) || (transpose != 0 && transpose != 1))
+    return FP8MOT_ERR_INVALID_ARG;
+  if (M == 0 || K == 0) return FP8MOT_OK;
+  if (x == nullptr || q == nullptr || d_scales == nullptr) return FP8MOT_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(q)) return FP8MOT_ERR_MISALIGNED;
+  {
+    const int64_t rows = transpose ? K : M, cols = transpose ? M : K;
+    const Span sx = {x, M * K * elem_bytes(x_elem)}, sq = {q, rows * code_columns(cols)};
+    const Span sc = {d_scales, (tile ? blocks128(rows) : rows) * blocks128(cols) * 4};
+    if (!apart(sq, {sx, sc}) || !apart(sc, sx)) return FP8MOT_ERR_INVALID_ARG;
+  }
+  int cus = 0;
+  int st = current_device(&cus);
+  if (st != FP8MOT_OK) return st;
+  return hip_status(launch_quant_block(x, x_elem == FP8MOT_ELEM_F32, q, d_scales, M, K, tile, transpose, stream));
+}
+
+int silu_mul_2in_block(const uint16_t* g, const uint16_t* u, uint8_t* q, float* d_scales,
+                       int64_t M, int64_t K, hipStream_t stream) {
+  if (!rows_ok(M, K)) return FP8MOT_ERR_INVALID_ARG;
+  if (M == 0 || K == 0) return FP8MOT_OK;
+  if (g == nullptr || u == nullptr || q == nullptr || d_scales == nullptr) return FP8MOT_ERR_INVALID_ARG;
+  if (!aligned16(g) || !aligned16(u) || !aligned16(q)) return FP8MOT_ERR_MISALIGNED;
+  {
+    const Span sg = {g, M * K * 2}, su = {u, M * K * 2}, sq = {q, M * code_columns(K)};
+    const Span sc = {d_scales, M * blocks128(K) * 4};
+    if (!apart(sq, {sg, su, sc}) || !apart(sc, {sg, su})) return FP8MOT_ERR_INVALID_ARG;
+  }
+  int cus = 0;
+  int st = current_device(&cus);
+  if (st != FP8MOT_OK) return st;
+  return hip_status(launch_silu_mul_block(g, u, q, d_scales, M, K, stream));
+}
+
+int fp8_linear_block(const uint8_t* qx, const uint8_t* qw, void* y, int64_t M, int64_t N,
+                     int64_t K, const float* d_sx, const float* d_sw, int w_rows,
+                     const void* bias, int bias_elem, int act, const void* residual,
+                     int residual_elem, uint16_t* pre, int out_kind, const float* d_sy,
+                     hipStream_t stream) {
+  // an empty operand has no scales: any pointer will do for the check
+  const float none = 0.0f;
+  const bool empty = M == 0 || N == 0 || K == 0;
+  int st = check_linear(qx, qw, y, M, N, K, empty ? &none : d_sx, empty ? &none : d_sw, out_kind, d_sy,
+                        FP8MOT_ACC_EXACT);
+  if (st != FP8MOT_OK) return st;
+  if ((w_rows != 0 && w_rows != 1) || !elem_ok(bias_elem) || !elem_ok(residual_elem) || !act_ok(act))
+    return FP8MOT_ERR_INVALID_ARG;
+  // the widest of y, residual and pre addresses a tile's rows like y
+  const int esz = residual != nullptr && residual_elem == FP8MOT_ELEM_F32 ? 4 : 2;
+  if (!gemm_sizes_ok(M, N, K, N, esz)) return FP8MOT_ERR_INVALID_ARG;
+  if (M == 0 || N == 0) return FP8MOT_OK;
+  if (!aligned16(bias) || !aligned16(residual) || !aligned16(pre)) return FP8MOT_ERR_MISALIGNED;
+  {
+    const int64_t kb = blocks128(K);
+    const Span sy = {y, M * N * out_bytes(out_kind)}, sp = {pre, M * N * 2};
+    const Span sr = {residual, M * N * elem_bytes(residual_elem)}, sb = {bias, N * elem_bytes(bias_elem)};
+    const Span x = {qx, M * K}, w = {qw, N * K}, px = {d_sx, M * kb * 4};
+    const Span pw = {d_sw, (w_rows ? N : blocks128(N)) * kb * 4};
+    const Span scale = {out_kind == FP8MOT_OUT_FP8 ? d_sy : nullptr, 4};
+    if (!apart(sy, {sp, sb, x, w, px, pw, scale}) || !same_or_apart(sy, sr) ||
+        !apart(sp, {sr, sb, x, w, px, pw, scale}))
+      return FP8MOT_ERR_INVALID_ARG;
+  }
+  int cus = 0;
+  st = current_device(&cus);
+  if (st != FP8MOT_OK) return st;
+  LinearActArgs g{};
+  g.qx = qx; g.qw = qw; g.y = y;
+  g.M = M; g.N = N; g.K = K;
+  g.sx = d_sx; g.sw = d_sw; g.row_scales = w_rows;
+  g.bias = bias; g.bias_f32 = bias_elem == FP8MOT_ELEM_F32;
+  g.act = act;
+  g.residual = residual; g.residual_f32 = residual_elem == FP8MOT_ELEM_F32;
+  g.pre = pre;
+  g.out_kind = out_kind; g.sy = d_sy;
+  return hip_status(launch_linear_block(g, cus, stream));
+}
+
+int fp8_residual_norm(const void* x, int x_elem, const void* hidden, int h_elem,
+                      const void* gate, int gate_elem, int64_t gates,
+                      const void* post_weight, const void* weight, int w_elem, void* r,
+                      void* y, int out_kind, const float* d_sy, float* d_scales, float* rstd,
+                      float* post_rstd, int64_t rows, int64_t H, float alpha, float eps,
+                      hipStream_t stream) {
+  if (!elem_ok(x_elem) || !elem_ok(h_elem) || !elem_ok(gate_elem) || !elem_ok(w_elem)) return FP8MOT_ERR_INVALID_ARG;
+  if (out_kind < 0 || out_kind > FP8MOT_OUT_FP8_BLOCK) return FP8MOT_ERR_INVALID_ARG;
+  if (out_kind == FP8MOT_OUT_FP8 && d_sy == nullptr) return FP8MOT_ERR_UNSUPPORTED;
+  if (!rows_ok(rows, H) || !std::isfinite(eps) || eps < 0.0f || !std::isfinite(alpha)) return FP8MOT_ERR_INVALID_ARG;
+  if (hidden == nullptr && rows > 0 && H > 0 && (gate != nullptr || post_weight != nullptr || r != nullptr))
+    return FP8MOT_ERR_INVALID_ARG;
+  if (gate != nullptr && (gates < 1 || rows % gates != 0)) return FP8MOT_ERR_INVALID_ARG;
+  if (rows == 0 || H == 0) return FP8MOT_OK;
+  const bool block = out_kind == FP8MOT_OUT_FP8_BLOCK;
+  if (x == nullptr || y == nullptr || (hidden != nullptr && r == nullptr) || (block && d_scales == nullptr))
+    return FP8MOT_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(hidden) || !aligned16(gate) || !aligned16(post_weight) || !aligned16(weight) ||
+      !aligned16(r) || !aligned16(y))
+    return FP8MOT_ERR_MISALIGNED;
+  {
+    const Span sx = {x, rows * H * elem_bytes(x_elem)}, sh = {hidden, rows * H * elem_bytes(h_elem)};
+    const Span sg = {gate, gate != nullptr ? gates * H * elem_bytes(gate_elem) : 0};
+    const Span sp = {post_weight, H * elem_bytes(w_elem)}, sw = {weight, H * elem_bytes(w_elem)};
+    const Span sr = {r, sx.bytes}, sy = {y, block ? rows * code_columns(H) : rows * H * out_bytes(out_kind)};
+    const Span sc = {block ? d_scales : nullptr, rows * blocks128(H) * 4};
+    const Span st = {rstd, rows * 4}, su = {post_weight != nullptr ? post_rstd : nullptr, rows * 4};
+    const Span scale = {out_kind == FP8MOT_OUT_FP8 ? d_sy : nullptr, 4};
+    if (!same_or_apart(sr, sx) || !apart(sr, {sh, sg, sp, sw, sy, sc, st, su, scale}) ||
+        !(hidden == nullptr ? same_or_apart(sy, sx) : apart(sy, sx)) || !apart(sy, {sh, sg, sp, sw, sc, st, su, scale}) ||
+        !apart(sc, {sx, sh, sg, sp, sw, st, su}) || !apart(st, {sx, sh, sg, sp, sw, su, scale}) ||
+        !apart(su, {sx, sh, sg, sp, sw, scale}))
+      return FP8MOT_ERR_INVALID_ARG;
+  }
+  int cus = 0;
+  int st = current_device(&cus);
+  if (st != FP8MOT_OK) return st;
+  ResidualNormArgs g{};
+  g.x = x; g.x_f32 = x_elem == FP8MOT_ELEM_F32;
+  g.h = hidden; g.h_f32 = hidden != nullptr && h_elem == FP8MOT_ELEM_F32;
+  g.gate = gate; g.gate_f32 = gate_elem == FP8MOT_ELEM_F32;
+  g.gate_rows = gate != nullptr ? rows / gates : rows;
+  g.post_w = post_weight; g.w = weight; g.w_f32 = w_elem == FP8MOT_ELEM_F32;
+  g.r = r; g.y = y; g.out_kind = out_kind; g.sy = d_sy; g.scales = d_scales;
+  g.rstd = rstd; g.post_rstd = post_rstd;
+  g.rows = rows; g.H = H; g.alpha = alpha; g.eps = eps;
+  return hip_status(launch_residual_norm(g, stream));
+}
+
+size_t fp8_residual_norm_backward_workspace(int64_t rows, int64_t H, int64_t gates) {
+  if (!rows_ok(rows, H) || gates < 1 || rows % gates != 0) return 0;
+  return (size_t)residual_norm_backward_floats(rows, H, gates) * sizeof(float);
+}
+
+int fp8_residual_norm_backward(const void* dy, const void* r, int r_elem, const void* hidden,
+                               int h_elem, const void* gate, int gate_elem, int64_t gates,
+                               const void* post_weight, const void* weight, int w_elem,
+                               const float* rstd, const float* post_rstd, const void* dr,
+                               void* dx, void* dhidden, float* dgate, float* dpost_weight,
+                               float* dweight, int64_t rows, int64_t H, float alpha, void* ws,
+                               size_t ws_bytes, hipStream_t stream) {
+  if (!elem_ok(r_elem) || !elem_ok(h_elem) || !elem_ok(gate_elem) || !elem_ok(w_elem) || !rows_ok(rows, H) ||
+      !std::isfinite(alpha))
+    return FP8MOT_ERR_INVALID_ARG;
+  if (gate == nullptr) gates = 1;
+  if (gates < 1 || rows % gates != 0) return FP8MOT_ERR_INVALID_ARG;
+  if (H == 0) return FP8MOT_OK;
+  if ((dgate != nullptr && gate == nullptr) || (dpost_weight != nullptr && post_weight == nullptr))
+    return FP8MOT_ERR_INVALID_ARG;
+  if (rows > 0) {
+    if (dy == nullptr || r == nullptr || rstd == nullptr || dx == nullptr) return FP8MOT_ERR_INVALID_ARG;
+    if (hidden == nullptr ? gate != nullptr || post_weight != nullptr || dhidden != nullptr : dhidden == nullptr)
+      return FP8MOT_ERR_INVALID_ARG;
+    if (post_weight != nullptr && post_rstd == nullptr) return FP8MOT_ERR_INVALID_ARG;
+  }
+  if (!aligned16(dy) || !aligned16(r) || !aligned16(hidden) || !aligned16(gate) || !aligned16(post_weight) ||
+      !aligned16(weight) || !aligned16(dr) || !aligned16(dx) || !aligned16(dhidden) || !aligned16(dgate) ||
+      !aligned16(dpost_weight) || !aligned16(dweight))
+    return FP8MOT_ERR_MISALIGNED;
+  const size_t need = fp8_residual_norm_backward_workspace(rows, H, gates);
+  if (need > 0 && (ws == nullptr || !aligned16(ws) || ws_bytes < need)) return FP8MOT_ERR_WORKSPACE;
+  if (rows == 0 && dgate == nullptr && dpost_weight == nullptr && dweight == nullptr) return FP8MOT_OK;
+  {
+    const int64_t nx = rows * H * elem_bytes(r_elem), nh = rows * H * elem_bytes(h_elem);
+    const Span sy = {dy, nh}, sr = {r, nx}, sh = {hidden, nh}, sd = {dr, nx}, sx = {dx, nx}, so = {dhidden, nh};
+    const Span sg = {gate, gates * H * elem_bytes(gate_elem)}, sp = {post_weight, H * elem_bytes(w_elem)};
+    const Span sw = {weight, H * elem_bytes(w_elem)}, st = {rstd, rows * 4}, su = {post_rstd, rows * 4};
+    const Span og = {dgate, gates * H * 4}, op = {dpost_weight, H * 4}, ow = {dweight, H * 4};
+    if (!same_or_apart(sx, sy) || !same_or_apart(sx, sr) || !same_or_apart(sx, sd) ||
+        !apart(sx, {sh, so, sg, sp, sw, st, su, og, op, ow}) || !same_or_apart(so, sy) || !same_or_apart(so, sh) ||
+        !apart(so, {sr, sd, sg, sp, sw, st, su, og, op, ow}) || !apart(og, {sy, sr, sh, sd, sg, sp, sw, st, su, op, ow}) ||
+        !apart(op, {sy, sr, sh, sd, sg, sp, sw, st, su, ow}) || !apart(ow, {sy, sr, sh, sd, sg, sp, sw, st, su}) ||
+        !apart({ws, (int64_t)need}, {sy, sr, sh, sd, sx, so, sg, sp, sw, st, su, og, op, ow}))
+      return FP8MOT_ERR_INVALID_ARG;
+  }
+  int cus = 0;
+  int st = current_device(&cus);
+  if (st != FP8MOT_OK) return st;
+  ResidualNormBwdArgs g{};
+  g.dy = dy; g.r = r; g.x_f32 = r_elem == FP8MOT_ELEM_F32;
+  g.h = hidden; g.h_f32 = h_elem == FP8MOT_ELEM_F32;
+  g.gate = gate; g.gate_f32 = gate_elem == FP8MOT_ELEM_F32; g.gates = gates;
+  g.post_w = post_weight; g.w = weight; g.w_f32 = w_elem == FP8MOT_ELEM_F32;
+  g.rstd = rstd; g.post_rstd = post_rstd; g.dr = dr;
+  g.dx = dx; g.dh = dhidden; g.dw = dweight; g.dgate = dgate; g.dpost = dpost_weight;
+  g.rows = rows; g.H = H; g.alpha = alpha;
+  return hip_status(launch_residual_norm_backward(g, static_cast<float*>(ws), stream));
 }
 
 int fp8_quant_per_row(const uint16_t* x, uint8_t* q, float* d_scales,

@@ -81,5 +81,16 @@ __device__ __forceinline__ void copy_to_lds(v4i rsrc, uint32_t lds_addr, int vof
       : "memory", "m0");
 }
 
+// The same with four bytes per lane, at lds_addr + 4 * i.
+__device__ __forceinline__ void copy4_to_lds(v4i rsrc, uint32_t lds_addr, int voff, int soff) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dword %1, %2, %3 offen lds"
+      :
+      : "s"(lds_addr), "v"(voff), "s"(rsrc), "s"(soff)
+      : "memory", "m0");
+}
+
 }  // namespace tile
 }  // namespace fp8mot

@@ -148,6 +148,18 @@ hipError_t launch_linear_act(const LinearActArgs& g, int accum, float* ws, int n
 hipError_t launch_linear_tile(const LinearActArgs& g, const LinearPlan& p, int accum, float* part,
                               int num_cus, hipStream_t stream);
 
+// FP8 Linear whose operands have a scale for each block of 128 of K
+// (fp8_linear_block): a.sx [M, KB], a.sw [N, KB] with a.row_scales, else
+// [ceil(N / 128), KB]; KB = ceil(K / 128).
+hipError_t launch_linear_block(const LinearActArgs& g, int num_cus, hipStream_t stream);
+
+// Codes and scales of x [M, K] with a scale for each block of 128 (fp8_quant_block).
+hipError_t launch_quant_block(const void* x, int x_f32, uint8_t* q, float* scales, int64_t M, int64_t K, int tile,
+                              int transpose, hipStream_t stream);
+// The same, blocks of a row's columns, of g / (1 + exp(-g)) u.
+hipError_t launch_silu_mul_block(const uint16_t* g, const uint16_t* u, uint8_t* q, float* scales, int64_t rows,
+                                 int64_t K, hipStream_t stream);
+
 // dz = dy act'(pre), dbias[n] = sum_m dz; part: [act_backward_partials(M, N), N] floats.
 int64_t act_backward_partials(int64_t M, int64_t N);
 hipError_t launch_act_backward(const uint16_t* dy, const uint16_t* pre, int act, uint16_t* dz,
@@ -192,5 +204,57 @@ struct LayerNormBwdArgs {
 int64_t layer_norm_backward_partials(int64_t rows, int64_t H);
 hipError_t launch_layer_norm_backward(const LayerNormBwdArgs& g, float* dw, float* db, float* part,
                                       hipStream_t stream);
+
+// Norms before and after a block, its gate and residual scale
+// (fp8_residual_norm); H > 0, rows > 0.
+struct ResidualNormArgs {
+  const void* x;          // [rows, H], FP32 if x_f32, else BF16
+  int x_f32;
+  const void* h;          // [rows, H] or NULL
+  int h_f32;
+  const void* gate;       // [gates, H] or NULL
+  int gate_f32;
+  int64_t gate_rows;      // rows that share a gate: rows / gates
+  const void* post_w;     // [H] or NULL: no norm of h
+  const void* w;          // [H] or NULL
+  int w_f32;              // element type of post_w and w
+  void* r;                // [rows, H] of x's type; NULL without h
+  void* y;                // [rows, H], kind out_kind (fp8mot_out)
+  int out_kind;
+  const float* sy;        // FP8 output scale
+  float* scales;          // [rows, ceil(H / 128)] (block output)
+  float* rstd;            // [rows] or NULL
+  float* post_rstd;       // [rows] or NULL
+  int64_t rows, H;
+  float alpha, eps;
+};
+hipError_t launch_residual_norm(const ResidualNormArgs& g, hipStream_t stream);
+
+struct ResidualNormBwdArgs {
+  const void* dy;         // [rows, H], h's element type
+  const void* r;          // [rows, H], FP32 if x_f32, else BF16
+  int x_f32;              // element type of r, dr and dx
+  const void* h;          // [rows, H] or NULL
+  int h_f32;              // element type of dy, h and dh
+  const void* gate;       // [gates, H] or NULL
+  int gate_f32;
+  int64_t gates;          // 1 without a gate
+  const void* post_w;     // [H] or NULL
+  const void* w;          // [H] or NULL
+  int w_f32;
+  const float* rstd;      // [rows]
+  const float* post_rstd; // [rows], with post_w
+  const void* dr;         // [rows, H] or NULL
+  void* dx;               // [rows, H]
+  void* dh;               // [rows, H], with h
+  float* dw;              // [H] or NULL
+  float* dgate;           // [gates, H] or NULL
+  float* dpost;           // [H] or NULL
+  int64_t rows, H;
+  float alpha;
+};
+// Floats of workspace.
+int64_t residual_norm_backward_floats(int64_t rows, int64_t H, int64_t gates);
+hipError_t launch_residual_norm_backward(const ResidualNormBwdArgs& g, float* ws, hipStream_t stream);
 
 }  // namespace fp8mot

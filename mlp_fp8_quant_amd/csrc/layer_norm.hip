@@ -27,23 +27,6 @@ namespace {
 
 using namespace rows;
 
-// Sum over the threads that share a row, the same in each: TC = 16 or 64
-// lanes, or (0) the whole workgroup.  red: 16 floats of LDS that no other sum
-// in flight uses.
-template <int TC>
-__device__ __forceinline__ float row_sum(float v, float* red) {
-  if constexpr (TC == 16) return sum16(v);
-  v = wave_sum(v);
-  if constexpr (TC == 0) {
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    const int waves = blockDim.x >> 6;
-    v = red[0];
-    for (int w = 1; w < waves; ++w) v = __fadd_rn(v, red[w]);
-  }
-  return v;
-}
-
 // Whether a row's mean needs the correction, from the mean square d2 of the
 // differences from it: below four standard deviations some 2^-24 of it is less
 // than the other roundings of (x - mean) rstd.  Equal in the threads that share a
@@ -56,24 +39,6 @@ __device__ __forceinline__ bool off_centre(float mean, float d2, float eps) {
 __device__ __forceinline__ float centred(float d2, float off) {
   return __builtin_fmaxf(__builtin_fmaf(-off, off, d2), 0.0f);
 }
-
-// A tree over eight values: fewer roundings in a row than one after another.
-__device__ __forceinline__ float sum8(const float* f) {
-  return __fadd_rn(__fadd_rn(__fadd_rn(f[0], f[1]), __fadd_rn(f[2], f[3])),
-                   __fadd_rn(__fadd_rn(f[4], f[5]), __fadd_rn(f[6], f[7])));
-}
-
-// A sum that keeps what its additions round off (of many terms in one thread,
-// where the roundings of a plain sum would add up: 2e-5 of rstd at 2^26
-// columns).
-struct LongSum {
-  float s = 0.0f, lost = 0.0f;
-  __device__ __forceinline__ void add(float v) {
-    const float y = __fadd_rn(v, -lost), t = __fadd_rn(s, y);
-    lost = __fadd_rn(__fadd_rn(t, -s), -y);
-    s = t;
-  }
-};
 
 __device__ __forceinline__ void emit8(const LayerNormArgs& g, int64_t base, int64_t i, float rs, float* y) {
   if (g.out_kind == 0) {

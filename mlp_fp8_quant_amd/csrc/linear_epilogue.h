@@ -145,13 +145,18 @@ struct Epilogue {
   float alpha;   // s_x s_w (without row scales)
   float rs;      // 1 / s_y, correctly rounded (FP8 output)
 };
-__device__ __forceinline__ Epilogue open_epilogue(const LinearActArgs& g, int64_t m0) {
+__device__ __forceinline__ Epilogue open_outputs(const LinearActArgs& g, int64_t m0) {   // of sums scaled already
   Epilogue e;
   e.y = rows_of(g.y, m0, g.M, g.N, g.out_kind == 0 ? 2 : (g.out_kind == 1 ? 1 : 4));
   e.residual = rows_of(g.residual, m0, g.M, g.N, g.residual_f32 ? 4 : 2);
   e.pre = rows_of(g.pre, m0, g.M, g.N, 2);
-  e.alpha = g.row_scales ? 0.0f : __fmul_rn(*g.sx, *g.sw);
+  e.alpha = 1.0f;
   e.rs = g.out_kind == 1 ? 1.0f / *g.sy : 0.0f;
+  return e;
+}
+__device__ __forceinline__ Epilogue open_epilogue(const LinearActArgs& g, int64_t m0) {
+  Epilogue e = open_outputs(g, m0);
+  e.alpha = g.row_scales ? 0.0f : __fmul_rn(*g.sx, *g.sw);
   return e;
 }
 

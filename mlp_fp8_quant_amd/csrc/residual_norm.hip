@@ -1,0 +1,644 @@
+// The norms before and after a block, fused with the block's gate and residual
+// scale, and their backward pass (declared in include/fp8mot.h as
+// fp8_residual_norm and fp8_residual_norm_backward).
+//
+//   forward   v = h rs_h pw (or h),  rs_h = 1 / sqrt(sum h^2 / H + eps)
+//             r = x + alpha gate v                    the residual stream
+//             y = r rs w,  rs = 1 / sqrt(sum r^2 / H + eps)
+//   backward  g = dy w,  n = r rs,  z = h rs_h (or h)
+//             dx = rs (g - n sum(g n) / H) + dr,  p = alpha gate pw dx
+//             dh = rs_h (p - z sum(p z) / H)  (or p)
+//             dw = sum_rows dy n,  A = sum of dx z over a gate's rows:
+//             dgate = alpha pw A,  dpw = sum_gates alpha gate A
+//
+// Everything between the reads and the stores is FP32; y and rs are taken from
+// r before its rounding to the stream's type.  Bound by memory: a row is read
+// once and kept in registers over its sums.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "block_scale.h"
+#include "device_common.h"
+#include "kernels.h"
+#include "rowwise.h"
+
+namespace fp8mot {
+
+namespace {
+
+using namespace rows;
+using block::kBlock;
+
+template <bool F32>
+__device__ __forceinline__ const void* row_at(const void* p, int64_t at) {
+  return static_cast<const uint8_t*>(p) + at * (F32 ? 4 : 2);
+}
+template <bool F32>
+__device__ __forceinline__ void store8(void* p, int64_t at, int64_t i, int64_t n, const float* f) {
+  if constexpr (F32) store8_f32(static_cast<float*>(p) + at, i, n, f);
+  else store8_bf16(static_cast<uint16_t*>(p) + at, i, n, f);
+}
+// Eight values of a parameter of n columns, ones where there is none.
+__device__ __forceinline__ void param8(const void* p, int f32, int64_t i, int64_t n, float* f) {
+  if (p == nullptr) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = 1.0f;
+  } else {
+    load8_values(p, f32, i, n, f);
+  }
+}
+__device__ __forceinline__ const void* gate_at(const void* gate, int f32, int64_t at) {
+  return gate == nullptr ? nullptr : static_cast<const uint8_t*>(gate) + at * (f32 ? 4 : 2);
+}
+
+__device__ __forceinline__ float root(float sum, float inv_h, float eps) {
+  return 1.0f / __fsqrt_rn(__builtin_fmaf(sum, inv_h, eps));
+}
+__device__ __forceinline__ float square8(const float* f) {
+  float q[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) q[k] = __fmul_rn(f[k], f[k]);
+  return sum8(q);
+}
+
+// Columns i .. i + 7 of row r of y.  For block output sixteen lanes hold a
+// block's columns, and all of them come here (those past the row's end with
+// zeros: they write the padding).
+__device__ __forceinline__ void emit8(const ResidualNormArgs& g, int64_t r, int64_t i, float rs, float* y) {
+  if (g.out_kind == 3) {
+    const float s = block::scale_of(block::max16(block::max8(y)));
+    block::quotients<8>(y, s);
+    const int64_t Hp = (g.H + 15) / 16 * 16;
+    if (i < Hp) store8_fp8(static_cast<uint8_t*>(g.y) + r * Hp, i, Hp, y);
+    if (i % kBlock == 0 && i < g.H) g.scales[r * ((g.H + kBlock - 1) / kBlock) + i / kBlock] = s;
+  } else if (i < g.H) {
+    if (g.out_kind == 0) {
+      store8_bf16(static_cast<uint16_t*>(g.y) + r * g.H, i, g.H, y);
+    } else if (g.out_kind == 1) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] = __fmul_rn(y[k], rs);
+      store8_fp8(static_cast<uint8_t*>(g.y) + r * g.H, i, g.H, y);
+    } else {
+      store8_f32(static_cast<float*>(g.y) + r * g.H, i, g.H, y);
+    }
+  }
+}
+
+// T threads cover a row, U groups of eight columns each.  TC: 16 or 64 of
+// them, 256 / TC rows side by side in a workgroup; or 0: the whole workgroup.
+// A workgroup walks rows.
+template <bool XF, bool HF, int TC, int U>
+__global__ __launch_bounds__(TC > 0 ? 256 : 1024) void residual_norm_kernel(ResidualNormArgs g) {
+  __shared__ float red[2][16];
+  constexpr int RPB = TC > 0 ? 256 / (TC > 0 ? TC : 1) : 1;
+  const int T = TC > 0 ? TC : blockDim.x, t = TC > 0 ? threadIdx.x % T : threadIdx.x;
+  const float inv_h = 1.0f / (float)g.H, rs = g.out_kind == 1 ? 1.0f / *g.sy : 0.0f;
+  const bool has_h = g.h != nullptr, post = g.post_w != nullptr;
+  // (the sums' LDS takes turns: a wave may be at the next sum while others
+  // still read this one)
+  int turn = 0;
+  auto total = [&](float v) {
+    turn ^= 1;
+    return row_sum<TC>(v, red[turn]);
+  };
+  for (int64_t r = (int64_t)blockIdx.x * RPB + (TC > 0 ? threadIdx.x / T : 0); r < g.rows;
+       r += (int64_t)gridDim.x * RPB) {
+    float v[U][8], h[U][8];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int64_t i = 8 * (int64_t)(j * T + t);
+      values8<XF>(load8<XF>(row_at<XF>(g.x, r * g.H), i, g.H), v[j]);
+      if (has_h) values8<HF>(load8<HF>(row_at<HF>(g.h, r * g.H), i, g.H), h[j]);
+    }
+    if (has_h) {
+      float post_rs = 1.0f;
+      if (post) {
+        float s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < U; ++j) s = __fadd_rn(s, square8(h[j]));
+        post_rs = root(total(s), inv_h, g.eps);
+        if (t == 0 && g.post_rstd != nullptr) g.post_rstd[r] = post_rs;
+      }
+      const void* gate = gate_at(g.gate, g.gate_f32, (int64_t)((uint32_t)r / (uint32_t)g.gate_rows) * g.H);
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const int64_t i = 8 * (int64_t)(j * T + t);
+        float f[8];
+        if (post) {
+          param8(g.post_w, g.w_f32, i, g.H, f);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) h[j][k] = __fmul_rn(__fmul_rn(h[j][k], post_rs), f[k]);
+        }
+        if (gate != nullptr) {
+          param8(gate, g.gate_f32, i, g.H, f);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) h[j][k] = __fmul_rn(h[j][k], f[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[j][k] = __builtin_fmaf(g.alpha, h[j][k], v[j][k]);
+        if (i < g.H) store8<XF>(g.r, r * g.H, i, g.H, v[j]);
+      }
+    }
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < U; ++j) s = __fadd_rn(s, square8(v[j]));
+    const float rstd = root(total(s), inv_h, g.eps);
+    if (t == 0 && g.rstd != nullptr) g.rstd[r] = rstd;
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int64_t i = 8 * (int64_t)(j * T + t);
+      float w[8];
+      param8(g.w, g.w_f32, i, g.H, w);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[j][k] = __fmul_rn(__fmul_rn(v[j][k], rstd), w[k]);
+      emit8(g, r, i, rs, v[j]);
+    }
+  }
+}
+
+// Rows too long for registers: x and h are read again for every sum, from cache
+// after the first.
+template <bool XF, bool HF>
+__global__ __launch_bounds__(1024) void residual_norm_long_kernel(ResidualNormArgs g) {
+  __shared__ float red[2][16];
+  const float inv_h = 1.0f / (float)g.H, rs = g.out_kind == 1 ? 1.0f / *g.sy : 0.0f;
+  const bool has_h = g.h != nullptr, post = g.post_w != nullptr;
+  const int64_t end = (g.H + 8 * 1024 - 1) / (8 * 1024) * (8 * 1024);   // whole workgroups, for the block output
+  int turn = 0;
+  auto total = [&](float v) {
+    turn ^= 1;
+    return row_sum<0>(v, red[turn]);
+  };
+  for (int64_t r = blockIdx.x; r < g.rows; r += gridDim.x) {
+    const int64_t base = r * g.H;
+    float post_rs = 1.0f;
+    if (has_h && post) {
+      LongSum s;
+      for (int64_t i = 8 * (int64_t)threadIdx.x; i < g.H; i += 8 * 1024) {
+        float h[8];
+        values8<HF>(load8<HF>(row_at<HF>(g.h, base), i, g.H), h);
+        s.add(square8(h));
+      }
+      post_rs = root(total(s.s), inv_h, g.eps);
+      if (threadIdx.x == 0 && g.post_rstd != nullptr) g.post_rstd[r] = post_rs;
+    }
+    const void* gate =
+        has_h ? gate_at(g.gate, g.gate_f32, (int64_t)((uint32_t)r / (uint32_t)g.gate_rows) * g.H) : nullptr;
+    auto stream8 = [&](int64_t i, float* v) {
+      values8<XF>(load8<XF>(row_at<XF>(g.x, base), i, g.H), v);
+      if (!has_h) return;
+      float h[8], f[8];
+      values8<HF>(load8<HF>(row_at<HF>(g.h, base), i, g.H), h);
+      if (post) {
+        param8(g.post_w, g.w_f32, i, g.H, f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) h[k] = __fmul_rn(__fmul_rn(h[k], post_rs), f[k]);
+      }
+      if (gate != nullptr) {
+        param8(gate, g.gate_f32, i, g.H, f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) h[k] = __fmul_rn(h[k], f[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = __builtin_fmaf(g.alpha, h[k], v[k]);
+    };
+    LongSum s;
+    for (int64_t i = 8 * (int64_t)threadIdx.x; i < g.H; i += 8 * 1024) {
+      float v[8];
+      stream8(i, v);
+      s.add(square8(v));
+    }
+    const float rstd = root(total(s.s), inv_h, g.eps);
+    if (threadIdx.x == 0 && g.rstd != nullptr) g.rstd[r] = rstd;
+    for (int64_t i = 8 * (int64_t)threadIdx.x; i < end; i += 8 * 1024) {
+      float v[8] = {}, w[8];
+      if (i < g.H) {
+        stream8(i, v);
+        if (has_h) store8<XF>(g.r, base, i, g.H, v);   // over x, where r is x: these columns are done with it
+        param8(g.w, g.w_f32, i, g.H, w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = __fmul_rn(__fmul_rn(v[k], rstd), w[k]);
+      }
+      emit8(g, r, i, rs, v);
+    }
+  }
+}
+
+unsigned row_grid(int64_t n, int64_t most) { return (unsigned)(n < most ? n : most); }
+
+template <bool XF, bool HF, int TC, int U>
+hipError_t run_norm(const ResidualNormArgs& g, int threads, hipStream_t stream) {
+  const int rpb = TC > 0 ? 256 / (TC > 0 ? TC : 1) : 1;
+  hipLaunchKernelGGL((residual_norm_kernel<XF, HF, TC, U>), dim3(row_grid((g.rows + rpb - 1) / rpb, 1 << 16)),
+                     dim3(threads), 0, stream, g);
+  return hipGetLastError();
+}
+
+template <bool XF, bool HF>
+hipError_t norm_of_types(const ResidualNormArgs& g, hipStream_t stream) {
+  const int64_t units = (g.H + 7) / 8;
+  if (units <= 16) return run_norm<XF, HF, 16, 1>(g, 256, stream);
+  if (units <= 64) return run_norm<XF, HF, 64, 1>(g, 256, stream);
+  if (units <= 1024) return run_norm<XF, HF, 0, 1>(g, (int)((units + 63) / 64 * 64), stream);
+  if (units <= 2048) return run_norm<XF, HF, 0, 2>(g, 1024, stream);
+  hipLaunchKernelGGL((residual_norm_long_kernel<XF, HF>), dim3(row_grid(g.rows, 1 << 20)), dim3(1024), 0, stream, g);
+  return hipGetLastError();
+}
+
+// ---- backward ----
+
+// Where a slab's column sums go: its rows of the partial sums, or the results
+// themselves where it is the only one (of its gate).  NULL: not wanted.
+struct Sums {
+  float *w, *post, *gate;
+};
+__device__ __forceinline__ void put_sums(const Sums& o, const ResidualNormBwdArgs& g, int64_t i, const float* pw,
+                                         const float* gate, const float* sw, const float* sa) {
+  float f[8];
+  if (o.w != nullptr) store8_f32(o.w, i, g.H, sw);
+  if (o.post != nullptr) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = __fmul_rn(__fmul_rn(g.alpha, gate[k]), sa[k]);
+    store8_f32(o.post, i, g.H, f);
+  }
+  if (o.gate != nullptr) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = __fmul_rn(__fmul_rn(g.alpha, pw[k]), sa[k]);
+    store8_f32(o.gate, i, g.H, f);
+  }
+}
+
+// The slabs of a launch: per_gate of them cover the rows of each gate, `rows`
+// each.  part: [slabs, 3, H] partial sums.
+struct Slabs {
+  int64_t per_gate, rows;
+  float* part;
+};
+__device__ __forceinline__ Sums sums_of(const ResidualNormBwdArgs& g, const Slabs& s, int64_t slab) {
+  const bool one = g.gates * s.per_gate == 1;
+  float* p = s.part + slab * 3 * g.H;
+  return {g.dw == nullptr ? nullptr : (one ? g.dw : p), g.dpost == nullptr ? nullptr : (one ? g.dpost : p + g.H),
+          g.dgate == nullptr ? nullptr : (s.per_gate == 1 ? g.dgate + slab * g.H : p + 2 * g.H)};
+}
+
+struct RowRange {
+  int64_t gate, first, end;
+};
+__device__ __forceinline__ RowRange rows_of_slab(const ResidualNormBwdArgs& g, const Slabs& s, int64_t slab) {
+  const int64_t gate_rows = g.rows / g.gates;
+  RowRange r;
+  r.gate = slab / s.per_gate;
+  r.first = r.gate * gate_rows + (slab - r.gate * s.per_gate) * s.rows;
+  r.end = r.first + s.rows < (r.gate + 1) * gate_rows ? r.first + s.rows : (r.gate + 1) * gate_rows;
+  return r;
+}
+
+// T threads cover a row, eight columns each (TC: 16 or 64, and as many rows
+// side by side as the workgroup holds; or 0: the whole workgroup).  They walk
+// the rows of the workgroup's slab, which lies within one gate's rows.
+template <bool XF, bool HF, int TC, int NT>
+__global__ __launch_bounds__(NT) void residual_norm_backward_kernel(ResidualNormBwdArgs g, Slabs sl) {
+  __shared__ float red[2][16];
+  __shared__ f4 cols[TC > 0 ? 4 * NT / 2 : 1];
+  const int G = TC > 0 ? (int)blockDim.x / (TC > 0 ? TC : 1) : 1;   // rows side by side
+  const int t = TC > 0 ? threadIdx.x % (TC > 0 ? TC : 1) : threadIdx.x;
+  const float inv_h = 1.0f / (float)g.H;
+  const bool has_h = g.h != nullptr, post = g.post_w != nullptr;
+  const int64_t i = 8 * (int64_t)t;
+  float w[8], gate[8], pw[8];
+  param8(g.w, g.w_f32, i, g.H, w);
+  param8(g.post_w, g.w_f32, i, g.H, pw);
+  int turn = 0;
+  auto total = [&](float v) {
+    turn ^= 1;
+    return row_sum<TC>(v, red[turn]);
+  };
+  for (int64_t slab = blockIdx.x; slab < sl.per_gate * g.gates; slab += gridDim.x) {
+  const RowRange rr = rows_of_slab(g, sl, slab);
+  float sw[8] = {}, sa[8] = {};
+  param8(gate_at(g.gate, g.gate_f32, rr.gate * g.H), g.gate_f32, i, g.H, gate);
+  for (int64_t r = rr.first + (TC > 0 ? threadIdx.x / (TC > 0 ? TC : 1) : 0); r < rr.end; r += G) {
+    float dy[8], n[8], z[8], d[8];
+    values8<HF>(load8<HF>(row_at<HF>(g.dy, r * g.H), i, g.H), dy);
+    values8<XF>(load8<XF>(row_at<XF>(g.r, r * g.H), i, g.H), n);
+    if (has_h) values8<HF>(load8<HF>(row_at<HF>(g.h, r * g.H), i, g.H), z);
+    if (g.dr != nullptr) values8<XF>(load8<XF>(row_at<XF>(g.dr, r * g.H), i, g.H), d);
+    const float rs = g.rstd[r], post_rs = post ? g.post_rstd[r] : 1.0f;
+    float e[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      n[k] = __fmul_rn(n[k], rs);
+      sw[k] = __builtin_fmaf(dy[k], n[k], sw[k]);
+      dy[k] = __fmul_rn(dy[k], w[k]);
+      e[k] = __fmul_rn(dy[k], n[k]);
+    }
+    const float c = __fmul_rn(total(sum8(e)), inv_h);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      n[k] = __fmul_rn(rs, __builtin_fmaf(-n[k], c, dy[k]));
+      if (g.dr != nullptr) n[k] = __fadd_rn(n[k], d[k]);   // dx
+    }
+    if (i < g.H) store8<XF>(g.dx, r * g.H, i, g.H, n);
+    if (has_h) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (post) z[k] = __fmul_rn(z[k], post_rs);
+        sa[k] = __builtin_fmaf(n[k], z[k], sa[k]);
+        n[k] = __fmul_rn(n[k], __fmul_rn(__fmul_rn(g.alpha, gate[k]), pw[k]));   // p
+        e[k] = __fmul_rn(n[k], z[k]);
+      }
+      if (post) {
+        const float c2 = __fmul_rn(total(sum8(e)), inv_h);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) n[k] = __fmul_rn(post_rs, __builtin_fmaf(-z[k], c2, n[k]));
+      }
+      if (i < g.H) store8<HF>(g.dh, r * g.H, i, g.H, n);
+    }
+  }
+  const int q = TC > 0 ? threadIdx.x / (TC > 0 ? TC : 1) : 0;
+  if constexpr (TC > 0) {
+    // the rows side by side (a power of two) are added in a tree
+    for (int h = G >> 1; h > 0; h >>= 1) {
+      const int at = (q & (h - 1)) * TC + t, n4 = h * TC;
+      if (q >= h && q < 2 * h) {
+        cols[at] = (f4){sw[0], sw[1], sw[2], sw[3]};
+        cols[n4 + at] = (f4){sw[4], sw[5], sw[6], sw[7]};
+        cols[2 * n4 + at] = (f4){sa[0], sa[1], sa[2], sa[3]};
+        cols[3 * n4 + at] = (f4){sa[4], sa[5], sa[6], sa[7]};
+      }
+      __syncthreads();
+      if (q < h) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          sw[k] = __fadd_rn(sw[k], cols[(k >> 2) * n4 + at][k & 3]);
+          sa[k] = __fadd_rn(sa[k], cols[(2 + (k >> 2)) * n4 + at][k & 3]);
+        }
+      }
+      __syncthreads();
+    }
+  }
+  if (q == 0 && i < g.H) put_sums(sums_of(g, sl, slab), g, i, pw, gate, sw, sa);
+  }
+}
+
+// Rows too long for that, in three launches: each row's sum(g n) / H into c;
+// the column sums; dx and dh (which may lie over what is read).
+struct LongRow {
+  float rs, post_rs, c;
+};
+template <bool XF, bool HF>
+__device__ __forceinline__ void long_row8(const ResidualNormBwdArgs& g, int64_t r, int64_t i, float rs, float* dy,
+                                          float* n, float* gw) {
+  values8<HF>(load8<HF>(row_at<HF>(g.dy, r * g.H), i, g.H), dy);
+  values8<XF>(load8<XF>(row_at<XF>(g.r, r * g.H), i, g.H), n);
+  param8(g.w, g.w_f32, i, g.H, gw);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    n[k] = __fmul_rn(n[k], rs);
+    gw[k] = __fmul_rn(dy[k], gw[k]);
+  }
+}
+template <bool XF, bool HF>
+__device__ __forceinline__ void long_dx8(const ResidualNormBwdArgs& g, int64_t r, int64_t i, const LongRow& a,
+                                         const float* n, const float* gw, float* dx, float* z) {
+  float d[8];
+  if (g.dr != nullptr) values8<XF>(load8<XF>(row_at<XF>(g.dr, r * g.H), i, g.H), d);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    dx[k] = __fmul_rn(a.rs, __builtin_fmaf(-n[k], a.c, gw[k]));
+    if (g.dr != nullptr) dx[k] = __fadd_rn(dx[k], d[k]);
+  }
+  if (g.h == nullptr) return;
+  values8<HF>(load8<HF>(row_at<HF>(g.h, r * g.H), i, g.H), z);
+  if (g.post_w != nullptr) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) z[k] = __fmul_rn(z[k], a.post_rs);
+  }
+}
+__device__ __forceinline__ LongRow long_row(const ResidualNormBwdArgs& g, const float* c, int64_t r) {
+  return {g.rstd[r], g.post_w != nullptr ? g.post_rstd[r] : 1.0f, c == nullptr ? 0.0f : c[r]};
+}
+
+template <bool XF, bool HF>
+__global__ __launch_bounds__(1024) void residual_norm_row_long_kernel(ResidualNormBwdArgs g, float* __restrict__ c) {
+  __shared__ float red[2][16];
+  const float inv_h = 1.0f / (float)g.H;
+  int turn = 0;
+  for (int64_t r = blockIdx.x; r < g.rows; r += gridDim.x, turn ^= 1) {
+    LongSum s;
+    for (int64_t i = 8 * (int64_t)threadIdx.x; i < g.H; i += 8 * 1024) {
+      float dy[8], n[8], gw[8];
+      long_row8<XF, HF>(g, r, i, g.rstd[r], dy, n, gw);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) n[k] = __fmul_rn(gw[k], n[k]);
+      s.add(sum8(n));
+    }
+    const float v = __fmul_rn(row_sum<0>(s.s, red[turn]), inv_h);
+    if (threadIdx.x == 0) c[r] = v;
+  }
+}
+
+template <bool XF, bool HF>
+__global__ __launch_bounds__(256) void residual_norm_columns_long_kernel(ResidualNormBwdArgs g, Slabs sl,
+                                                                         const float* __restrict__ c) {
+  const int64_t i = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+  if (i >= g.H) return;
+  float gate[8], pw[8];
+  param8(g.post_w, g.w_f32, i, g.H, pw);
+  for (int64_t slab = blockIdx.y; slab < sl.per_gate * g.gates; slab += gridDim.y) {
+    const RowRange rr = rows_of_slab(g, sl, slab);
+    float sw[8] = {}, sa[8] = {};
+    param8(gate_at(g.gate, g.gate_f32, rr.gate * g.H), g.gate_f32, i, g.H, gate);
+    for (int64_t r = rr.first; r < rr.end; ++r) {
+      const LongRow a = long_row(g, c, r);
+      float dy[8], n[8], gw[8], dx[8], z[8] = {};
+      long_row8<XF, HF>(g, r, i, a.rs, dy, n, gw);
+      long_dx8<XF, HF>(g, r, i, a, n, gw, dx, z);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        sw[k] = __builtin_fmaf(dy[k], n[k], sw[k]);
+        sa[k] = __builtin_fmaf(dx[k], z[k], sa[k]);
+      }
+    }
+    put_sums(sums_of(g, sl, slab), g, i, pw, gate, sw, sa);
+  }
+}
+
+template <bool XF, bool HF>
+__global__ __launch_bounds__(1024) void residual_norm_dx_long_kernel(ResidualNormBwdArgs g,
+                                                                     const float* __restrict__ c) {
+  __shared__ float red[2][16];
+  const float inv_h = 1.0f / (float)g.H;
+  const bool has_h = g.h != nullptr, post = g.post_w != nullptr;
+  const int64_t gate_rows = g.rows / g.gates;
+  int turn = 0;
+  for (int64_t r = blockIdx.x; r < g.rows; r += gridDim.x, turn ^= 1) {
+    const LongRow a = long_row(g, c, r);
+    const void* gate = gate_at(g.gate, g.gate_f32, r / gate_rows * g.H);
+    auto row8 = [&](int64_t i, float* dx, float* z, float* p) {
+      float dy[8], n[8], gw[8], f[8], e[8];
+      long_row8<XF, HF>(g, r, i, a.rs, dy, n, gw);
+      long_dx8<XF, HF>(g, r, i, a, n, gw, dx, z);
+      if (!has_h) return;
+      param8(gate, g.gate_f32, i, g.H, f);
+      param8(g.post_w, g.w_f32, i, g.H, e);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) p[k] = __fmul_rn(dx[k], __fmul_rn(__fmul_rn(g.alpha, f[k]), e[k]));
+    };
+    float c2 = 0.0f;
+    if (has_h && post) {
+      LongSum s;
+      for (int64_t i = 8 * (int64_t)threadIdx.x; i < g.H; i += 8 * 1024) {
+        float dx[8], z[8], p[8];
+        row8(i, dx, z, p);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) p[k] = i + k < g.H ? __fmul_rn(p[k], z[k]) : 0.0f;
+        s.add(sum8(p));
+      }
+      c2 = __fmul_rn(row_sum<0>(s.s, red[turn]), inv_h);
+    }
+    for (int64_t i = 8 * (int64_t)threadIdx.x; i < g.H; i += 8 * 1024) {
+      float dx[8], z[8], p[8];
+      row8(i, dx, z, p);
+      store8<XF>(g.dx, r * g.H, i, g.H, dx);
+      if (!has_h) continue;
+      if (post) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) p[k] = __fmul_rn(a.post_rs, __builtin_fmaf(-z[k], c2, p[k]));
+      }
+      store8<HF>(g.dh, r * g.H, i, g.H, p);
+    }
+  }
+}
+
+// Sums over slabs of part [slabs, 3, H], in an order that depends on the sizes
+// alone: plane 0 and 1 over all slabs, and with `each_gate` the third for every
+// gate over its own (y = 2 + gate).  64 columns a workgroup, four per thread;
+// sixteen threads share a column's slabs.
+__global__ __launch_bounds__(256) void residual_norm_sums_kernel(ResidualNormBwdArgs g, Slabs sl, int each_gate) {
+  __shared__ float red[16][68];
+  const int q = threadIdx.x & 15, s = threadIdx.x >> 4;
+  for (int64_t y = blockIdx.y; y < 2 + (each_gate ? g.gates : 0); y += gridDim.y, __syncthreads()) {
+    const int plane = y < 2 ? (int)y : 2;
+    float* out = plane == 0 ? g.dw : plane == 1 ? g.dpost : (g.dgate == nullptr ? nullptr : g.dgate + (y - 2) * g.H);
+    if (out == nullptr) continue;
+    const int64_t first = plane < 2 ? 0 : (y - 2) * sl.per_gate, count = (plane < 2 ? g.gates : 1) * sl.per_gate;
+    const int64_t n = (int64_t)blockIdx.x * 64 + 4 * q;
+    const float* v = sl.part + (first * 3 + plane) * g.H + n;
+    float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (n + 4 <= g.H) {
+#pragma unroll 4
+      for (int64_t p = s; p < count; p += 16) {
+        const f4 x = *reinterpret_cast<const f4a4*>(v + p * 3 * g.H);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) t[k] = __fadd_rn(t[k], x[k]);
+      }
+    } else {
+      for (int64_t p = s; p < count; p += 16)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (n + k < g.H) t[k] = __fadd_rn(t[k], v[p * 3 * g.H + k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) red[s][4 * q + k] = t[k];
+    __syncthreads();
+    if (threadIdx.x < 64) {
+      float u = red[0][threadIdx.x];
+#pragma unroll
+      for (int p = 1; p < 16; ++p) u = __fadd_rn(u, red[p][threadIdx.x]);
+      const int64_t c = (int64_t)blockIdx.x * 64 + threadIdx.x;
+      if (c < g.H) out[c] = u;
+    }
+  }
+}
+
+// rows of up to this many elements go through residual_norm_backward_kernel
+constexpr int64_t kBwdRegs = 1024 * 8;
+
+// Threads of a workgroup, rows side by side in it, slabs for each gate.
+struct BwdShape {
+  int threads, side;
+  int64_t per_gate;
+};
+BwdShape bwd_shape(int64_t rows, int64_t H, int64_t gates) {
+  const int64_t units = (H + 7) / 8, gate_rows = rows / gates;
+  BwdShape b{0, 1, 0};
+  int64_t slabs;
+  if (H > kBwdRegs) {
+    b.threads = 1024;
+    const int64_t room = 2048 / ((H + 2047) / 2048);
+    slabs = room < 1 ? 1 : room < 256 ? room : 256;
+  } else if (units <= 64) {
+    const int tc = units <= 16 ? 16 : 64;
+    b.threads = 256;
+    b.side = b.threads / tc;
+    slabs = 768;
+  } else {
+    b.threads = (int)((units + 63) / 64 * 64);
+    slabs = b.threads >= 512 ? 256 : b.threads >= 192 ? 512 : 768;
+  }
+  if (rows <= 4 * b.side && gates == 1) slabs = 1;
+  b.per_gate = (slabs + gates - 1) / gates;
+  const int64_t most = (gate_rows + b.side - 1) / b.side;
+  if (b.per_gate > most) b.per_gate = most;
+  return b;
+}
+
+template <bool XF, bool HF>
+hipError_t run_backward(const ResidualNormBwdArgs& g, const BwdShape& b, const Slabs& sl, float* c,
+                        hipStream_t stream) {
+  const int64_t slabs = g.gates * b.per_gate;
+  const dim3 grid(row_grid(slabs, 1 << 20));
+  if (g.H <= 128) {
+    hipLaunchKernelGGL((residual_norm_backward_kernel<XF, HF, 16, 256>), grid, dim3(b.threads), 0, stream, g, sl);
+  } else if (g.H <= 512) {
+    hipLaunchKernelGGL((residual_norm_backward_kernel<XF, HF, 64, 256>), grid, dim3(b.threads), 0, stream, g, sl);
+  } else if (g.H <= kBwdRegs) {
+    hipLaunchKernelGGL((residual_norm_backward_kernel<XF, HF, 0, 1024>), grid, dim3(b.threads), 0, stream, g, sl);
+  } else {
+    const unsigned rows = row_grid(g.rows, 1 << 20);
+    hipLaunchKernelGGL((residual_norm_row_long_kernel<XF, HF>), dim3(rows), dim3(1024), 0, stream, g, c);
+    if (g.dw != nullptr || g.dgate != nullptr || g.dpost != nullptr)
+      hipLaunchKernelGGL((residual_norm_columns_long_kernel<XF, HF>), dim3((unsigned)((g.H + 2047) / 2048), row_grid(slabs, 65535)),
+                         dim3(256), 0, stream, g, sl, c);
+    hipLaunchKernelGGL((residual_norm_dx_long_kernel<XF, HF>), dim3(rows), dim3(1024), 0, stream, g, c);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_residual_norm(const ResidualNormArgs& g, hipStream_t stream) {
+  if (g.x_f32) return g.h_f32 ? norm_of_types<true, true>(g, stream) : norm_of_types<true, false>(g, stream);
+  return g.h_f32 ? norm_of_types<false, true>(g, stream) : norm_of_types<false, false>(g, stream);
+}
+
+int64_t residual_norm_backward_floats(int64_t rows, int64_t H, int64_t gates) {
+  if (rows == 0 || H == 0) return 0;
+  const int64_t slabs = gates * bwd_shape(rows, H, gates).per_gate;
+  return (slabs > 1 ? slabs * 3 * H : 0) + (H > kBwdRegs ? rows : 0);
+}
+
+hipError_t launch_residual_norm_backward(const ResidualNormBwdArgs& g, float* ws, hipStream_t stream) {
+  Slabs sl{0, 0, ws};   // no rows: sums of no slabs
+  bool each_gate = true;
+  if (g.rows > 0) {
+    const BwdShape b = bwd_shape(g.rows, g.H, g.gates);
+    const int64_t slabs = g.gates * b.per_gate, gate_rows = g.rows / g.gates;
+    sl.per_gate = b.per_gate;
+    sl.rows = (gate_rows + b.per_gate - 1) / b.per_gate;
+    float* c = ws + (slabs > 1 ? slabs * 3 * g.H : 0);
+    hipError_t e;
+    if (g.x_f32) e = g.h_f32 ? run_backward<true, true>(g, b, sl, c, stream) : run_backward<true, false>(g, b, sl, c, stream);
+    else e = g.h_f32 ? run_backward<false, true>(g, b, sl, c, stream) : run_backward<false, false>(g, b, sl, c, stream);
+    if (e != hipSuccess || slabs == 1) return e;
+    each_gate = b.per_gate > 1;
+  }
+  if (g.dw == nullptr && g.dpost == nullptr && (g.dgate == nullptr || !each_gate)) return hipSuccess;
+  hipLaunchKernelGGL(residual_norm_sums_kernel,
+                     dim3((unsigned)((g.H + 63) / 64), row_grid(2 + (each_gate ? g.gates : 0), 65535)), dim3(256), 0,
+                     stream, g, sl, each_gate ? 1 : 0);
+  return hipGetLastError();
+}
+
+}  // namespace fp8mot

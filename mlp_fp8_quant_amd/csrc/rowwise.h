@@ -1,5 +1,6 @@
 // Pieces of the kernels that stream rows of floats: groups of eight
-// consecutive elements of a row, sums over a wave, E4M3 and BF16 output.
+// consecutive elements of a row, sums over a wave or a workgroup, E4M3 and BF16
+// output.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -188,6 +189,41 @@ __device__ __forceinline__ float wave_sum(float v) {
   const float c = __int_as_float(__builtin_amdgcn_readlane(i, 32)), d = __int_as_float(__builtin_amdgcn_readlane(i, 48));
   return __fadd_rn(__fadd_rn(a, b), __fadd_rn(c, d));
 }
+
+// Sum over the threads that share a row, the same in each: TC = 16 or 64
+// lanes, or (0) the whole workgroup.  red: 16 floats of LDS that no other sum
+// in flight uses.
+template <int TC>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+  if constexpr (TC == 16) return sum16(v);
+  v = wave_sum(v);
+  if constexpr (TC == 0) {
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    const int waves = blockDim.x >> 6;
+    v = red[0];
+    for (int w = 1; w < waves; ++w) v = __fadd_rn(v, red[w]);
+  }
+  return v;
+}
+
+// A tree over eight values: fewer roundings in a row than one after another.
+__device__ __forceinline__ float sum8(const float* f) {
+  return __fadd_rn(__fadd_rn(__fadd_rn(f[0], f[1]), __fadd_rn(f[2], f[3])),
+                   __fadd_rn(__fadd_rn(f[4], f[5]), __fadd_rn(f[6], f[7])));
+}
+
+// A sum that keeps what its additions round off (of many terms in one thread,
+// where the roundings of a plain sum would add up: 2e-5 of rstd at 2^26
+// columns).
+struct LongSum {
+  float s = 0.0f, lost = 0.0f;
+  __device__ __forceinline__ void add(float v) {
+    const float y = __fadd_rn(v, -lost), t = __fadd_rn(s, y);
+    lost = __fadd_rn(__fadd_rn(t, -s), -y);
+    s = t;
+  }
+};
 
 }  // namespace rows
 }  // namespace fp8mot

@@ -209,6 +209,111 @@ def _(dy, x, weight, mean, rstd, dres=None):
     return torch.empty(x.shape, dtype=x.dtype, device=x.device), col(), col()
 
 
+def _like(t, *shape, dtype):
+    return torch.empty(shape, dtype=dtype, device=t.device)
+
+
+def _block_codes(t, lead, cols, lead_scales=None):
+    lead_scales = lead if lead_scales is None else lead_scales
+    return (_like(t, *lead, api._up(cols, 16), dtype=torch.uint8),
+            _like(t, *lead_scales, api._blocks(cols), dtype=torch.float32))
+
+
+@torch.library.custom_op(f"{NS}::quant_block", mutates_args=())
+def quant_block(x: torch.Tensor, tile: bool = False,
+                transpose: bool = False) -> tuple[torch.Tensor, torch.Tensor]:
+    """(codes, scales) of x with a scale for each block of 128."""
+    return api.fp8_quant_block(x, tile, transpose)
+
+
+@quant_block.register_fake
+def _(x, tile=False, transpose=False):
+    lead, cols = ((x.shape[1],), x.shape[0]) if transpose else (x.shape[:-1], x.shape[-1])
+    return _block_codes(x, lead, cols, (api._blocks(lead[0]),) if tile else None)
+
+
+@torch.library.custom_op(f"{NS}::silu_mul_block", mutates_args=())
+def silu_mul_block(g: torch.Tensor, u: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+    """(codes, scales) of silu(g) * u with a scale for each 128 columns."""
+    return api.silu_mul_2in_block(g, u)
+
+
+@silu_mul_block.register_fake
+def _(g, u):
+    return _block_codes(g, g.shape[:-1], g.shape[-1])
+
+
+@torch.library.custom_op(f"{NS}::linear_block", mutates_args=())
+def linear_block(qx: torch.Tensor, qw: torch.Tensor, sx: torch.Tensor, sw: torch.Tensor,
+                 bias: Optional[torch.Tensor] = None, act: int = api.ACT_NONE,
+                 residual: Optional[torch.Tensor] = None, out_kind: int = api.OUT_BF16,
+                 sy: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """linear_act of operands with a scale for each block of 128 of K."""
+    return api.fp8_linear_block(qx, qw, sx, sw, bias, act, residual, out_kind, sy)
+
+
+@linear_block.register_fake
+def _(qx, qw, sx, sw, bias=None, act=api.ACT_NONE, residual=None, out_kind=api.OUT_BF16, sy=None):
+    return _like(qx, *qx.shape[:-1], qw.shape[0], dtype=api._out_dtype(out_kind))
+
+
+@torch.library.custom_op(f"{NS}::residual_norm", mutates_args=())
+def residual_norm(x: torch.Tensor, hidden: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                  gate: Optional[torch.Tensor] = None, post_weight: Optional[torch.Tensor] = None,
+                  alpha: float = 1.0, eps: float = 1e-6, out_kind: int = api.OUT_BF16,
+                  sy: Optional[torch.Tensor] = None
+                  ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(y, r, rstd, post_rstd) of a block's output and the stream it is added
+    to; post_rstd is empty without post_weight."""
+    y, r, rstd, post = api.fp8_residual_norm(x, weight, hidden, gate, post_weight, alpha, eps,
+                                             out_kind, sy, stats=True)
+    return y, r, rstd, rstd.new_empty(0) if post is None else post
+
+
+@residual_norm.register_fake
+def _(x, hidden, weight=None, gate=None, post_weight=None, alpha=1.0, eps=1e-6,
+      out_kind=api.OUT_BF16, sy=None):
+    stat = _like(x, *x.shape[:-1], dtype=torch.float32)
+    return (_like(x, *x.shape, dtype=api._out_dtype(out_kind)), torch.empty_like(x), stat,
+            _like(x, 0, dtype=torch.float32) if post_weight is None else torch.empty_like(stat))
+
+
+@torch.library.custom_op(f"{NS}::residual_norm_block", mutates_args=())
+def residual_norm_block(x: torch.Tensor, hidden: torch.Tensor,
+                        weight: Optional[torch.Tensor] = None,
+                        gate: Optional[torch.Tensor] = None,
+                        post_weight: Optional[torch.Tensor] = None, alpha: float = 1.0,
+                        eps: float = 1e-6) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(codes, scales, r): residual_norm whose y has a scale for each 128 columns."""
+    (q, s), r = api.fp8_residual_norm(x, weight, hidden, gate, post_weight, alpha, eps,
+                                      api.OUT_FP8_BLOCK)
+    return q, s, r
+
+
+@residual_norm_block.register_fake
+def _(x, hidden, weight=None, gate=None, post_weight=None, alpha=1.0, eps=1e-6):
+    return (*_block_codes(x, x.shape[:-1], x.shape[-1]), torch.empty_like(x))
+
+
+@torch.library.custom_op(f"{NS}::residual_norm_backward", mutates_args=())
+def residual_norm_backward(dy: torch.Tensor, r: torch.Tensor, weight: torch.Tensor,
+                           rstd: torch.Tensor, hidden: torch.Tensor, gate: torch.Tensor,
+                           post_weight: torch.Tensor, post_rstd: torch.Tensor,
+                           alpha: float = 1.0, dr: Optional[torch.Tensor] = None
+                           ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor,
+                                      torch.Tensor]:
+    """(dx, dhidden, dweight, dgate, dpost_weight) of residual_norm with all its inputs."""
+    return api.fp8_residual_norm_backward(dy, r, weight, rstd, hidden, gate, post_weight, post_rstd,
+                                          alpha, dr)
+
+
+@residual_norm_backward.register_fake
+def _(dy, r, weight, rstd, hidden, gate, post_weight, post_rstd, alpha=1.0, dr=None):
+    col = lambda t: torch.empty(t.shape, dtype=torch.float32, device=t.device)  # noqa: E731
+    return torch.empty_like(r), torch.empty_like(hidden), col(weight), col(gate), col(post_weight)
+
+
 OPS = (quant_static, linear, silu_mul_2in, silu_mul, gated_mlp, qkv, quant_per_row,
        linear_rowwise, linear_act, linear_act_train, linear_act_backward, layer_norm,
-       layer_norm_backward)
+       layer_norm_backward, quant_block, silu_mul_block, linear_block, residual_norm,
+       residual_norm_block, residual_norm_backward)
