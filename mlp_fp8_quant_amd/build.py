@@ -25,7 +25,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_NAME = "libfp8mot.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["elementwise.hip", "gemm.hip", "linear_act_tile.hip", "linear_act.hip", "layer_norm.hip",
-           "block_quant.hip", "linear_block.hip", "residual_norm.hip", "mfma_ceiling.hip", "verify.hip", "capi.hip"]
+           "block_quant.hip", "linear_block.hip", "linear_block_tile.hip", "residual_norm.hip",
+           "mfma_ceiling.hip", "verify.hip", "capi.hip"]
 
 BINDING_PATH = os.path.join(PKG, "_binding.so")
 

@@ -81,7 +81,19 @@ __device__ __forceinline__ void copy_to_lds(v4i rsrc, uint32_t lds_addr, int vof
       : "memory", "m0");
 }
 
-// The same with four bytes per lane, at lds_addr + 4 * i.
+// The same to lds_addr + AT, which the write of M0 adds.
+template <int AT>
+__device__ __forceinline__ void copy_to_lds_at(v4i rsrc, uint32_t lds_addr, int voff, int soff) {
+  asm volatile(
+      "s_add_u32 m0, %0, %4\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dwordx4 %1, %2, %3 offen lds"
+      :
+      : "s"(lds_addr), "v"(voff), "s"(rsrc), "s"(soff), "n"(AT)
+      : "memory", "m0", "scc");
+}
+
+// Four bytes per lane, to lds_addr + 4 * i.
 __device__ __forceinline__ void copy4_to_lds(v4i rsrc, uint32_t lds_addr, int voff, int soff) {
   asm volatile(
       "s_mov_b32 m0, %0\n\t"

@@ -242,23 +242,54 @@ hipError_t launch_rows(const LinearActArgs& g, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// How a shape runs (MI355X, 256 CUs; us measured).  Few outputs: the smallest
+// tile of 16 x 16 blocks whose grid gives no CU more than one workgroup, and up
+// to two of 64 x 64, as in fp8_linear_act's rule: 1x4096x4096 5.3 with one block
+// (with two 5.6), 64x4096x4096 7.6 with 32x32 (64x32 10.1, 32x16 10.6),
+// 128x12288x4096 25.1 with 64x64 in pairs (alone 29.8), 512x4096x12288 69 (128x128
+// with two K groups 67, 128x128 84).
+//
+// More outputs: the cheapest of three tiles by an estimate of rounds of workgroups
+// times (rate * K + what a tile costs besides): 256x128 4096x12288x4096 347 (128x128
+// 357, two K groups 402), 128x128 two to a CU 5000x5000x4096 198 (213, 228) and
+// 3000x3000x512 21 (26, 30), 128x128 with two K groups 2048x2048x8192 62 (82, 66).
+int linear_block_plan(int64_t M, int64_t N, int64_t K) {
+  constexpr int64_t kCus = 256;
+  auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+  const int64_t area = up(up(M, 16) * up(N, 16), kCus);   // blocks per CU
+  if (M <= 16) return area <= 1 ? kRows1x1 : area <= 2 ? kRows1x2 : kRows1x4;
+  if (area <= 2) return kRows2x1;
+  if (area <= 4) return kRows2x2;
+  if (M <= 32) return kRows2x4;
+  if (area <= 8) return kRows4x2;
+  if (area <= 16) return kRows4x4;
+  if (M <= 64 || area <= 32) return kRows4x4Pair;
+  const int64_t small = up(M, 128) * up(N, 128), large = up(M, 256) * up(N, 128);
+  const double k = (double)K, pairs = (double)small / (2 * kCus);
+  const double t256 = (double)up(large, kCus) * (0.0118 * k + 9.0);
+  const double t128 = pairs <= 0.5 ? 0.0072 * k + 7.0
+                                   : (pairs <= 1.0 ? 1.0 : 0.5 * (pairs + (double)up(small, 2 * kCus))) * (0.0128 * k + 7.0);
+  const double tk2 = (double)up(small, kCus) * (0.00667 * k + 7.6);
+  if (t256 <= t128 && t256 <= tk2) return kTile256x128;
+  return t128 <= tk2 ? kTile128x128 : kTile128x128K2;
+}
+
 }  // namespace
 
 hipError_t launch_linear_block(const LinearActArgs& g, int num_cus, hipStream_t stream) {
-  constexpr int64_t kCus = 256;
-  auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-  const int64_t area = up(up(g.M, 16) * up(g.N, 16), kCus);   // blocks per CU
-  if (g.M <= 16) {
-    if (area <= 1) return launch_rows<1, 1, 16>(g, stream);
-    if (area <= 2) return launch_rows<1, 2, 8>(g, stream);
-    return launch_rows<1, 4, 4>(g, stream);
+  const int tile = linear_block_plan(g.M, g.N, g.K);
+  switch (tile) {
+    case kRows1x1: return launch_rows<1, 1, 16>(g, stream);
+    case kRows1x2: return launch_rows<1, 2, 8>(g, stream);
+    case kRows1x4: return launch_rows<1, 4, 4>(g, stream);
+    case kRows2x1: return launch_rows<2, 1, 8>(g, stream);
+    case kRows2x2: return launch_rows<2, 2, 8>(g, stream);
+    case kRows2x4: return launch_rows<2, 4, 4>(g, stream);
+    case kRows4x2: return launch_rows<4, 2, 4>(g, stream);
+    case kRows4x4: return launch_rows<4, 4, 4>(g, stream);
+    case kRows4x4Pair: return launch_rows<4, 4, 2>(g, stream);
+    default: return launch_linear_block_tile(g, tile, num_cus, stream);
   }
-  if (area <= 2) return launch_rows<2, 1, 8>(g, stream);
-  if (area <= 4) return launch_rows<2, 2, 8>(g, stream);
-  if (g.M <= 32) return launch_rows<2, 4, 4>(g, stream);
-  if (area <= 8) return launch_rows<4, 2, 4>(g, stream);
-  if (area <= 16) return launch_rows<4, 4, 4>(g, stream);
-  return launch_rows<4, 4, 2>(g, stream);
 }
 
 }  // namespace fp8mot

@@ -34,7 +34,9 @@ def on(*ts):
 # sizes that reach every kernel, and both sides of every tile's edges
 SHAPES = [(1, 1, 16), (1, 100, 128), (1, 4096, 272), (1, 8192, 400), (7, 20000, 144), (16, 129, 1040), (17, 1, 128),
           (17, 257, 384), (33, 96, 2064), (40, 3001, 256), (64, 130, 512), (65, 2000, 640), (100, 777, 1296),
-          (130, 4097, 128), (257, 1023, 272), (600, 900, 528), (513, 2052, 160)]
+          (130, 4097, 128), (257, 1023, 272), (600, 900, 528), (513, 2052, 160),
+          (20, 9000, 272), (1030, 2100, 400), (700, 3150, 128), (1100, 5003, 272), (2200, 2049, 528), (1024, 3000, 2064),
+          (510, 16380, 2064)]
 
 
 @pytest.mark.parametrize("w_rows", [False, True])
@@ -47,6 +49,18 @@ def test_products(M, N, K, w_rows):
     ref.check(y, y64, err, "fp32")
     assert torch.equal(y, fp8.fp8_linear_block(*d, out_kind=fp8.OUT_F32))
     assert torch.equal(fp8.fp8_linear_block(*d), y.to(BF16))
+
+
+@pytest.mark.parametrize("w_rows", [False, True])
+def test_workgroups_that_walk_tiles(w_rows):
+    # 512 tiles of 256x128 on 256 CUs, ragged on both sides; K ends inside a stage and a batch of scales
+    M, N, K = 1020, 16380, 2064
+    qx, qw, sx, sw, g = operands(M, N, K, w_rows, 11)
+    bias = torch.randn(N, generator=g)
+    y = fp8.fp8_linear_block(*on(qx, qw, sx, sw), bias=bias.to(device()), out_kind=fp8.OUT_F32)
+    for r in (slice(0, 130), slice(500, 560), slice(960, 1020)):
+        y64, _, err, _ = ref.linear(qx[r], qw, sx[r], sw, w_rows, bias)
+        ref.check(y[r], y64, err)
 
 
 @pytest.mark.parametrize("act", ACTS)
