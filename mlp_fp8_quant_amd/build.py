@@ -97,7 +97,7 @@ def build_binding(verbose=False) -> str:
     cmd += [os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", PKG, "-lfp8mot"]
     for d in ext.library_paths():
         cmd += ["-L", d]
-    cmd += ["-lc10", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    cmd += ["-lc10", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
     if verbose:
         print(" ".join(cmd), flush=True)
     _run(cmd)

@@ -47,6 +47,9 @@ __device__ __forceinline__ void param8(const void* p, int f32, int64_t i, int64_
     load8_values(p, f32, i, n, f);
   }
 }
+__device__ __forceinline__ float param1(const void* p, int f32, int64_t i) {
+  return f32 ? static_cast<const float*>(p)[i] : bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
+}
 __device__ __forceinline__ const void* gate_at(const void* gate, int f32, int64_t at) {
   return gate == nullptr ? nullptr : static_cast<const uint8_t*>(gate) + at * (f32 ? 4 : 2);
 }
@@ -84,16 +87,54 @@ __device__ __forceinline__ void emit8(const ResidualNormArgs& g, int64_t r, int6
   }
 }
 
+// alpha gate pw of eight columns: what the block's output is multiplied by.
+template <class Args>
+__device__ __forceinline__ void factor8(const Args& g, int64_t gate, int64_t i, float* f) {
+  float pw[8];
+  param8(gate_at(g.gate, g.gate_f32, gate * g.H), g.gate_f32, i, g.H, f);
+  param8(g.post_w, g.w_f32, i, g.H, pw);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] = __fmul_rn(__fmul_rn(g.alpha, f[k]), pw[k]);
+}
+
 // T threads cover a row, U groups of eight columns each.  TC: 16 or 64 of
-// them, 256 / TC rows side by side in a workgroup; or 0: the whole workgroup.
-// A workgroup walks rows.
-template <bool XF, bool HF, int TC, int U>
-__global__ __launch_bounds__(TC > 0 ? 256 : 1024) void residual_norm_kernel(ResidualNormArgs g) {
+// them, NT / TC rows side by side in a workgroup; or 0: the whole workgroup.  A
+// workgroup walks `walk` rows (of each side) that lie together, so that a gate is
+// seldom another one: the next row is on its way while this one is summed, and
+// the norms' weights and the gate stay in registers.  FULL: the groups are exactly
+// the row.  16384x5120 BF16 with 8 gates -> BF16 141 us, 4.8 TB/s, bound by memory;
+// -> block codes 139 us, 4.2 TB/s, also by what lies between a row's sums and its
+// codes.
+template <bool XF, bool HF, int TC, int U, int NT, bool FULL>
+__global__ __launch_bounds__(NT) void residual_norm_kernel(ResidualNormArgs g, int64_t walk) {
   __shared__ float red[2][16];
-  constexpr int RPB = TC > 0 ? 256 / (TC > 0 ? TC : 1) : 1;
+  constexpr int RPB = TC > 0 ? NT / (TC > 0 ? TC : 1) : 1;
   const int T = TC > 0 ? TC : blockDim.x, t = TC > 0 ? threadIdx.x % T : threadIdx.x;
-  const float inv_h = 1.0f / (float)g.H, rs = g.out_kind == 1 ? 1.0f / *g.sy : 0.0f;
   const bool has_h = g.h != nullptr, post = g.post_w != nullptr;
+  const int64_t first = (int64_t)blockIdx.x * RPB * walk + (TC > 0 ? threadIdx.x / T : 0);
+  const int64_t end = (int64_t)(blockIdx.x + 1) * RPB * walk < g.rows ? (int64_t)(blockIdx.x + 1) * RPB * walk : g.rows;
+  if (first >= end) return;   // with TC = 0 whole workgroups
+  Raw8<XF> nx[U];
+  Raw8<HF> nh[U];
+  auto load = [&](int64_t r) {
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int64_t i = 8 * (int64_t)(j * T + t);
+      nx[j] = load8<XF, FULL>(row_at<XF>(g.x, r * g.H), i, g.H);
+      if (has_h) nh[j] = load8<HF, FULL>(row_at<HF>(g.h, r * g.H), i, g.H);
+    }
+  };
+  load(first);
+  float w[U][8], f[U][8];
+  auto gate_of = [&](int64_t r) { return (int)((uint32_t)r / (uint32_t)g.gate_rows); };
+  int gate = gate_of(first);
+#pragma unroll
+  for (int j = 0; j < U; ++j) {
+    const int64_t i = 8 * (int64_t)(j * T + t);
+    param8(g.w, g.w_f32, i, g.H, w[j]);
+    if (has_h) factor8(g, gate, i, f[j]);
+  }
+  const float inv_h = 1.0f / (float)g.H, rs = g.out_kind == 1 ? 1.0f / *g.sy : 0.0f;
   // (the sums' LDS takes turns: a wave may be at the next sum while others
   // still read this one)
   int turn = 0;
@@ -101,15 +142,14 @@ __global__ __launch_bounds__(TC > 0 ? 256 : 1024) void residual_norm_kernel(Resi
     turn ^= 1;
     return row_sum<TC>(v, red[turn]);
   };
-  for (int64_t r = (int64_t)blockIdx.x * RPB + (TC > 0 ? threadIdx.x / T : 0); r < g.rows;
-       r += (int64_t)gridDim.x * RPB) {
+  for (int64_t r = first; r < end; r += RPB) {
     float v[U][8], h[U][8];
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      const int64_t i = 8 * (int64_t)(j * T + t);
-      values8<XF>(load8<XF>(row_at<XF>(g.x, r * g.H), i, g.H), v[j]);
-      if (has_h) values8<HF>(load8<HF>(row_at<HF>(g.h, r * g.H), i, g.H), h[j]);
+      values8<XF>(nx[j], v[j]);
+      if (has_h) values8<HF>(nh[j], h[j]);
     }
+    if (r + RPB < end) load(r + RPB);
     if (has_h) {
       float post_rs = 1.0f;
       if (post) {
@@ -119,25 +159,19 @@ __global__ __launch_bounds__(TC > 0 ? 256 : 1024) void residual_norm_kernel(Resi
         post_rs = root(total(s), inv_h, g.eps);
         if (t == 0 && g.post_rstd != nullptr) g.post_rstd[r] = post_rs;
       }
-      const void* gate = gate_at(g.gate, g.gate_f32, (int64_t)((uint32_t)r / (uint32_t)g.gate_rows) * g.H);
+      const int now = gate_of(r);
 #pragma unroll
       for (int j = 0; j < U; ++j) {
         const int64_t i = 8 * (int64_t)(j * T + t);
-        float f[8];
-        if (post) {
-          param8(g.post_w, g.w_f32, i, g.H, f);
+        if (now != gate) factor8(g, now, i, f[j]);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) h[j][k] = __fmul_rn(__fmul_rn(h[j][k], post_rs), f[k]);
+        for (int k = 0; k < 8; ++k) {
+          if (post) h[j][k] = __fmul_rn(h[j][k], post_rs);
+          v[j][k] = __builtin_fmaf(h[j][k], f[j][k], v[j][k]);
         }
-        if (gate != nullptr) {
-          param8(gate, g.gate_f32, i, g.H, f);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) h[j][k] = __fmul_rn(h[j][k], f[k]);
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[j][k] = __builtin_fmaf(g.alpha, h[j][k], v[j][k]);
-        if (i < g.H) store8<XF>(g.r, r * g.H, i, g.H, v[j]);
+        if (FULL || i < g.H) store8<XF>(g.r, r * g.H, i, g.H, v[j]);
       }
+      gate = now;
     }
     float s = 0.0f;
 #pragma unroll
@@ -147,10 +181,8 @@ __global__ __launch_bounds__(TC > 0 ? 256 : 1024) void residual_norm_kernel(Resi
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       const int64_t i = 8 * (int64_t)(j * T + t);
-      float w[8];
-      param8(g.w, g.w_f32, i, g.H, w);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[j][k] = __fmul_rn(__fmul_rn(v[j][k], rstd), w[k]);
+      for (int k = 0; k < 8; ++k) v[j][k] = __fmul_rn(__fmul_rn(v[j][k], rstd), w[j][k]);
       emit8(g, r, i, rs, v[j]);
     }
   }
@@ -182,25 +214,17 @@ __global__ __launch_bounds__(1024) void residual_norm_long_kernel(ResidualNormAr
       post_rs = root(total(s.s), inv_h, g.eps);
       if (threadIdx.x == 0 && g.post_rstd != nullptr) g.post_rstd[r] = post_rs;
     }
-    const void* gate =
-        has_h ? gate_at(g.gate, g.gate_f32, (int64_t)((uint32_t)r / (uint32_t)g.gate_rows) * g.H) : nullptr;
     auto stream8 = [&](int64_t i, float* v) {
       values8<XF>(load8<XF>(row_at<XF>(g.x, base), i, g.H), v);
       if (!has_h) return;
       float h[8], f[8];
       values8<HF>(load8<HF>(row_at<HF>(g.h, base), i, g.H), h);
-      if (post) {
-        param8(g.post_w, g.w_f32, i, g.H, f);
+      factor8(g, (int64_t)((uint32_t)r / (uint32_t)g.gate_rows), i, f);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) h[k] = __fmul_rn(__fmul_rn(h[k], post_rs), f[k]);
+      for (int k = 0; k < 8; ++k) {
+        if (post) h[k] = __fmul_rn(h[k], post_rs);
+        v[k] = __builtin_fmaf(h[k], f[k], v[k]);
       }
-      if (gate != nullptr) {
-        param8(gate, g.gate_f32, i, g.H, f);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) h[k] = __fmul_rn(h[k], f[k]);
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = __builtin_fmaf(g.alpha, h[k], v[k]);
     };
     LongSum s;
     for (int64_t i = 8 * (int64_t)threadIdx.x; i < g.H; i += 8 * 1024) {
@@ -226,59 +250,67 @@ __global__ __launch_bounds__(1024) void residual_norm_long_kernel(ResidualNormAr
 
 unsigned row_grid(int64_t n, int64_t most) { return (unsigned)(n < most ? n : most); }
 
-template <bool XF, bool HF, int TC, int U>
+template <bool XF, bool HF, int TC, int U, int NT>
 hipError_t run_norm(const ResidualNormArgs& g, int threads, hipStream_t stream) {
-  const int rpb = TC > 0 ? 256 / (TC > 0 ? TC : 1) : 1;
-  hipLaunchKernelGGL((residual_norm_kernel<XF, HF, TC, U>), dim3(row_grid((g.rows + rpb - 1) / rpb, 1 << 16)),
-                     dim3(threads), 0, stream, g);
+  const int rpb = TC > 0 ? NT / (TC > 0 ? TC : 1) : 1;
+  // as many workgroups as 24 waves a CU hold (256 CUs) or, but for workgroups of a
+  // multiple of three, 20: 4096x4096 BF16 in two of eight waves 26.1, in three 31.2;
+  // 8000x6000 in two of twelve 87, in one 114
+  const int waves = threads / 64, room = waves % 3 == 0 ? 24 : 20;
+  const int64_t most = 256 * (waves > room ? 1 : room / waves), blocks = (g.rows + rpb - 1) / rpb;
+  const int64_t walk = (blocks + most - 1) / most;
+  const dim3 grid((unsigned)((blocks + walk - 1) / walk));
+  if (TC == 0 && g.H == (int64_t)threads * U * 8)
+    hipLaunchKernelGGL((residual_norm_kernel<XF, HF, TC, U, NT, TC == 0>), grid, dim3(threads), 0, stream, g, walk);
+  else
+    hipLaunchKernelGGL((residual_norm_kernel<XF, HF, TC, U, NT, false>), grid, dim3(threads), 0, stream, g, walk);
   return hipGetLastError();
 }
 
+// One group of eight per thread while a workgroup holds the row so: two or three
+// in fewer threads halve the sums over waves, but leave less in flight
+// (16384x5120 BF16 -> block codes 139 us in 640 threads, 158 in 320, 172 in 256).
 template <bool XF, bool HF>
 hipError_t norm_of_types(const ResidualNormArgs& g, hipStream_t stream) {
   const int64_t units = (g.H + 7) / 8;
-  if (units <= 16) return run_norm<XF, HF, 16, 1>(g, 256, stream);
-  if (units <= 64) return run_norm<XF, HF, 64, 1>(g, 256, stream);
-  if (units <= 1024) return run_norm<XF, HF, 0, 1>(g, (int)((units + 63) / 64 * 64), stream);
-  if (units <= 2048) return run_norm<XF, HF, 0, 2>(g, 1024, stream);
+  if (units <= 16) return run_norm<XF, HF, 16, 1, 256>(g, 256, stream);
+  if (units <= 64) return run_norm<XF, HF, 64, 1, 256>(g, 256, stream);
+  if (units <= 512) return run_norm<XF, HF, 0, 1, 512>(g, (int)((units + 63) / 64 * 64), stream);
+  if (units <= 1024) return run_norm<XF, HF, 0, 1, 1024>(g, (int)((units + 63) / 64 * 64), stream);
+  if (units <= 2048) return run_norm<XF, HF, 0, 2, 1024>(g, 1024, stream);
   hipLaunchKernelGGL((residual_norm_long_kernel<XF, HF>), dim3(row_grid(g.rows, 1 << 20)), dim3(1024), 0, stream, g);
   return hipGetLastError();
 }
 
 // ---- backward ----
 
-// Where a slab's column sums go: its rows of the partial sums, or the results
-// themselves where it is the only one (of its gate).  NULL: not wanted.
-struct Sums {
-  float *w, *post, *gate;
-};
-__device__ __forceinline__ void put_sums(const Sums& o, const ResidualNormBwdArgs& g, int64_t i, const float* pw,
-                                         const float* gate, const float* sw, const float* sa) {
-  float f[8];
-  if (o.w != nullptr) store8_f32(o.w, i, g.H, sw);
-  if (o.post != nullptr) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = __fmul_rn(__fmul_rn(g.alpha, gate[k]), sa[k]);
-    store8_f32(o.post, i, g.H, f);
-  }
-  if (o.gate != nullptr) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = __fmul_rn(__fmul_rn(g.alpha, pw[k]), sa[k]);
-    store8_f32(o.gate, i, g.H, f);
-  }
-}
-
 // The slabs of a launch: per_gate of them cover the rows of each gate, `rows`
-// each.  part: [slabs, 3, H] partial sums.
+// each.  part: [slabs, 2, H] sums over a slab, of dy n and of dx z.
 struct Slabs {
   int64_t per_gate, rows;
   float* part;
 };
-__device__ __forceinline__ Sums sums_of(const ResidualNormBwdArgs& g, const Slabs& s, int64_t slab) {
-  const bool one = g.gates * s.per_gate == 1;
-  float* p = s.part + slab * 3 * g.H;
-  return {g.dw == nullptr ? nullptr : (one ? g.dw : p), g.dpost == nullptr ? nullptr : (one ? g.dpost : p + g.H),
-          g.dgate == nullptr ? nullptr : (s.per_gate == 1 ? g.dgate + slab * g.H : p + 2 * g.H)};
+// A slab's column sums go to its part, or, the only slab of all (or of its gate),
+// to the results themselves.
+__device__ __forceinline__ void put_sums(const ResidualNormBwdArgs& g, const Slabs& s, int64_t slab, int64_t gate,
+                                         int64_t i, const float* sw, const float* sa) {
+  const bool one = g.gates * s.per_gate == 1, wanted = g.dpost != nullptr || g.dgate != nullptr;
+  float* p = s.part + slab * 2 * g.H;
+  float f[8];
+  if (g.dw != nullptr) store8_f32(one ? g.dw : p, i, g.H, sw);
+  if (one && g.dpost != nullptr) {
+    param8(gate_at(g.gate, g.gate_f32, gate * g.H), g.gate_f32, i, g.H, f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = __fmul_rn(__fmul_rn(g.alpha, f[k]), sa[k]);
+    store8_f32(g.dpost, i, g.H, f);
+  }
+  if (s.per_gate == 1 && g.dgate != nullptr) {
+    param8(g.post_w, g.w_f32, i, g.H, f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = __fmul_rn(__fmul_rn(g.alpha, f[k]), sa[k]);
+    store8_f32(g.dgate + slab * g.H, i, g.H, f);
+  }
+  if (!one && wanted) store8_f32(p + g.H, i, g.H, sa);
 }
 
 struct RowRange {
@@ -295,36 +327,61 @@ __device__ __forceinline__ RowRange rows_of_slab(const ResidualNormBwdArgs& g, c
 
 // T threads cover a row, eight columns each (TC: 16 or 64, and as many rows
 // side by side as the workgroup holds; or 0: the whole workgroup).  They walk
-// the rows of the workgroup's slab, which lies within one gate's rows.
-template <bool XF, bool HF, int TC, int NT>
+// the rows of the workgroup's slab, which lies within one gate's rows, the next
+// row's loads on their way during this row's sums.  FULL: the threads' columns
+// are exactly the row.
+template <bool XF, bool HF, int TC, int NT, bool FULL>
 __global__ __launch_bounds__(NT) void residual_norm_backward_kernel(ResidualNormBwdArgs g, Slabs sl) {
   __shared__ float red[2][16];
   __shared__ f4 cols[TC > 0 ? 4 * NT / 2 : 1];
   const int G = TC > 0 ? (int)blockDim.x / (TC > 0 ? TC : 1) : 1;   // rows side by side
   const int t = TC > 0 ? threadIdx.x % (TC > 0 ? TC : 1) : threadIdx.x;
+  const int q = TC > 0 ? threadIdx.x / (TC > 0 ? TC : 1) : 0;
   const float inv_h = 1.0f / (float)g.H;
-  const bool has_h = g.h != nullptr, post = g.post_w != nullptr;
+  const bool has_h = g.h != nullptr, post = g.post_w != nullptr, has_dr = g.dr != nullptr;
   const int64_t i = 8 * (int64_t)t;
-  float w[8], gate[8], pw[8];
-  param8(g.w, g.w_f32, i, g.H, w);
-  param8(g.post_w, g.w_f32, i, g.H, pw);
   int turn = 0;
   auto total = [&](float v) {
     turn ^= 1;
     return row_sum<TC>(v, red[turn]);
   };
+  Raw8<HF> ndy, nz;
+  Raw8<XF> nr, nd;
+  float nrs = 0.0f, npost = 1.0f;
+  auto load8_of = [&](auto& to, const void* p, int64_t r) {
+    constexpr bool F = sizeof(to) == 32;
+    const void* row = row_at<F>(p, r * g.H);
+    to = TC == 16 || FULL ? load8<F, FULL>(row, i, g.H) : load8_ahead<F>(row, i, g.H);
+  };
+  auto load = [&](int64_t r) {
+    load8_of(ndy, g.dy, r);
+    load8_of(nr, g.r, r);
+    if (has_h) load8_of(nz, g.h, r);
+    if (has_dr) load8_of(nd, g.dr, r);
+    nrs = g.rstd[r];
+    if (post) npost = g.post_rstd[r];
+  };
   for (int64_t slab = blockIdx.x; slab < sl.per_gate * g.gates; slab += gridDim.x) {
   const RowRange rr = rows_of_slab(g, sl, slab);
-  float sw[8] = {}, sa[8] = {};
-  param8(gate_at(g.gate, g.gate_f32, rr.gate * g.H), g.gate_f32, i, g.H, gate);
-  for (int64_t r = rr.first + (TC > 0 ? threadIdx.x / (TC > 0 ? TC : 1) : 0); r < rr.end; r += G) {
-    float dy[8], n[8], z[8], d[8];
-    values8<HF>(load8<HF>(row_at<HF>(g.dy, r * g.H), i, g.H), dy);
-    values8<XF>(load8<XF>(row_at<XF>(g.r, r * g.H), i, g.H), n);
-    if (has_h) values8<HF>(load8<HF>(row_at<HF>(g.h, r * g.H), i, g.H), z);
-    if (g.dr != nullptr) values8<XF>(load8<XF>(row_at<XF>(g.dr, r * g.H), i, g.H), d);
-    const float rs = g.rstd[r], post_rs = post ? g.post_rstd[r] : 1.0f;
-    float e[8];
+  int64_t r = rr.first + q;
+  if (r < rr.end) load(r);
+  float w[8], f[8], sw[8] = {}, sa[8] = {};
+  param8(g.w, g.w_f32, i, g.H, w);
+  factor8(g, rr.gate, i, f);
+  for (; r < rr.end; r += G) {
+    float dy[8], n[8], z[8], d[8], e[8];
+    if constexpr (TC != 16 && !FULL) {
+      shift8<HF>(ndy, i, g.H);
+      shift8<XF>(nr, i, g.H);
+      if (has_h) shift8<HF>(nz, i, g.H);
+      if (has_dr) shift8<XF>(nd, i, g.H);
+    }
+    values8<HF>(ndy, dy);
+    values8<XF>(nr, n);
+    if (has_h) values8<HF>(nz, z);
+    if (has_dr) values8<XF>(nd, d);
+    const float rs = nrs, post_rs = npost;
+    if (r + G < rr.end) load(r + G);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       n[k] = __fmul_rn(n[k], rs);
@@ -336,15 +393,15 @@ __global__ __launch_bounds__(NT) void residual_norm_backward_kernel(ResidualNorm
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       n[k] = __fmul_rn(rs, __builtin_fmaf(-n[k], c, dy[k]));
-      if (g.dr != nullptr) n[k] = __fadd_rn(n[k], d[k]);   // dx
+      if (has_dr) n[k] = __fadd_rn(n[k], d[k]);   // dx
     }
-    if (i < g.H) store8<XF>(g.dx, r * g.H, i, g.H, n);
+    if (FULL || i < g.H) store8<XF>(g.dx, r * g.H, i, g.H, n);
     if (has_h) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         if (post) z[k] = __fmul_rn(z[k], post_rs);
         sa[k] = __builtin_fmaf(n[k], z[k], sa[k]);
-        n[k] = __fmul_rn(n[k], __fmul_rn(__fmul_rn(g.alpha, gate[k]), pw[k]));   // p
+        n[k] = __fmul_rn(n[k], f[k]);   // p
         e[k] = __fmul_rn(n[k], z[k]);
       }
       if (post) {
@@ -352,10 +409,9 @@ __global__ __launch_bounds__(NT) void residual_norm_backward_kernel(ResidualNorm
 #pragma unroll
         for (int k = 0; k < 8; ++k) n[k] = __fmul_rn(post_rs, __builtin_fmaf(-z[k], c2, n[k]));
       }
-      if (i < g.H) store8<HF>(g.dh, r * g.H, i, g.H, n);
+      if (FULL || i < g.H) store8<HF>(g.dh, r * g.H, i, g.H, n);
     }
   }
-  const int q = TC > 0 ? threadIdx.x / (TC > 0 ? TC : 1) : 0;
   if constexpr (TC > 0) {
     // the rows side by side (a power of two) are added in a tree
     for (int h = G >> 1; h > 0; h >>= 1) {
@@ -377,7 +433,7 @@ __global__ __launch_bounds__(NT) void residual_norm_backward_kernel(ResidualNorm
       __syncthreads();
     }
   }
-  if (q == 0 && i < g.H) put_sums(sums_of(g, sl, slab), g, i, pw, gate, sw, sa);
+  if (q == 0 && i < g.H) put_sums(g, sl, slab, rr.gate, i, sw, sa);
   }
 }
 
@@ -443,12 +499,9 @@ __global__ __launch_bounds__(256) void residual_norm_columns_long_kernel(Residua
                                                                          const float* __restrict__ c) {
   const int64_t i = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
   if (i >= g.H) return;
-  float gate[8], pw[8];
-  param8(g.post_w, g.w_f32, i, g.H, pw);
   for (int64_t slab = blockIdx.y; slab < sl.per_gate * g.gates; slab += gridDim.y) {
     const RowRange rr = rows_of_slab(g, sl, slab);
     float sw[8] = {}, sa[8] = {};
-    param8(gate_at(g.gate, g.gate_f32, rr.gate * g.H), g.gate_f32, i, g.H, gate);
     for (int64_t r = rr.first; r < rr.end; ++r) {
       const LongRow a = long_row(g, c, r);
       float dy[8], n[8], gw[8], dx[8], z[8] = {};
@@ -460,7 +513,7 @@ __global__ __launch_bounds__(256) void residual_norm_columns_long_kernel(Residua
         sa[k] = __builtin_fmaf(dx[k], z[k], sa[k]);
       }
     }
-    put_sums(sums_of(g, sl, slab), g, i, pw, gate, sw, sa);
+    put_sums(g, sl, slab, rr.gate, i, sw, sa);
   }
 }
 
@@ -474,16 +527,14 @@ __global__ __launch_bounds__(1024) void residual_norm_dx_long_kernel(ResidualNor
   int turn = 0;
   for (int64_t r = blockIdx.x; r < g.rows; r += gridDim.x, turn ^= 1) {
     const LongRow a = long_row(g, c, r);
-    const void* gate = gate_at(g.gate, g.gate_f32, r / gate_rows * g.H);
     auto row8 = [&](int64_t i, float* dx, float* z, float* p) {
-      float dy[8], n[8], gw[8], f[8], e[8];
+      float dy[8], n[8], gw[8], f[8];
       long_row8<XF, HF>(g, r, i, a.rs, dy, n, gw);
       long_dx8<XF, HF>(g, r, i, a, n, gw, dx, z);
       if (!has_h) return;
-      param8(gate, g.gate_f32, i, g.H, f);
-      param8(g.post_w, g.w_f32, i, g.H, e);
+      factor8(g, r / gate_rows, i, f);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) p[k] = __fmul_rn(dx[k], __fmul_rn(__fmul_rn(g.alpha, f[k]), e[k]));
+      for (int k = 0; k < 8; ++k) p[k] = __fmul_rn(dx[k], f[k]);
     };
     float c2 = 0.0f;
     if (has_h && post) {
@@ -511,43 +562,77 @@ __global__ __launch_bounds__(1024) void residual_norm_dx_long_kernel(ResidualNor
   }
 }
 
-// Sums over slabs of part [slabs, 3, H], in an order that depends on the sizes
-// alone: plane 0 and 1 over all slabs, and with `each_gate` the third for every
-// gate over its own (y = 2 + gate).  64 columns a workgroup, four per thread;
-// sixteen threads share a column's slabs.
+// Columns n .. n + 3 of a gate (zeros past the row).
+__device__ __forceinline__ void gate4(const ResidualNormBwdArgs& g, int64_t gate, int64_t n, float* f) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) f[k] = n + k < g.H ? param1(g.gate, g.gate_f32, gate * g.H + n + k) : 0.0f;
+}
+
+// The results from part, in an order that depends on the sizes alone: y = 0
+// dweight, sums over all slabs; 1 dpost_weight, sums over all slabs of the second
+// plane times the slab's gate; 2 + a (with each_gate) dgate a, its slabs' sums.  A
+// workgroup takes 4 Q columns, four per thread, and L threads share a column's
+// slabs.
+template <int Q>
 __global__ __launch_bounds__(256) void residual_norm_sums_kernel(ResidualNormBwdArgs g, Slabs sl, int each_gate) {
-  __shared__ float red[16][68];
-  const int q = threadIdx.x & 15, s = threadIdx.x >> 4;
+  constexpr int L = 256 / Q, C = 4 * Q, P = 256 / C, R = 4;
+  static_assert(L / P == 4, "four rows of red per thread");
+  __shared__ float red[L][C + 1], red2[P][C + 1];
+  const int q = threadIdx.x % Q, s = threadIdx.x / Q;
+  const int64_t n = (int64_t)blockIdx.x * C + 4 * q, per_gate = sl.per_gate;
   for (int64_t y = blockIdx.y; y < 2 + (each_gate ? g.gates : 0); y += gridDim.y, __syncthreads()) {
-    const int plane = y < 2 ? (int)y : 2;
-    float* out = plane == 0 ? g.dw : plane == 1 ? g.dpost : (g.dgate == nullptr ? nullptr : g.dgate + (y - 2) * g.H);
+    float* out = y == 0 ? g.dw : y == 1 ? g.dpost : (g.dgate == nullptr ? nullptr : g.dgate + (y - 2) * g.H);
     if (out == nullptr) continue;
-    const int64_t first = plane < 2 ? 0 : (y - 2) * sl.per_gate, count = (plane < 2 ? g.gates : 1) * sl.per_gate;
-    const int64_t n = (int64_t)blockIdx.x * 64 + 4 * q;
-    const float* v = sl.part + (first * 3 + plane) * g.H + n;
+    const int64_t first = y < 2 ? 0 : (y - 2) * per_gate, count = (y < 2 ? g.gates : 1) * per_gate;
+    const float* v = sl.part + (first * 2 + (y > 0)) * g.H;
+    const bool by_gate = y == 1 && g.gate != nullptr;
     float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (n + 4 <= g.H) {
-#pragma unroll 4
-      for (int64_t p = s; p < count; p += 16) {
-        const f4 x = *reinterpret_cast<const f4a4*>(v + p * 3 * g.H);
+    auto four = [&](const float* row, float* x) {
+      if (n + 4 <= g.H) {
+        const f4 w = *reinterpret_cast<const f4a4*>(row + n);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) t[k] = __fadd_rn(t[k], x[k]);
+        for (int k = 0; k < 4; ++k) x[k] = w[k];
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = n + k < g.H ? row[n + k] : 0.0f;
       }
-    } else {
-      for (int64_t p = s; p < count; p += 16)
+    };
+    int64_t p = s;
+    for (; p + L * (R - 1) < count; p += L * R) {
+      float x[R][4], f[R][4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (n + k < g.H) t[k] = __fadd_rn(t[k], v[p * 3 * g.H + k]);
+      for (int r = 0; r < R; ++r) {
+        four(v + (p + L * r) * 2 * g.H, x[r]);
+        if (by_gate) gate4(g, (p + L * r) / per_gate, n, f[r]);
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) t[k] = by_gate ? __builtin_fmaf(x[r][k], f[r][k], t[k]) : __fadd_rn(t[k], x[r][k]);
+    }
+    for (; p < count; p += L) {
+      float x[4], f[4];
+      four(v + p * 2 * g.H, x);
+      if (by_gate) gate4(g, p / per_gate, n, f);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) t[k] = by_gate ? __builtin_fmaf(x[k], f[k], t[k]) : __fadd_rn(t[k], x[k]);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) red[s][4 * q + k] = t[k];
     __syncthreads();
-    if (threadIdx.x < 64) {
-      float u = red[0][threadIdx.x];
+    {
+      const int c = threadIdx.x % C, h = threadIdx.x / C;
+      red2[h][c] = __fadd_rn(__fadd_rn(red[4 * h][c], red[4 * h + 1][c]), __fadd_rn(red[4 * h + 2][c], red[4 * h + 3][c]));
+    }
+    __syncthreads();
+    const int64_t c = (int64_t)blockIdx.x * C + threadIdx.x;
+    if (threadIdx.x < C && c < g.H) {
+      float u = red2[0][threadIdx.x];
 #pragma unroll
-      for (int p = 1; p < 16; ++p) u = __fadd_rn(u, red[p][threadIdx.x]);
-      const int64_t c = (int64_t)blockIdx.x * 64 + threadIdx.x;
-      if (c < g.H) out[c] = u;
+      for (int h = 1; h < P; ++h) u = __fadd_rn(u, red2[h][threadIdx.x]);
+      if (y > 0) u = __fmul_rn(u, g.alpha);
+      if (y > 1 && g.post_w != nullptr) u = __fmul_rn(u, param1(g.post_w, g.w_f32, c));
+      out[c] = u;
     }
   }
 }
@@ -555,7 +640,13 @@ __global__ __launch_bounds__(256) void residual_norm_sums_kernel(ResidualNormBwd
 // rows of up to this many elements go through residual_norm_backward_kernel
 constexpr int64_t kBwdRegs = 1024 * 8;
 
-// Threads of a workgroup, rows side by side in it, slabs for each gate.
+// Threads of a workgroup, rows side by side in it, slabs for each gate: one
+// workgroup of eight waves or more per CU, two of four to seven, three of fewer
+// (16384x5120 BF16 210 us with 256 slabs, 239 with 384; 16384x2048 97, 92 with 512;
+// 12000x1027 60 with 512, 55 with 768), of at least one, two or four rows one after
+// another by the number of rows, since every slab's sums are written and read once
+// more (256x4096 16.9 with four, 15.0 with two).  A few rows are one slab, whose
+// sums need no second launch.
 struct BwdShape {
   int threads, side;
   int64_t per_gate;
@@ -570,39 +661,45 @@ BwdShape bwd_shape(int64_t rows, int64_t H, int64_t gates) {
     slabs = room < 1 ? 1 : room < 256 ? room : 256;
   } else if (units <= 64) {
     const int tc = units <= 16 ? 16 : 64;
-    b.threads = 256;
+    b.threads = rows >= 256 * 4 * (512 / tc) ? 512 : 256;
     b.side = b.threads / tc;
-    slabs = 768;
   } else {
     b.threads = (int)((units + 63) / 64 * 64);
-    slabs = b.threads >= 512 ? 256 : b.threads >= 192 ? 512 : 768;
   }
-  if (rows <= 4 * b.side && gates == 1) slabs = 1;
+  if (H <= kBwdRegs) slabs = b.threads >= 512 ? 256 : b.threads >= 256 ? 512 : 768;
+  if (rows <= (H <= 4096 ? 4 : 2) * b.side && gates == 1) slabs = 1;
   b.per_gate = (slabs + gates - 1) / gates;
-  const int64_t most = (gate_rows + b.side - 1) / b.side;
+  const int64_t walk = H > kBwdRegs ? 4 : b.side > 1 || rows <= 64 ? 1 : rows <= 256 ? 2 : 4;
+  const int64_t most = (gate_rows + walk * b.side - 1) / (walk * b.side);
   if (b.per_gate > most) b.per_gate = most;
   return b;
+}
+
+template <bool XF, bool HF, int TC, int NT>
+hipError_t run_backward_kernel(const ResidualNormBwdArgs& g, const BwdShape& b, const Slabs& sl, hipStream_t stream) {
+  const dim3 grid(row_grid(g.gates * b.per_gate, 1 << 20)), block(b.threads);
+  if (TC == 0 && g.H == (int64_t)b.threads * 8)
+    hipLaunchKernelGGL((residual_norm_backward_kernel<XF, HF, TC, NT, TC == 0>), grid, block, 0, stream, g, sl);
+  else
+    hipLaunchKernelGGL((residual_norm_backward_kernel<XF, HF, TC, NT, false>), grid, block, 0, stream, g, sl);
+  return hipGetLastError();
 }
 
 template <bool XF, bool HF>
 hipError_t run_backward(const ResidualNormBwdArgs& g, const BwdShape& b, const Slabs& sl, float* c,
                         hipStream_t stream) {
-  const int64_t slabs = g.gates * b.per_gate;
-  const dim3 grid(row_grid(slabs, 1 << 20));
-  if (g.H <= 128) {
-    hipLaunchKernelGGL((residual_norm_backward_kernel<XF, HF, 16, 256>), grid, dim3(b.threads), 0, stream, g, sl);
-  } else if (g.H <= 512) {
-    hipLaunchKernelGGL((residual_norm_backward_kernel<XF, HF, 64, 256>), grid, dim3(b.threads), 0, stream, g, sl);
-  } else if (g.H <= kBwdRegs) {
-    hipLaunchKernelGGL((residual_norm_backward_kernel<XF, HF, 0, 1024>), grid, dim3(b.threads), 0, stream, g, sl);
-  } else {
-    const unsigned rows = row_grid(g.rows, 1 << 20);
-    hipLaunchKernelGGL((residual_norm_row_long_kernel<XF, HF>), dim3(rows), dim3(1024), 0, stream, g, c);
-    if (g.dw != nullptr || g.dgate != nullptr || g.dpost != nullptr)
-      hipLaunchKernelGGL((residual_norm_columns_long_kernel<XF, HF>), dim3((unsigned)((g.H + 2047) / 2048), row_grid(slabs, 65535)),
-                         dim3(256), 0, stream, g, sl, c);
-    hipLaunchKernelGGL((residual_norm_dx_long_kernel<XF, HF>), dim3(rows), dim3(1024), 0, stream, g, c);
-  }
+  if (g.H <= 128) return run_backward_kernel<XF, HF, 16, 512>(g, b, sl, stream);
+  if (g.H <= 512) return run_backward_kernel<XF, HF, 64, 512>(g, b, sl, stream);
+  if (b.threads <= 512) return run_backward_kernel<XF, HF, 0, 512>(g, b, sl, stream);
+  if (b.threads <= 768) return run_backward_kernel<XF, HF, 0, 768>(g, b, sl, stream);
+  if (g.H <= kBwdRegs) return run_backward_kernel<XF, HF, 0, 1024>(g, b, sl, stream);
+  const unsigned rows = row_grid(g.rows, 1 << 20);
+  hipLaunchKernelGGL((residual_norm_row_long_kernel<XF, HF>), dim3(rows), dim3(1024), 0, stream, g, c);
+  if (g.dw != nullptr || g.dgate != nullptr || g.dpost != nullptr)
+    hipLaunchKernelGGL((residual_norm_columns_long_kernel<XF, HF>),
+                       dim3((unsigned)((g.H + 2047) / 2048), row_grid(g.gates * b.per_gate, 65535)), dim3(256), 0,
+                       stream, g, sl, c);
+  hipLaunchKernelGGL((residual_norm_dx_long_kernel<XF, HF>), dim3(rows), dim3(1024), 0, stream, g, c);
   return hipGetLastError();
 }
 
@@ -616,7 +713,7 @@ hipError_t launch_residual_norm(const ResidualNormArgs& g, hipStream_t stream) {
 int64_t residual_norm_backward_floats(int64_t rows, int64_t H, int64_t gates) {
   if (rows == 0 || H == 0) return 0;
   const int64_t slabs = gates * bwd_shape(rows, H, gates).per_gate;
-  return (slabs > 1 ? slabs * 3 * H : 0) + (H > kBwdRegs ? rows : 0);
+  return (slabs > 1 ? slabs * 2 * H : 0) + (H > kBwdRegs ? rows : 0);
 }
 
 hipError_t launch_residual_norm_backward(const ResidualNormBwdArgs& g, float* ws, hipStream_t stream) {
@@ -627,7 +724,7 @@ hipError_t launch_residual_norm_backward(const ResidualNormBwdArgs& g, float* ws
     const int64_t slabs = g.gates * b.per_gate, gate_rows = g.rows / g.gates;
     sl.per_gate = b.per_gate;
     sl.rows = (gate_rows + b.per_gate - 1) / b.per_gate;
-    float* c = ws + (slabs > 1 ? slabs * 3 * g.H : 0);
+    float* c = ws + (slabs > 1 ? slabs * 2 * g.H : 0);
     hipError_t e;
     if (g.x_f32) e = g.h_f32 ? run_backward<true, true>(g, b, sl, c, stream) : run_backward<true, false>(g, b, sl, c, stream);
     else e = g.h_f32 ? run_backward<false, true>(g, b, sl, c, stream) : run_backward<false, false>(g, b, sl, c, stream);
@@ -635,9 +732,14 @@ hipError_t launch_residual_norm_backward(const ResidualNormBwdArgs& g, float* ws
     each_gate = b.per_gate > 1;
   }
   if (g.dw == nullptr && g.dpost == nullptr && (g.dgate == nullptr || !each_gate)) return hipSuccess;
-  hipLaunchKernelGGL(residual_norm_sums_kernel,
-                     dim3((unsigned)((g.H + 63) / 64), row_grid(2 + (each_gate ? g.gates : 0), 65535)), dim3(256), 0,
-                     stream, g, sl, each_gate ? 1 : 0);
+  // (few columns in workgroups of 64 would leave most CUs idle)
+  const unsigned planes = row_grid(2 + (each_gate ? g.gates : 0), 65535);
+  if (g.H * planes >= 32768)
+    hipLaunchKernelGGL(residual_norm_sums_kernel<16>, dim3((unsigned)((g.H + 63) / 64), planes), dim3(256), 0, stream, g,
+                       sl, each_gate ? 1 : 0);
+  else
+    hipLaunchKernelGGL(residual_norm_sums_kernel<4>, dim3((unsigned)((g.H + 15) / 16), planes), dim3(256), 0, stream, g,
+                       sl, each_gate ? 1 : 0);
   return hipGetLastError();
 }
 
