@@ -41,7 +41,8 @@ __device__ __forceinline__ float silu_mul_close(float g, float u) {
 // Blocks of 128 columns.  Sixteen lanes take a block, eight columns each, R
 // blocks one after another with all their loads in flight.  FLAT: rows are
 // whole blocks, so that block i lies at element 128 i of x and of q and no
-// division finds its row.
+// division finds its row.  16384x5120 BF16 42 us, 5.9 TB/s; SwiGLU 4096x12288 44
+// to 51 us, 5.1 to 5.9 TB/s.
 template <bool F32, bool SILU, bool FLAT, int R>
 __global__ __launch_bounds__(256) void quant_rows_kernel(const void* __restrict__ x, const void* __restrict__ u,
                                                          uint8_t* __restrict__ q, float* __restrict__ scales,
@@ -90,35 +91,35 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const void* __restrict_
   }
 }
 
-// 128 x 128 squares of x, a workgroup each: thread t takes columns 8 (t % 16)
-// .. + 7 of rows 8 (t / 16) .. + 7.  TILE: one scale for the square; else (with
-// TRANS) one for each of its columns.  TRANS: the codes of the transposed
-// tensor, turned through 16 KB of LDS (eight codes of one column, rows 8 r ..
-// 8 r + 7, lie at chunk r ^ (column / 8) of the column's 128 bytes, which
+// 128 x 128 tiles of x with one scale each, a workgroup to a tile (25600x5120 BF16
+// 75 us, 5.3 TB/s; transposed 81): thread t takes
+// columns 8 (t % 16) .. + 7 of rows 8 (t / 16) .. + 7.  TRANS: the codes of the
+// transposed tensor, turned through 16 KB of LDS (eight codes of one column, rows
+// 8 r .. 8 r + 7, lie at chunk r ^ (column / 8) of the column's 128 bytes, which
 // spreads both accesses over the banks).
-template <bool F32, bool TILE, bool TRANS>
-__global__ __launch_bounds__(256) void quant_square_kernel(const void* __restrict__ x, uint8_t* __restrict__ q,
-                                                           float* __restrict__ scales, int64_t M, int64_t K) {
-  __shared__ int top[TILE ? 4 : 4 * kBlock];
+template <bool F32, bool TRANS>
+__global__ __launch_bounds__(256) void quant_tile_kernel(const void* __restrict__ x, uint8_t* __restrict__ q,
+                                                         float* __restrict__ scales, int64_t M, int64_t K) {
+  __shared__ int top[4];
   __shared__ __attribute__((aligned(16))) uint8_t turn[TRANS ? kBlock * kBlock : 16];
   const int cl = threadIdx.x & 15, rl = threadIdx.x >> 4;
   const int64_t kb = (K + kBlock - 1) / kBlock, mb = (M + kBlock - 1) / kBlock;
-  for (int64_t square = blockIdx.x; square < kb * mb; square += gridDim.x) {
-  const int64_t tm = square / kb, tk = square - tm * kb;
-  const int64_t m0 = tm * kBlock + 8 * rl, k0 = tk * kBlock + 8 * cl;
-  Raw8<F32> raw[8];
+  for (int64_t tile = blockIdx.x; tile < kb * mb; tile += gridDim.x) {
+    const int64_t tm = tile / kb, tk = tile - tm * kb;
+    const int64_t m0 = tm * kBlock + 8 * rl, k0 = tk * kBlock + 8 * cl;
+    Raw8<F32> raw[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (m0 + j < M) raw[j] = load8<F32>(static_cast<const uint8_t*>(x) + (m0 + j) * K * (F32 ? 4 : 2), k0, K);
-    else raw[j] = Raw8<F32>{};
-  }
-  float f[8][8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) values8<F32>(raw[j], f[j]);
-  if constexpr (TILE) {
+    for (int j = 0; j < 8; ++j) {
+      if (m0 + j < M) raw[j] = load8<F32>(static_cast<const uint8_t*>(x) + (m0 + j) * K * (F32 ? 4 : 2), k0, K);
+      else raw[j] = Raw8<F32>{};
+    }
+    float f[8][8];
     int m = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, block::max8(f[j]));
+    for (int j = 0; j < 8; ++j) {
+      values8<F32>(raw[j], f[j]);
+      m = max(m, block::max8(f[j]));
+    }
     m = block::max16(m);
     m = max(max(__builtin_amdgcn_readlane(m, 0), __builtin_amdgcn_readlane(m, 16)),
             max(__builtin_amdgcn_readlane(m, 32), __builtin_amdgcn_readlane(m, 48)));
@@ -128,56 +129,107 @@ __global__ __launch_bounds__(256) void quant_square_kernel(const void* __restric
 #pragma unroll
     for (int j = 0; j < 8; ++j) block::quotients<8>(f[j], s);
     if (threadIdx.x == 0) scales[TRANS ? tk * mb + tm : tm * kb + tk] = s;
-  } else {
-    // over the thread's rows, then its wave's four threads of the same
-    // columns, then the waves
+    if constexpr (!TRANS) {
+      const int64_t Kp = (K + 15) / 16 * 16;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (m0 + j < M && k0 < Kp)
+          *reinterpret_cast<u2a1*>(q + (m0 + j) * Kp + k0) =
+              (u2a1){e4m3_pack4(f[j][0], f[j][1], f[j][2], f[j][3]), e4m3_pack4(f[j][4], f[j][5], f[j][6], f[j][7])};
+    } else {
+      uint2* const at = reinterpret_cast<uint2*>(turn);
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        at[(8 * cl + c) * 16 + (rl ^ cl)] = make_uint2(e4m3_pack4(f[0][c], f[1][c], f[2][c], f[3][c]),
+                                                       e4m3_pack4(f[4][c], f[5][c], f[6][c], f[7][c]));
+      __syncthreads();
+      const int64_t Mp = (M + 15) / 16 * 16, m1 = tm * kBlock + 8 * cl;
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        const int c = 16 * p + rl;   // column of x, row of the codes
+        const uint2 v = at[c * 16 + (cl ^ (c >> 3))];
+        if (tk * kBlock + c < K && m1 < Mp)
+          *reinterpret_cast<u2a1*>(q + (tk * kBlock + c) * Mp + m1) = (u2a1){v.x, v.y};
+      }
+    }
+    __syncthreads();   // LDS is free for the next tile
+  }
+}
+
+// Blocks of 128 rows of a column, as rows of the transposed tensor.  A workgroup
+// takes 128 rows by 8 LC columns: thread t columns 8 (t % LC) .. + 7 of rows
+// R (t / LC) .. + R - 1, R = LC / 2.  The columns' maxima are joined through LDS,
+// where one thread per column forms the scale and its reciprocal (each thread for
+// itself: 25600x5120 103 us, 89 so), and the codes are turned through it: R codes of a
+// column, rows R r .. + R - 1, lie at chunk r ^ (TURN * (column / 8)) of its 128 bytes,
+// which spreads the writes over the banks.
+template <bool F32, int LC>
+__global__ __launch_bounds__(256) void quant_columns_kernel(const void* __restrict__ x, uint8_t* __restrict__ q,
+                                                            float* __restrict__ scales, int64_t M, int64_t K) {
+  constexpr int C = 8 * LC, RL = 256 / LC, R = kBlock / RL, D = R / 4;   // D: dwords of codes per thread and column
+  static_assert(R == 4 || R == 8, "");
+  constexpr int TURN = LC == 16 ? 1 : 4;   // chunks by which neighbouring lanes' columns are turned
+  __shared__ __attribute__((aligned(16))) uint32_t turn[C * kBlock / 4];
+  __shared__ float scale[C], inverse[C];
+  static_assert(RL * C <= C * kBlock / 4, "the maxima fit the codes' LDS");
+  int (*const top)[C] = reinterpret_cast<int (*)[C]>(turn);   // until the scales are known
+  const int cl = threadIdx.x % LC, rl = threadIdx.x / LC;
+  const int64_t kb = (K + C - 1) / C, mb = (M + kBlock - 1) / kBlock;
+  for (int64_t part = blockIdx.x; part < kb * mb; part += gridDim.x) {
+    const int64_t tm = part / kb, k1 = (part - tm * kb) * C;
+    const int64_t m0 = tm * kBlock + R * rl, k0 = k1 + 8 * cl;
+    Raw8<F32> raw[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      if (m0 + j < M) raw[j] = load8<F32>(static_cast<const uint8_t*>(x) + (m0 + j) * K * (F32 ? 4 : 2), k0, K);
+      else raw[j] = Raw8<F32>{};
+    }
+    float f[R][8];
+#pragma unroll
+    for (int j = 0; j < R; ++j) values8<F32>(raw[j], f[j]);
+    int m[8];
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      int m = 0;
+      m[c] = block::magnitude(f[0][c]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) m = max(m, block::magnitude(f[j][c]));
-      m = max(m, __shfl_xor(m, 16));
-      m = max(m, __shfl_xor(m, 32));
-      if ((threadIdx.x & 63) < 16) top[(threadIdx.x >> 6) * kBlock + 8 * cl + c] = m;
+      for (int j = 1; j < R; ++j) m[c] = max(m[c], block::magnitude(f[j][c]));
+    }
+    *reinterpret_cast<int4*>(&top[rl][8 * cl]) = make_int4(m[0], m[1], m[2], m[3]);
+    *reinterpret_cast<int4*>(&top[rl][8 * cl + 4]) = make_int4(m[4], m[5], m[6], m[7]);
+    __syncthreads();
+    if (threadIdx.x < C) {
+      const int c = threadIdx.x;
+      int t = top[0][c];
+#pragma unroll
+      for (int r = 1; r < RL; ++r) t = max(t, top[r][c]);
+      const float s = block::scale_of(t);
+      scale[c] = s;
+      inverse[c] = 1.0f / s;
+      if (k1 + c < K) scales[(k1 + c) * mb + tm] = s;
+    }
+    __syncthreads();
+    const int64_t Mp = (M + 15) / 16 * 16;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const float s = scale[8 * cl + c], r = inverse[8 * cl + c];
+      float v[R];
+#pragma unroll
+      for (int j = 0; j < R; ++j) v[j] = f[j][c];
+      block::quotients<R>(v, s, r);
+#pragma unroll
+      for (int d = 0; d < D; ++d)
+        turn[(8 * cl + c) * 32 + (rl ^ (cl * TURN)) * D + d] =
+            e4m3_pack4(v[4 * d], v[4 * d + 1], v[4 * d + 2], v[4 * d + 3]);
     }
     __syncthreads();
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const int* t = top + 8 * cl + c;
-      const float s = block::scale_of(max(max(t[0], t[kBlock]), max(t[2 * kBlock], t[3 * kBlock])));
-      float v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = f[j][c];
-      block::quotients<8>(v, s);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j][c] = v[j];
-      if (rl == 0 && k0 + c < K) scales[(k0 + c) * mb + tm] = s;
+    for (int p = 0; p < C / 8; ++p) {
+      const int c = 8 * p + (threadIdx.x >> 5), w = threadIdx.x & 31;   // column of x, dword of its codes
+      const uint32_t v = turn[c * 32 + ((w / D) ^ ((c >> 3) * TURN)) * D + w % D];
+      if (k1 + c < K && tm * kBlock + 4 * w < Mp)
+        *reinterpret_cast<uint32_t*>(q + (k1 + c) * Mp + tm * kBlock + 4 * w) = v;
     }
-  }
-  if constexpr (!TRANS) {
-    const int64_t Kp = (K + 15) / 16 * 16;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (m0 + j < M && k0 < Kp)
-        *reinterpret_cast<u2a1*>(q + (m0 + j) * Kp + k0) =
-            (u2a1){e4m3_pack4(f[j][0], f[j][1], f[j][2], f[j][3]), e4m3_pack4(f[j][4], f[j][5], f[j][6], f[j][7])};
-  } else {
-    uint2* const at = reinterpret_cast<uint2*>(turn);
-#pragma unroll
-    for (int c = 0; c < 8; ++c)
-      at[(8 * cl + c) * 16 + (rl ^ cl)] = make_uint2(e4m3_pack4(f[0][c], f[1][c], f[2][c], f[3][c]),
-                                                     e4m3_pack4(f[4][c], f[5][c], f[6][c], f[7][c]));
-    __syncthreads();
-    const int64_t Mp = (M + 15) / 16 * 16, m = tm * kBlock + 8 * cl;
-#pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      const int c = 16 * p + rl;   // column of x, row of the codes
-      const uint2 v = at[c * 16 + (cl ^ (c >> 3))];
-      if (tk * kBlock + c < K && m < Mp)
-        *reinterpret_cast<u2a1*>(q + (tk * kBlock + c) * Mp + m) = (u2a1){v.x, v.y};
-    }
-  }
-  __syncthreads();   // LDS is free for the next square
+    __syncthreads();   // LDS is free for the next part
   }
 }
 
@@ -199,14 +251,20 @@ template <bool F32>
 hipError_t run_quant(const void* x, uint8_t* q, float* scales, int64_t M, int64_t K, int tile, int transpose,
                      hipStream_t stream) {
   if (!tile && !transpose) return run_rows<F32, false>(x, nullptr, q, scales, M, K, stream);
-  const int64_t squares = ((M + kBlock - 1) / kBlock) * ((K + kBlock - 1) / kBlock);
-  const dim3 grid((unsigned)(squares < (1 << 20) ? squares : (1 << 20)));
-  if (!tile)
-    hipLaunchKernelGGL((quant_square_kernel<F32, false, true>), grid, dim3(256), 0, stream, x, q, scales, M, K);
-  else if (transpose)
-    hipLaunchKernelGGL((quant_square_kernel<F32, true, true>), grid, dim3(256), 0, stream, x, q, scales, M, K);
-  else
-    hipLaunchKernelGGL((quant_square_kernel<F32, true, false>), grid, dim3(256), 0, stream, x, q, scales, M, K);
+  const int64_t mb = (M + kBlock - 1) / kBlock, squares = mb * ((K + kBlock - 1) / kBlock);
+  auto grid = [](int64_t n) { return dim3((unsigned)(n < (1 << 20) ? n : (1 << 20))); };
+  if (tile) {
+    if (transpose)
+      hipLaunchKernelGGL((quant_tile_kernel<F32, true>), grid(squares), dim3(256), 0, stream, x, q, scales, M, K);
+    else
+      hipLaunchKernelGGL((quant_tile_kernel<F32, false>), grid(squares), dim3(256), 0, stream, x, q, scales, M, K);
+  } else if (squares <= 1024) {
+    // 64 columns: more workgroups (1531x2053 8.4 us, 11.4 with 128; 25600x5120 96, 89)
+    hipLaunchKernelGGL((quant_columns_kernel<F32, 8>), grid(mb * ((K + 63) / 64)), dim3(256), 0, stream, x, q, scales, M,
+                       K);
+  } else {
+    hipLaunchKernelGGL((quant_columns_kernel<F32, 16>), grid(squares), dim3(256), 0, stream, x, q, scales, M, K);
+  }
   return hipGetLastError();
 }
 

@@ -41,17 +41,22 @@ __device__ __forceinline__ int max16(int v) {
 
 __device__ __forceinline__ float scale_of(int amax) { return __int_as_float(amax) / 448.0f; }
 
-// f = f / s for the encoder (see div_by_scale).
+// f = f / s for the encoder (see div_by_scale); r = 1 / s.
 template <int N>
-__device__ __forceinline__ void quotients(float* f, float s) {
+__device__ __forceinline__ void quotients(float* f, float s, float r) {
   if (div_by_scale_ok(s)) {
-    const float r = 1.0f / s, lim = 1024.0f * s;
+    const float lim = 1024.0f * s;
 #pragma unroll
     for (int k = 0; k < N; ++k) f[k] = div_by_scale(f[k], s, r, lim);
   } else if (s != 0.0f) {
 #pragma unroll
     for (int k = 0; k < N; ++k) f[k] = f[k] / s;
   }
+}
+
+template <int N>
+__device__ __forceinline__ void quotients(float* f, float s) {
+  quotients<N>(f, s, 1.0f / s);
 }
 
 }  // namespace block
