@@ -307,12 +307,10 @@ __global__ __launch_bounds__(WM* WN * 64 * KSPL, 2) void linear_block_tile_kerne
   }
   // Per stage: before the MFMAs of a step the next step's fragments are read;
   // at the last step wait for the next stage's copies and this wave's own
-  // reads, barrier, read ahead, and refill the freed buffer with stage s + 2
-  // (past the end: zeros into a buffer nobody reads again -- at the last
-  // stage, where no barrier has freed this one, the next one).  The scales of
-  // the next batch go out after the first stage of this one, whose barrier
-  // follows the last use of their slot.  inside: stage s + 2 of both groups
-  // exists, so that nothing is asked or selected per stage.
+  // reads, barrier, read ahead, and refill the freed buffer with stage s + 2.
+  // The scales of the next batch go out after the first stage of this one, whose
+  // barrier follows the last use of their slot.  inside: stage s + 2 of both
+  // groups exists, so that nothing is asked or selected per stage.
   auto stage = [&](auto buffer, int s, auto inside) {
     constexpr bool kInside = decltype(inside)::value;
     constexpr int u = decltype(buffer)::value;
@@ -347,7 +345,9 @@ __global__ __launch_bounds__(WM* WN * 64 * KSPL, 2) void linear_block_tile_kerne
     stage(buf0, s, no);
     if (s + 1 < KT) stage(buf1, s + 1, no);
   }
-  if (KT > 0) {
+  // (of an odd number of stages the second group has no last one: its scale would
+  // be the next row's, which zeros times an infinity would not survive)
+  if (KT > 0 && gstage(KT - 1) < stages) {
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
       v4f w[4];

@@ -133,6 +133,23 @@ def test_nan_and_infinite_scales_stay_in_their_rows(M, N, K):
     assert torch.equal(y.cpu()[~bad], clean.cpu()[~bad])
 
 
+@pytest.mark.parametrize("w_rows", [False, True])
+@pytest.mark.parametrize("K", [1264, 1296, 1408])   # 10 and 11 blocks, whole and not
+def test_infinite_first_scales_stay_in_their_rows(K, w_rows):
+    # the two halves of K that a tile's wave groups take end at different blocks
+    M, N = 1500, 1450
+    qx, qw, sx, sw, _ = operands(M, N, K, w_rows, 10)
+    y = fp8.fp8_linear_block(*on(qx, qw, sx, sw), out_kind=fp8.OUT_F32)
+    sx2, sw2 = sx.clone(), sw.clone()
+    sx2[1::2, 0] = float("inf")
+    sw2[1::2, 0] = float("nan")
+    rows = torch.arange(M) % 2 == 0
+    cols = (torch.arange(N) // (1 if w_rows else 128)) % 2 == 0
+    y2 = fp8.fp8_linear_block(*on(qx, qw, sx2, sw2), out_kind=fp8.OUT_F32).cpu()
+    assert torch.equal(y2[rows][:, cols], y.cpu()[rows][:, cols])
+    assert not torch.isfinite(y2[~rows]).any() and y2[:, ~cols].isnan().all()
+
+
 def test_one_nan_block_of_a_batch_leaves_the_others():
     # what fp8_quant_block makes of a NaN, through the product
     g = torch.Generator().manual_seed(1)
