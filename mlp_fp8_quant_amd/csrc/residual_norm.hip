@@ -307,38 +307,72 @@ hipError_t norm_of_types(const ResidualNormArgs& g, hipStream_t stream) {
 
 // The slabs of a launch: per_gate of them cover the rows of each gate, `rows`
 // each.  part: [slabs, 2, H up to a multiple of 4] sums over a slab, of dy n and of
-// dx z.
+// dx z.  Of many gates `together` (else 0) are walked one after another and share
+// a slab, whose second sum is then that of alpha gate dx z.
 __host__ __device__ inline int64_t part_columns(int64_t H) { return (H + 3) / 4 * 4; }
 struct Slabs {
-  int64_t per_gate, rows;
+  int64_t per_gate, rows, together, count;
   float* part;
 };
+// alpha f a: a gradient from the sum a of dx z.
+__device__ __forceinline__ void scaled8(float alpha, const float* f, const float* a, float* out) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) out[k] = __fmul_rn(__fmul_rn(alpha, f[k]), a[k]);
+}
 // A slab's column sums go to its part, or, the only slab of all (or of its gate),
 // to the results themselves.
 __device__ __forceinline__ void put_sums(const ResidualNormBwdArgs& g, const Slabs& s, int64_t slab, int64_t gate,
                                          int64_t i, const float* sw, const float* sa) {
-  const bool one = g.gates * s.per_gate == 1, wanted = g.dpost != nullptr || g.dgate != nullptr;
+  const bool one = s.count == 1, wanted = g.dpost != nullptr || g.dgate != nullptr;
   float* p = s.part + slab * 2 * part_columns(g.H);
   float f[8];
   if (g.dw != nullptr) store8_f32(one ? g.dw : p, i, g.H, sw);
   if (one && g.dpost != nullptr) {
     param8(gate_at(g.gate, g.gate_f32, gate * g.H), g.gate_f32, i, g.H, f);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = __fmul_rn(__fmul_rn(g.alpha, f[k]), sa[k]);
+    scaled8(g.alpha, f, sa, f);
     store8_f32(g.dpost, i, g.H, f);
   }
   if (s.per_gate == 1 && g.dgate != nullptr) {
     param8(g.post_w, g.w_f32, i, g.H, f);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = __fmul_rn(__fmul_rn(g.alpha, f[k]), sa[k]);
+    scaled8(g.alpha, f, sa, f);
     store8_f32(g.dgate + slab * g.H, i, g.H, f);
   }
   if (!one && wanted) store8_f32(p + part_columns(g.H), i, g.H, sa);
 }
 
+// The same where gates share a slab: what a gate's sum of dx z gives, and the
+// slab's sums.
+__device__ __forceinline__ void put_gate(const ResidualNormBwdArgs& g, int64_t gate, int64_t i, const float* gt,
+                                         const float* pw, float* sa, float* sp) {
+  float f[8];
+  scaled8(g.alpha, pw, sa, f);
+  if (g.dgate != nullptr && i < g.H) store8_f32(g.dgate + gate * g.H, i, g.H, f);
+  scaled8(g.alpha, gt, sa, f);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    sp[k] = __fadd_rn(sp[k], f[k]);
+    sa[k] = 0.0f;
+  }
+}
+__device__ __forceinline__ void put_together(const ResidualNormBwdArgs& g, const Slabs& s, int64_t slab, int64_t i,
+                                             const float* sw, const float* sp) {
+  float* p = s.part + slab * 2 * part_columns(g.H);
+  if (g.dw != nullptr) store8_f32(p, i, g.H, sw);
+  if (g.dpost != nullptr) store8_f32(p + part_columns(g.H), i, g.H, sp);
+}
+
 struct RowRange {
   int64_t gate, first, end;
 };
+// The rows of the gates from walk * together on.
+__device__ __forceinline__ RowRange rows_together(const ResidualNormBwdArgs& g, const Slabs& s, int64_t walk) {
+  const int64_t gate_rows = g.rows / g.gates;
+  RowRange r;
+  r.gate = walk * s.together;
+  r.first = r.gate * gate_rows;
+  r.end = (r.gate + s.together) * gate_rows < g.rows ? (r.gate + s.together) * gate_rows : g.rows;
+  return r;
+}
 __device__ __forceinline__ RowRange rows_of_slab(const ResidualNormBwdArgs& g, const Slabs& s, int64_t slab) {
   const int64_t gate_rows = g.rows / g.gates;
   RowRange r;
@@ -352,8 +386,9 @@ __device__ __forceinline__ RowRange rows_of_slab(const ResidualNormBwdArgs& g, c
 // side by side as the workgroup holds; or 0: the whole workgroup).  They walk
 // the rows of the workgroup's slab, which lies within one gate's rows, the next
 // row's loads on their way during this row's sums.  FULL: the threads' columns
-// are exactly the row.
-template <bool XF, bool HF, int TC, int NT, bool FULL>
+// are exactly the row.  MANY: gates share a slab, and rows side by side are those
+// of different gates, each T threads walking `together` gates of their own.
+template <bool XF, bool HF, int TC, int NT, bool FULL, bool MANY>
 __global__ __launch_bounds__(NT) void residual_norm_backward_kernel(ResidualNormBwdArgs g, Slabs sl) {
   __shared__ float red[32];
   __shared__ f4 cols[TC > 0 ? 4 * NT / 2 : 1];
@@ -366,6 +401,7 @@ __global__ __launch_bounds__(NT) void residual_norm_backward_kernel(ResidualNorm
   RowSums<TC> total(red);
   Raw8<HF> ndy, nz;
   Raw8<XF> nr, nd;
+  Raw8<true> ng;   // the next gate, as it is stored
   float nrs = 0.0f, npost = 1.0f;
   auto load8_of = [&](auto& to, const void* p, int64_t r) {
     constexpr bool F = sizeof(to) == 32;
@@ -380,14 +416,40 @@ __global__ __launch_bounds__(NT) void residual_norm_backward_kernel(ResidualNorm
     nrs = g.rstd[r];
     if (post) npost = g.post_rstd[r];
   };
-  for (int64_t slab = blockIdx.x; slab < sl.per_gate * g.gates; slab += gridDim.x) {
-  const RowRange rr = rows_of_slab(g, sl, slab);
-  int64_t r = rr.first + q;
+  auto load_gate = [&](int64_t gate) {
+    const void* p = gate_at(g.gate, g.gate_f32, gate * g.H);
+    if (g.gate_f32) ng = TC == 16 || FULL ? load8<true, FULL>(p, i, g.H) : load8_ahead<true>(p, i, g.H);
+    else ng.q[0] = (TC == 16 || FULL ? load8<false, FULL>(p, i, g.H) : load8_ahead<false>(p, i, g.H)).q[0];
+  };
+  auto gate_values = [&](float* f) {
+    if (g.gate_f32) {
+      if (TC != 16 && !FULL) shift8<true>(ng, i, g.H);
+      values8<true>(ng, f);
+    } else {
+      Raw8<false> b = {ng.q[0]};
+      if (TC != 16 && !FULL) shift8<false>(b, i, g.H);
+      values8<false>(b, f);
+    }
+  };
+  const int64_t gate_rows = MANY ? g.rows / g.gates : 0;
+  constexpr bool kSide = !MANY;   // the rows side by side are one gate's
+  const int step = kSide ? G : 1;
+  for (int64_t slab = blockIdx.x; slab < sl.count; slab += gridDim.x) {
+  const RowRange rr = MANY ? rows_together(g, sl, slab * G + q) : rows_of_slab(g, sl, slab);
+  int64_t r = kSide ? rr.first + q : rr.first, gate = rr.gate, gate_end = rr.first + gate_rows;
   if (r < rr.end) load(r);
-  float w[8], f[8], sw[8] = {}, sa[8] = {};
+  float w[8], f[8], pw[8], sw[8] = {}, sa[8] = {}, sp[8] = {};   // f: alpha gate pw, or the gate alone
   param8(g.w, g.w_f32, i, g.H, w);
-  factor8(g, rr.gate, i, f);
-  for (; r < rr.end; r += G) {
+  if constexpr (MANY) {
+    param8(g.post_w, g.w_f32, i, g.H, pw);
+    if (r < rr.end) {
+      load_gate(gate);
+      gate_values(f);
+    }
+  } else {
+    factor8(g, rr.gate, i, f);
+  }
+  for (; r < rr.end; r += step) {
     float dy[8], n[8], z[8], d[8], e[8];
     if constexpr (TC != 16 && !FULL) {
       shift8<HF>(ndy, i, g.H);
@@ -400,7 +462,9 @@ __global__ __launch_bounds__(NT) void residual_norm_backward_kernel(ResidualNorm
     if (has_h) values8<HF>(nz, z);
     if (has_dr) values8<XF>(nd, d);
     const float rs = nrs, post_rs = npost;
-    if (r + G < rr.end) load(r + G);
+    if (r + step < rr.end) load(r + step);
+    const bool last = MANY && r + 1 == gate_end;
+    if (last && r + 1 < rr.end) load_gate(gate + 1);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       n[k] = __fmul_rn(n[k], rs);
@@ -420,7 +484,7 @@ __global__ __launch_bounds__(NT) void residual_norm_backward_kernel(ResidualNorm
       for (int k = 0; k < 8; ++k) {
         if (post) z[k] = __fmul_rn(z[k], post_rs);
         sa[k] = __builtin_fmaf(n[k], z[k], sa[k]);
-        n[k] = __fmul_rn(n[k], f[k]);   // p
+        n[k] = __fmul_rn(n[k], MANY ? __fmul_rn(__fmul_rn(g.alpha, f[k]), pw[k]) : f[k]);   // p
         e[k] = __fmul_rn(n[k], z[k]);
       }
       if (post) {
@@ -430,6 +494,16 @@ __global__ __launch_bounds__(NT) void residual_norm_backward_kernel(ResidualNorm
       }
       if (FULL || i < g.H) store8<HF>(g.dh, r * g.H, i, g.H, n);
     }
+    if (last) {
+      put_gate(g, gate, i, f, pw, sa, sp);
+      if (r + 1 < rr.end) gate_values(f);
+      ++gate;
+      gate_end += gate_rows;
+    }
+  }
+  if constexpr (MANY) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sa[k] = sp[k];
   }
   if constexpr (TC > 0) {
     // the rows side by side (a power of two) are added in a tree
@@ -452,7 +526,10 @@ __global__ __launch_bounds__(NT) void residual_norm_backward_kernel(ResidualNorm
       __syncthreads();
     }
   }
-  if (q == 0 && i < g.H) put_sums(g, sl, slab, rr.gate, i, sw, sa);
+  if (q == 0 && i < g.H) {
+    if constexpr (MANY) put_together(g, sl, slab, i, sw, sa);
+    else put_sums(g, sl, slab, rr.gate, i, sw, sa);
+  }
   }
 }
 
@@ -513,14 +590,16 @@ __global__ __launch_bounds__(1024) void residual_norm_row_long_kernel(ResidualNo
   }
 }
 
-template <bool XF, bool HF>
+template <bool XF, bool HF, bool MANY>
 __global__ __launch_bounds__(256) void residual_norm_columns_long_kernel(ResidualNormBwdArgs g, Slabs sl,
                                                                          const float* __restrict__ c) {
   const int64_t i = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
   if (i >= g.H) return;
-  for (int64_t slab = blockIdx.y; slab < sl.per_gate * g.gates; slab += gridDim.y) {
-    const RowRange rr = rows_of_slab(g, sl, slab);
-    float sw[8] = {}, sa[8] = {};
+  const int64_t gate_rows = g.rows / g.gates;
+  for (int64_t slab = blockIdx.y; slab < sl.count; slab += gridDim.y) {
+    const RowRange rr = MANY ? rows_together(g, sl, slab) : rows_of_slab(g, sl, slab);
+    int64_t gate = rr.gate, gate_end = rr.first + gate_rows;
+    float sw[8] = {}, sa[8] = {}, sp[8] = {};
     for (int64_t r = rr.first; r < rr.end; ++r) {
       const LongRow a = long_row(g, c, r);
       float dy[8], n[8], gw[8], dx[8], z[8] = {};
@@ -531,8 +610,16 @@ __global__ __launch_bounds__(256) void residual_norm_columns_long_kernel(Residua
         sw[k] = __builtin_fmaf(dy[k], n[k], sw[k]);
         sa[k] = __builtin_fmaf(dx[k], z[k], sa[k]);
       }
+      if (MANY && r + 1 == gate_end) {
+        float gt[8], pw[8];
+        param8(gate_at(g.gate, g.gate_f32, gate * g.H), g.gate_f32, i, g.H, gt);
+        param8(g.post_w, g.w_f32, i, g.H, pw);
+        put_gate(g, gate++, i, gt, pw, sa, sp);
+        gate_end += gate_rows;
+      }
     }
-    put_sums(g, sl, slab, rr.gate, i, sw, sa);
+    if constexpr (MANY) put_together(g, sl, slab, i, sw, sp);
+    else put_sums(g, sl, slab, rr.gate, i, sw, sa);
   }
 }
 
@@ -589,9 +676,9 @@ __device__ __forceinline__ void gate4(const ResidualNormBwdArgs& g, int64_t gate
 
 // The results from part, in an order that depends on the sizes alone: y = 0
 // dweight, sums over all slabs; 1 dpost_weight, sums over all slabs of the second
-// plane times the slab's gate (a single one at the end); 2 + a (with each_gate) dgate a, its slabs' sums.  A
-// workgroup takes 4 Q columns, four per thread, and L threads share a column's
-// slabs.
+// plane times the slab's gate (a single one at the end; sums of gates together
+// hold it); 2 + a (with each_gate) dgate a, its slabs' sums.  A workgroup takes
+// 4 Q columns, four per thread, and L threads share a column's slabs.
 template <int Q>
 __global__ __launch_bounds__(256) void residual_norm_sums_kernel(ResidualNormBwdArgs g, Slabs sl, int each_gate) {
   constexpr int L = 256 / Q, C = 4 * Q, P = 256 / C, R = 4;
@@ -602,10 +689,10 @@ __global__ __launch_bounds__(256) void residual_norm_sums_kernel(ResidualNormBwd
   for (int64_t y = blockIdx.y; y < 2 + (each_gate ? g.gates : 0); y += gridDim.y, __syncthreads()) {
     float* out = y == 0 ? g.dw : y == 1 ? g.dpost : (g.dgate == nullptr ? nullptr : g.dgate + (y - 2) * g.H);
     if (out == nullptr) continue;
-    const int64_t first = y < 2 ? 0 : (y - 2) * per_gate, count = (y < 2 ? g.gates : 1) * per_gate;
+    const int64_t first = y < 2 ? 0 : (y - 2) * per_gate, count = y < 2 ? sl.count : per_gate;
     const int64_t Hs = part_columns(g.H);
     const float* v = sl.part + (first * 2 + (y > 0)) * Hs;
-    const bool by_gate = y == 1 && g.gate != nullptr && g.gates > 1;
+    const bool by_gate = y == 1 && g.gate != nullptr && g.gates > 1 && !sl.together;
     auto gate_of = [&](int64_t p) { return (int64_t)((uint32_t)p / (uint32_t)per_gate); };
     float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     // (columns past the row's end are read up to its padding, and not used)
@@ -647,7 +734,7 @@ __global__ __launch_bounds__(256) void residual_norm_sums_kernel(ResidualNormBwd
       float u = red2[0][threadIdx.x];
 #pragma unroll
       for (int h = 1; h < P; ++h) u = __fadd_rn(u, red2[h][threadIdx.x]);
-      if (y > 0) u = __fmul_rn(u, g.alpha);
+      if (y > 0 && !sl.together) u = __fmul_rn(u, g.alpha);
       if (y == 1 && g.gate != nullptr && g.gates == 1) u = __fmul_rn(u, param1(g.gate, g.gate_f32, c));
       if (y > 1 && g.post_w != nullptr) u = __fmul_rn(u, param1(g.post_w, g.w_f32, c));
       out[c] = u;
@@ -664,14 +751,17 @@ constexpr int64_t kBwdRegs = 1024 * 8;
 // 12000x1027 60 with 512, 55 with 768), of at least one, two or four rows one after
 // another by the number of rows, since every slab's sums are written and read once
 // more (256x4096 16.9 with four, 15.0 with two).  A few rows are one slab, whose
-// sums need no second launch.
+// sums need no second launch.  Of twice as many gates as there would be slabs
+// (times the rows side by side), some share one:
+// a gate for each row of 16384x5120 313 us (1018 with a slab each), of 200000x128
+// 106 (6541).
 struct BwdShape {
   int threads, side;
-  int64_t per_gate;
+  int64_t per_gate, together, count;
 };
 BwdShape bwd_shape(int64_t rows, int64_t H, int64_t gates) {
   const int64_t units = (H + 7) / 8, gate_rows = rows / gates;
-  BwdShape b{0, 1, 0};
+  BwdShape b{0, 1, 1, 0, 0};
   int64_t slabs;
   if (H > kBwdRegs) {
     b.threads = 1024;
@@ -686,20 +776,29 @@ BwdShape bwd_shape(int64_t rows, int64_t H, int64_t gates) {
   }
   if (H <= kBwdRegs) slabs = b.threads >= 512 ? 256 : b.threads >= 256 ? 512 : 768;
   if (rows <= (H <= 4096 ? 4 : 2) * b.side && gates == 1) slabs = 1;
+  if (slabs > 1 && gates >= 2 * slabs * b.side) {
+    b.together = (gates + slabs * b.side - 1) / (slabs * b.side);
+    const int64_t walks = (gates + b.together - 1) / b.together;
+    b.count = (walks + b.side - 1) / b.side;
+    return b;
+  }
   b.per_gate = (slabs + gates - 1) / gates;
   const int64_t walk = H > kBwdRegs ? 4 : b.side > 1 || rows <= 64 ? 1 : rows <= 256 ? 2 : 4;
   const int64_t most = (gate_rows + walk * b.side - 1) / (walk * b.side);
   if (b.per_gate > most) b.per_gate = most;
+  b.count = gates * b.per_gate;
   return b;
 }
 
 template <bool XF, bool HF, int TC, int NT>
 hipError_t run_backward_kernel(const ResidualNormBwdArgs& g, const BwdShape& b, const Slabs& sl, hipStream_t stream) {
-  const dim3 grid(row_grid(g.gates * b.per_gate, 1 << 20)), block(b.threads);
-  if (TC == 0 && g.H == (int64_t)b.threads * 8)
-    hipLaunchKernelGGL((residual_norm_backward_kernel<XF, HF, TC, NT, TC == 0>), grid, block, 0, stream, g, sl);
+  const dim3 grid(row_grid(b.count, 1 << 20)), block(b.threads);
+  if (b.together)
+    hipLaunchKernelGGL((residual_norm_backward_kernel<XF, HF, TC, NT, false, true>), grid, block, 0, stream, g, sl);
+  else if (TC == 0 && g.H == (int64_t)b.threads * 8)
+    hipLaunchKernelGGL((residual_norm_backward_kernel<XF, HF, TC, NT, TC == 0, false>), grid, block, 0, stream, g, sl);
   else
-    hipLaunchKernelGGL((residual_norm_backward_kernel<XF, HF, TC, NT, false>), grid, block, 0, stream, g, sl);
+    hipLaunchKernelGGL((residual_norm_backward_kernel<XF, HF, TC, NT, false, false>), grid, block, 0, stream, g, sl);
   return hipGetLastError();
 }
 
@@ -713,10 +812,13 @@ hipError_t run_backward(const ResidualNormBwdArgs& g, const BwdShape& b, const S
   if (g.H <= kBwdRegs) return run_backward_kernel<XF, HF, 0, 1024>(g, b, sl, stream);
   const unsigned rows = row_grid(g.rows, 1 << 20);
   hipLaunchKernelGGL((residual_norm_row_long_kernel<XF, HF>), dim3(rows), dim3(1024), 0, stream, g, c);
-  if (g.dw != nullptr || g.dgate != nullptr || g.dpost != nullptr)
-    hipLaunchKernelGGL((residual_norm_columns_long_kernel<XF, HF>),
-                       dim3((unsigned)((g.H + 2047) / 2048), row_grid(g.gates * b.per_gate, 65535)), dim3(256), 0,
-                       stream, g, sl, c);
+  if (g.dw != nullptr || g.dgate != nullptr || g.dpost != nullptr) {
+    const dim3 grid((unsigned)((g.H + 2047) / 2048), row_grid(b.count, 65535));
+    if (b.together)
+      hipLaunchKernelGGL((residual_norm_columns_long_kernel<XF, HF, true>), grid, dim3(256), 0, stream, g, sl, c);
+    else
+      hipLaunchKernelGGL((residual_norm_columns_long_kernel<XF, HF, false>), grid, dim3(256), 0, stream, g, sl, c);
+  }
   hipLaunchKernelGGL((residual_norm_dx_long_kernel<XF, HF>), dim3(rows), dim3(1024), 0, stream, g, c);
   return hipGetLastError();
 }
@@ -730,17 +832,19 @@ hipError_t launch_residual_norm(const ResidualNormArgs& g, hipStream_t stream) {
 
 int64_t residual_norm_backward_floats(int64_t rows, int64_t H, int64_t gates) {
   if (rows == 0 || H == 0) return 0;
-  const int64_t slabs = gates * bwd_shape(rows, H, gates).per_gate;
+  const int64_t slabs = bwd_shape(rows, H, gates).count;
   return (slabs > 1 ? slabs * 2 * part_columns(H) : 0) + (H > kBwdRegs ? rows : 0);
 }
 
 hipError_t launch_residual_norm_backward(const ResidualNormBwdArgs& g, float* ws, hipStream_t stream) {
-  Slabs sl{0, 0, ws};   // no rows: sums of no slabs
+  Slabs sl{0, 0, 0, 0, ws};   // no rows: sums of no slabs
   bool each_gate = true;
   if (g.rows > 0) {
     const BwdShape b = bwd_shape(g.rows, g.H, g.gates);
-    const int64_t slabs = g.gates * b.per_gate, gate_rows = g.rows / g.gates;
+    const int64_t slabs = b.count, gate_rows = g.rows / g.gates;
     sl.per_gate = b.per_gate;
+    sl.together = b.together;
+    sl.count = slabs;
     sl.rows = (gate_rows + b.per_gate - 1) / b.per_gate;
     float* c = ws + (slabs > 1 ? slabs * 2 * part_columns(g.H) : 0);
     hipError_t e;

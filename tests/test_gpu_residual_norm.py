@@ -100,6 +100,16 @@ def test_a_gate_for_each_few_rows(gates, H):
     check_backward(t, 1.0)
 
 
+@pytest.mark.parametrize("gates,per,H", [(16390, 1, 33), (16384, 3, 128), (4100, 2, 500), (1540, 3, 600), (1700, 1, 1027),
+                                         (520, 2, 4096), (515, 1, 5123), (700, 1, 7000), (513, 2, 8200), (41, 1, 200001)])
+@pytest.mark.parametrize("xt,wt,post", [(BF16, BF16, True), (F32, F32, False)])
+def test_many_gates(gates, per, H, xt, wt, post):
+    # gates share a workgroup's sums
+    t = inputs(gates * per, H, xt, BF16, wt, gates, post, H)
+    check_forward(t, 0.5)
+    check_backward(t, 0.5, dr=post)
+
+
 @pytest.mark.parametrize("H", [7, 128, 1030, 9000])
 @pytest.mark.parametrize("xt", [BF16, F32])
 def test_without_hidden(xt, H):
