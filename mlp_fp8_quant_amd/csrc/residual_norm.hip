@@ -678,7 +678,9 @@ __device__ __forceinline__ void gate4(const ResidualNormBwdArgs& g, int64_t gate
 // dweight, sums over all slabs; 1 dpost_weight, sums over all slabs of the second
 // plane times the slab's gate (a single one at the end; sums of gates together
 // hold it); 2 + a (with each_gate) dgate a, its slabs' sums.  A workgroup takes
-// 4 Q columns, four per thread, and L threads share a column's slabs.
+// 4 Q columns, four per thread, and L threads share a column's slabs, each a run of
+// them (strided, they would take a gate anew for each slab: 16384x5120 with 8 gates
+// 13.4 us, so 5.9).
 template <int Q>
 __global__ __launch_bounds__(256) void residual_norm_sums_kernel(ResidualNormBwdArgs g, Slabs sl, int each_gate) {
   constexpr int L = 256 / Q, C = 4 * Q, P = 256 / C, R = 4;
@@ -693,33 +695,41 @@ __global__ __launch_bounds__(256) void residual_norm_sums_kernel(ResidualNormBwd
     const int64_t Hs = part_columns(g.H);
     const float* v = sl.part + (first * 2 + (y > 0)) * Hs;
     const bool by_gate = y == 1 && g.gate != nullptr && g.gates > 1 && !sl.together;
-    auto gate_of = [&](int64_t p) { return (int64_t)((uint32_t)p / (uint32_t)per_gate); };
     float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     // (columns past the row's end are read up to its padding, and not used)
-    auto four = [&](const float* row, float* x) {
-      const f4 w = n < Hs ? *reinterpret_cast<const f4*>(row + n) : (f4){0.0f, 0.0f, 0.0f, 0.0f};
+    auto add = [&](int64_t p, int64_t end, float* u) {
+      auto four = [&](int64_t p) {
+        return n < Hs ? *reinterpret_cast<const f4*>(v + p * 2 * Hs + n) : (f4){0.0f, 0.0f, 0.0f, 0.0f};
+      };
+      for (; p + R <= end; p += R) {
+        f4 x[R];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] = w[k];
-    };
-    int64_t p = s;
-    for (; p + L * (R - 1) < count; p += L * R) {
-      float x[R][4], f[R][4];
+        for (int r = 0; r < R; ++r) x[r] = four(p + r);
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        four(v + (p + L * r) * 2 * Hs, x[r]);
-        if (by_gate) gate4(g, gate_of(p + L * r), n, f[r]);
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) u[k] = __fadd_rn(u[k], x[r][k]);
       }
+      for (; p < end; ++p) {
+        const f4 x = four(p);
 #pragma unroll
-      for (int r = 0; r < R; ++r)
+        for (int k = 0; k < 4; ++k) u[k] = __fadd_rn(u[k], x[k]);
+      }
+    };
+    const int64_t share = (count + L - 1) / L, end = (s + 1) * share < count ? (s + 1) * share : count;
+    if (by_gate) {
+      int64_t p = s * share, gate = p < end ? (uint32_t)p / (uint32_t)per_gate : 0;
+      for (; p < end; ++gate) {
+        const int64_t to = (gate + 1) * per_gate < end ? (gate + 1) * per_gate : end;
+        float u[4] = {0.0f, 0.0f, 0.0f, 0.0f}, f[4];
+        gate4(g, gate, n, f);
+        add(p, to, u);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) t[k] = by_gate ? __builtin_fmaf(x[r][k], f[r][k], t[k]) : __fadd_rn(t[k], x[r][k]);
-    }
-    for (; p < count; p += L) {
-      float x[4], f[4];
-      four(v + p * 2 * Hs, x);
-      if (by_gate) gate4(g, gate_of(p), n, f);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) t[k] = by_gate ? __builtin_fmaf(x[k], f[k], t[k]) : __fadd_rn(t[k], x[k]);
+        for (int k = 0; k < 4; ++k) t[k] = __builtin_fmaf(u[k], f[k], t[k]);
+        p = to;
+      }
+    } else {
+      add(s * share, end, t);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) red[s][4 * q + k] = t[k];
