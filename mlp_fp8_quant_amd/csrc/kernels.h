@@ -134,7 +134,7 @@ enum LinearTile {
   // few outputs: blocks of 16 rows of X by blocks of 16 rows of W (Pair: two
   // workgroups per CU)
   kRows1x1, kRows1x2, kRows1x4, kRows2x1, kRows2x2, kRows2x4, kRows4x2, kRows4x4, kRows4x6, kRows4x4Pair,
-  kTile256x256, kTile256x128, kTile128x128, kTile128x128K2
+  kTile256x256, kTile256x128, kTile128x128, kTile128x128K2, kTile128x64K2, kTile128x64
 };
 struct LinearPlan {
   int tile;      // LinearTile

@@ -243,35 +243,51 @@ hipError_t launch_rows(const LinearActArgs& g, hipStream_t stream) {
 }
 
 // How a shape runs (MI355X, 256 CUs; us measured).  Few outputs: the smallest
-// tile of 16 x 16 blocks whose grid gives no CU more than one workgroup, and up
-// to two of 64 x 64, as in fp8_linear_act's rule: 1x4096x4096 5.3 with one block
-// (with two 5.6), 64x4096x4096 7.6 with 32x32 (64x32 10.1, 32x16 10.6),
-// 128x12288x4096 25.1 with 64x64 in pairs (alone 29.8), 512x4096x12288 69 (128x128
-// with two K groups 67, 128x128 84).
+// tile whose grid gives no CU more than one workgroup: 1x4096x4096 5.3 with one block (with two 5.6), 64x4096x4096
+// 7.6 with 32x32 (64x32 10.1, 32x16 10.6), 256x4096x4096 15.6 with 64x64 (128x64 18.0), 86x5351x1520 8.6 with 64x64 (64x32, two
+// to some CUs, 11.3);
+// and up to 64 rows 64x64 in pairs: 40x20000x4096 24.7 (128x64 35.8).
 //
-// More outputs: the cheapest of three tiles by an estimate of rounds of workgroups
-// times (rate * K + what a tile costs besides): 256x128 4096x12288x4096 347 (128x128
-// 357, two K groups 402), 128x128 two to a CU 5000x5000x4096 198 (213, 228) and
-// 3000x3000x512 21 (26, 30), 128x128 with two K groups 2048x2048x8192 62 (82, 66).
+// More outputs: the least of the estimates below, rounds of workgroups times (rate
+// * K + what a tile costs besides), the rate less where a round leaves CUs idle.
+// Two K groups: 128x64 512x4096x12288 56 (128x128 67, 64x64 in pairs 77, 256x128
+// 120) and 1024x2048x2048 12.7 (18.8, 15.8, 26), 128x128 2048x2048x8192 64 (128x64
+// 75, without groups 68, 256x128 84).  Without: 128x64, three to a CU, 300x16384x2048
+// 28.9 (128x128 32.0, with groups 36.8), 128x128, two, 5000x5000x4096 205 (128x64 218,
+// 256x128 220), 256x128 4096x12288x4096 347 (128x128 357).
 int linear_block_plan(int64_t M, int64_t N, int64_t K) {
   constexpr int64_t kCus = 256;
   auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-  const int64_t area = up(up(M, 16) * up(N, 16), kCus);   // blocks per CU
-  if (M <= 16) return area <= 1 ? kRows1x1 : area <= 2 ? kRows1x2 : kRows1x4;
-  if (area <= 2) return kRows2x1;
-  if (area <= 4) return kRows2x2;
+  auto one_each = [&](int64_t bm, int64_t bn) { return up(M, bm) * up(N, bn) <= kCus; };   // at most a tile per CU
+  if (M <= 16) return one_each(16, 16) ? kRows1x1 : one_each(16, 32) ? kRows1x2 : kRows1x4;
+  if (one_each(32, 16)) return kRows2x1;
+  if (one_each(32, 32)) return kRows2x2;
   if (M <= 32) return kRows2x4;
-  if (area <= 8) return kRows4x2;
-  if (area <= 16) return kRows4x4;
-  if (M <= 64 || area <= 32) return kRows4x4Pair;
-  const int64_t small = up(M, 128) * up(N, 128), large = up(M, 256) * up(N, 128);
-  const double k = (double)K, pairs = (double)small / (2 * kCus);
-  const double t256 = (double)up(large, kCus) * (0.0118 * k + 9.0);
-  const double t128 = pairs <= 0.5 ? 0.0072 * k + 7.0
-                                   : (pairs <= 1.0 ? 1.0 : 0.5 * (pairs + (double)up(small, 2 * kCus))) * (0.0128 * k + 7.0);
-  const double tk2 = (double)up(small, kCus) * (0.00667 * k + 7.6);
-  if (t256 <= t128 && t256 <= tk2) return kTile256x128;
-  return t128 <= tk2 ? kTile128x128 : kTile128x128K2;
+  if (one_each(64, 32)) return kRows4x2;
+  if (one_each(64, 64)) return kRows4x4;
+  if (M <= 64) return kRows4x4Pair;
+  const double k = (double)K;
+  int best = kRows4x4Pair;
+  double least = (double)up(up(M, 64) * up(N, 64), 2 * kCus) * (0.0056 * k + 4.6);
+  auto offer = [&](int tile, double t) {
+    if (t < least) {
+      best = tile;
+      least = t;
+    }
+  };
+  const int64_t narrow = up(M, 128) * up(N, 64), square = up(M, 128) * up(N, 128), large = up(M, 256) * up(N, 128);
+  const double narrows = (double)narrow / kCus, pairs = (double)square / (2 * kCus);   // for each CU; pair of places
+  auto fill = [&](int64_t tiles) { return tiles < kCus ? (double)tiles / kCus : 1.0; };
+  offer(kTile128x64K2, (double)up(narrow, kCus) * ((0.0030 + 0.0012 * fill(narrow)) * k + 4.8));
+  offer(kTile128x64, narrows <= 1.0   ? 0.0051 * k + 4.0
+                     : narrows <= 2.0 ? (0.5 + 0.25 * narrows) * (0.0082 * k + 5.0)
+                                      : narrows * (0.0044 * k + 0.9) + 3.0);
+  offer(kTile128x128K2, (double)up(square, kCus) * ((0.0035 + 0.0032 * fill(square)) * k + 8.0));
+  offer(kTile128x128, pairs <= 0.5 ? 0.0072 * k + 7.0
+                                   : (pairs <= 1.0 ? 1.0 : 0.5 * (pairs + (double)up(square, 2 * kCus))) *
+                                         (0.0128 * k + 7.0));
+  offer(kTile256x128, (double)up(large, kCus) * (0.0118 * k + 9.0));
+  return best;
 }
 
 }  // namespace

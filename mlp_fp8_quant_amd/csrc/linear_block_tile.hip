@@ -2,7 +2,7 @@
 // fp8_linear_act's epilogue: the kernel behind fp8_linear_block for all but few
 // rows.
 //
-// A workgroup of WM x WN waves, 64 x 64 outputs each, computes a BM x BN tile
+// A workgroup of WM x WN waves, 64 x 32 FN outputs each, computes a BM x BN tile
 // from 128-K stages that the buffer unit copies straight into LDS, as in
 // linear_act_tile.hip.  A stage is one block: its products are summed from zero
 // in accumulators of their own (64 registers beside the 64 of the sums, which is
@@ -17,10 +17,19 @@
 // before the next batch is on its way into the other of two slots: those of X as
 // 16 bytes per row, W's as 16 bytes for the tile's 128 columns or, per row, four
 // bytes per lane and stage (column-major, for 16-byte reads).
+//
+// Many rows are bound by what issues beside the MFMAs and by power: at
+// 16384x25600x5120 (3475 to 3640 us, 1.18 to 1.24 PFLOP/s) the matrix cores work in
+// 62% of the cycles at 1.64 GHz, and decodes, FMAs and addresses issue in 53%.
+// Copies of the kernel that leave out a part (and so err) run 8% faster without the
+// block sums' FMAs, 7% with one decode for all fragments, 11% without the stages'
+// copies, 3% without the barrier, 0% without the wait for the copies.  A wave's
+// part of 64 x 32 decodes half as much again for each MFMA, but two K groups of
+// four such waves fill a CU's places where there are few tiles: 512x4096x12288 56
+// us against 67 with parts of 64 x 64, 0.92 PFLOP/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <atomic>
 #include <type_traits>
 #include <utility>
 
@@ -61,23 +70,24 @@ struct BlockTileArgs {
   int tiles_m, tiles_n;
 };
 
-// WROWS: W has a scale for each row.  KFULL: K is a multiple of the stage.
+// WROWS: W has a scale for each row.  KFULL: K is a multiple of the stage.  FN:
+// blocks of 32 columns of a wave's part.
 // KSPL = 2: two groups of WM x WN waves share the tile, taking the even and the
 // odd stages, and their sums are added (even + odd) through LDS; KSPL = 1 and
 // PERSIST: workgroups walk tiles blockIdx.x, + gridDim.x, .. with the next tile's
 // first stages copied in before this tile's epilogue, whose LDS is then apart
 // from the stages.
-template <int WM, int WN, int KSPL, bool PERSIST, bool WROWS, bool KFULL>
+template <int WM, int WN, int FN, int KSPL, bool PERSIST, bool WROWS, bool KFULL>
 __global__ __launch_bounds__(WM* WN * 64 * KSPL, 2) void linear_block_tile_kernel(BlockTileArgs t) {
   const int M = (int)t.a.M, N = (int)t.a.N, K = (int)t.a.K;
-  constexpr int BM = 64 * WM, BN = 64 * WN, NW = WM * WN, FM = 2, FN = 2;
-  static_assert(BN == 128, "one column of W's scale tiles");
+  constexpr int BM = 64 * WM, BN = 32 * FN * WN, NW = WM * WN, FM = 2;
+  static_assert(128 % BN == 0, "one column of W's scale tiles");
   static_assert(!PERSIST || KSPL == 1, "");
   constexpr int A_STAGE = BM * KS, B_STAGE = BN * KS, STAGE = A_STAGE + B_STAGE;
   constexpr int EPI = 4096;   // epilogue bytes per wave
   constexpr int A_LPW = BM / RPI / NW, B_LPW = BN / RPI / NW, LPW = A_LPW + B_LPW;   // copies of a wave
   static_assert(LPW * NW * RPI == BM + BN, "tile rows / waves");
-  constexpr int XS = BM * 16, WS = WROWS ? BN * 16 : 1024, SLOT = XS + WS;   // scales of a batch
+  constexpr int XS = BM * 16, WS = WROWS ? BN * 16 : 256, SLOT = XS + WS;   // scales of a batch
   constexpr int CODES = KSPL * NB * STAGE, LDS = CODES + 2 * SLOT + (PERSIST ? NW * EPI : 0);
   static_assert(LDS <= 160 * 1024, "stages, scales and epilogue fit the 160 KB LDS of a CU");
   static_assert(PERSIST || NW * EPI <= NB * STAGE, "the epilogue fits the stage buffers");
@@ -149,7 +159,7 @@ __global__ __launch_bounds__(WM* WN * 64 * KSPL, 2) void linear_block_tile_kerne
   // copy, and W's.  A row's 16 bytes may run into the next row's, which no stage
   // reads; rows past M or N lie past the window.
   constexpr int X_COPIES = BM / 64, W_COPIES = WROWS ? kBatch * BN / 64 : 1, WAVES = NW * KSPL;
-  static_assert(X_COPIES + 1 <= WAVES && W_COPIES % WAVES <= 1, "a wave's copies");
+  static_assert(X_COPIES + 1 <= WAVES && (W_COPIES < WAVES || W_COPIES % WAVES == 0), "a wave's copies");
   auto issue_scales = [&](const Windows& w, int h) {
     int ln = lane0;
     if constexpr (PERSIST) asm volatile("" : "+v"(ln));
@@ -160,14 +170,14 @@ __global__ __launch_bounds__(WM* WN * 64 * KSPL, 2) void linear_block_tile_kerne
     if constexpr (WROWS) {
       if (x) copy_to_lds(w.xs, dst + wave_id * 1024, (wave_id * 64 + ln) * stages * 4, h * 16);
 #pragma unroll
-      for (int c = 0; c < W_COPIES / WAVES; ++c) {
+      for (int c = 0; c < (W_COPIES + WAVES - 1) / WAVES; ++c) {
         const int d = c * WAVES + wave_id, s = d / (BN / 64), r = d % (BN / 64);
-        copy4_to_lds(w.ws, dst + XS + d * 256, h * kBatch + s < stages ? (r * 64 + ln) * stages * 4 : kOOB,
+        if (W_COPIES >= WAVES || d < W_COPIES) copy4_to_lds(w.ws, dst + XS + d * 256, h * kBatch + s < stages ? (r * 64 + ln) * stages * 4 : kOOB,
                      h * 16 + s * 4);
       }
     } else {
-      copy_to_lds(x ? w.xs : w.ws, dst + (x ? wave_id * 1024 : XS), x ? (wave_id * 64 + ln) * stages * 4 : ln == 0 ? 0 : kOOB,
-                  h * 16);
+      if (x) copy_to_lds(w.xs, dst + wave_id * 1024, (wave_id * 64 + ln) * stages * 4, h * 16);
+      else copy4_to_lds(w.ws, dst + XS, ln < kBatch ? ln * 4 : kOOB, h * 16);
     }
   };
 
@@ -198,7 +208,7 @@ __global__ __launch_bounds__(WM* WN * 64 * KSPL, 2) void linear_block_tile_kerne
   const int half = lane >> 5;
   {
     const int l31 = lane & 31;
-    const int ra = wm * 64 + l31, rb = wn * 64 + l31;
+    const int ra = wm * 64 + l31, rb = wn * (32 * FN) + l31;
 #pragma unroll
     for (int k = 0; k < NSTEP; ++k) {
       lds_a[k] = (int)(a_buf(0) - smem) + ra * KS + (swz(ra, 2 * k + half) << 4);
@@ -209,7 +219,7 @@ __global__ __launch_bounds__(WM* WN * 64 * KSPL, 2) void linear_block_tile_kerne
   // scales of the last finished block: X's two rows, W's tile or (WROWS) where
   // its columns' lie
   const int xs_at = CODES + (wm * 64 + (lane & 31)) * 16;
-  const int ws_at = CODES + XS + (WROWS ? (wn * 64 + 4 * half) * 4 : 0);
+  const int ws_at = CODES + XS + (WROWS ? (wn * (32 * FN) + 4 * half) * 4 : 0);
   float sx[FM] = {0.0f, 0.0f}, sw = 0.0f;
   int sw_at = ws_at + SLOT;   // zeros at first, for the sums of no block (a scale there could be infinite)
   if (WROWS && tid < BN / 4) *reinterpret_cast<v4f*>(smem + CODES + SLOT + XS + 16 * tid) = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
@@ -421,7 +431,7 @@ __global__ __launch_bounds__(WM* WN * 64 * KSPL, 2) void linear_block_tile_kerne
   float* const put = epi + (el & 31) * 32;
   const int turn = el & 7, up = el >> 5;
   const float* const get = epi + er * 32 + 4 * ((el & 7) ^ er);
-  const int row_w = wm * 64 + er, nw = n0 + wn * 64 + ec;   // row from m0
+  const int row_w = wm * 64 + er, nw = n0 + wn * (32 * FN) + ec;   // row from m0
   auto blocks_loop = [&](auto vec) {
     constexpr bool VEC = decltype(vec)::value;
     const linear::Epilogue e = linear::open_outputs(g, m0);
@@ -468,14 +478,14 @@ __global__ __launch_bounds__(WM* WN * 64 * KSPL, 2) void linear_block_tile_kerne
   }  // tiles
 }
 
-template <int WM, int WN, int KSPL, bool PERSIST, bool WROWS, bool KFULL>
+template <int WM, int WN, int FN, int KSPL, bool PERSIST, bool WROWS, bool KFULL>
 hipError_t launch_kernel(const LinearActArgs& a, int num_cus, hipStream_t stream) {
   BlockTileArgs t{};
   t.a = a;
   t.a.row_scales = 0;   // the epilogue's sums are scaled already
   t.tiles_m = (int)((a.M + 64 * WM - 1) / (64 * WM));
-  t.tiles_n = (int)((a.N + 64 * WN - 1) / (64 * WN));
-  auto kern = linear_block_tile_kernel<WM, WN, KSPL, PERSIST, WROWS, KFULL>;
+  t.tiles_n = (int)((a.N + 32 * FN * WN - 1) / (32 * FN * WN));
+  auto kern = linear_block_tile_kernel<WM, WN, FN, KSPL, PERSIST, WROWS, KFULL>;
   const int64_t tiles = (int64_t)t.tiles_m * t.tiles_n;
   // (one workgroup of a kernel that walks tiles fits a CU)
   const int64_t grid = PERSIST && tiles > num_cus && num_cus >= kNumXcd ? num_cus - num_cus % kNumXcd : tiles;
@@ -483,22 +493,24 @@ hipError_t launch_kernel(const LinearActArgs& a, int num_cus, hipStream_t stream
   return hipGetLastError();
 }
 
-template <int WM, int WN, int KSPL, bool PERSIST>
+template <int WM, int WN, int FN, int KSPL, bool PERSIST>
 hipError_t launch_shape(const LinearActArgs& a, int num_cus, hipStream_t stream) {
   if (a.K % KS == 0)
-    return a.row_scales ? launch_kernel<WM, WN, KSPL, PERSIST, true, true>(a, num_cus, stream)
-                        : launch_kernel<WM, WN, KSPL, PERSIST, false, true>(a, num_cus, stream);
-  return a.row_scales ? launch_kernel<WM, WN, KSPL, PERSIST, true, false>(a, num_cus, stream)
-                      : launch_kernel<WM, WN, KSPL, PERSIST, false, false>(a, num_cus, stream);
+    return a.row_scales ? launch_kernel<WM, WN, FN, KSPL, PERSIST, true, true>(a, num_cus, stream)
+                        : launch_kernel<WM, WN, FN, KSPL, PERSIST, false, true>(a, num_cus, stream);
+  return a.row_scales ? launch_kernel<WM, WN, FN, KSPL, PERSIST, true, false>(a, num_cus, stream)
+                      : launch_kernel<WM, WN, FN, KSPL, PERSIST, false, false>(a, num_cus, stream);
 }
 
 }  // namespace
 
 hipError_t launch_linear_block_tile(const LinearActArgs& g, int tile, int num_cus, hipStream_t stream) {
   switch (tile) {
-    case kTile256x128: return launch_shape<4, 2, 1, true>(g, num_cus, stream);
-    case kTile128x128: return launch_shape<2, 2, 1, false>(g, num_cus, stream);
-    default: return launch_shape<2, 2, 2, false>(g, num_cus, stream);
+    case kTile256x128: return launch_shape<4, 2, 2, 1, true>(g, num_cus, stream);
+    case kTile128x128: return launch_shape<2, 2, 2, 1, false>(g, num_cus, stream);
+    case kTile128x64K2: return launch_shape<2, 2, 1, 2, false>(g, num_cus, stream);
+    case kTile128x64: return launch_shape<2, 2, 1, 1, false>(g, num_cus, stream);
+    default: return launch_shape<2, 2, 2, 2, false>(g, num_cus, stream);
   }
 }
 

@@ -36,7 +36,8 @@ SHAPES = [(1, 1, 16), (1, 100, 128), (1, 4096, 272), (1, 8192, 400), (7, 20000, 
           (17, 257, 384), (33, 96, 2064), (40, 3001, 256), (64, 130, 512), (65, 2000, 640), (100, 777, 1296),
           (130, 4097, 128), (257, 1023, 272), (600, 900, 528), (513, 2052, 160),
           (20, 9000, 272), (1030, 2100, 400), (700, 3150, 128), (1100, 5003, 272), (2200, 2049, 528), (1024, 3000, 2064),
-          (510, 16380, 2064)]
+          (510, 16380, 2064), (60, 18001, 272), (140, 9000, 1296), (500, 4001, 1296), (505, 4002, 1408), (1500, 5003, 528),
+          (1500, 1450, 4112)]
 
 
 @pytest.mark.parametrize("w_rows", [False, True])
@@ -134,10 +135,11 @@ def test_nan_and_infinite_scales_stay_in_their_rows(M, N, K):
 
 
 @pytest.mark.parametrize("w_rows", [False, True])
-@pytest.mark.parametrize("K", [1264, 1296, 1408])   # 10 and 11 blocks, whole and not
-def test_infinite_first_scales_stay_in_their_rows(K, w_rows):
-    # the two halves of K that a tile's wave groups take end at different blocks
-    M, N = 1500, 1450
+@pytest.mark.parametrize("M,N,K", [(1500, 1450, 1264), (1500, 1450, 1296), (1500, 1450, 1408), (505, 4002, 1264),
+                                   (505, 4002, 1296), (505, 4002, 1408), (1500, 1450, 4080), (1500, 1450, 4112)])
+def test_infinite_first_scales_stay_in_their_rows(M, N, K, w_rows):
+    # even and odd numbers of blocks, the last one whole and not: the two halves of K that a tile's wave groups take
+    # end at different blocks
     qx, qw, sx, sw, _ = operands(M, N, K, w_rows, 10)
     y = fp8.fp8_linear_block(*on(qx, qw, sx, sw), out_kind=fp8.OUT_F32)
     sx2, sw2 = sx.clone(), sw.clone()
