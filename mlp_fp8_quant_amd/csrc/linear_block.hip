@@ -278,6 +278,7 @@ int linear_block_plan(int64_t M, int64_t N, int64_t K) {
     }
   };
   const int64_t narrow = up(M, 128) * up(N, 64), square = up(M, 128) * up(N, 128), large = up(M, 256) * up(N, 128);
+  if (narrow > INT32_MAX / 512) return kTile256x128;   // walks tiles: a launch counts its threads in 32 bits
   const double narrows = (double)narrow / kCus, pairs = (double)square / (2 * kCus);   // for each CU; pair of places
   auto fill = [&](int64_t tiles) { return tiles < kCus ? (double)tiles / kCus : 1.0; };
   offer(kTile128x64K2, (double)up(narrow, kCus) * ((0.0030 + 0.0012 * fill(narrow)) * k + 4.8));

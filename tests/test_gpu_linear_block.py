@@ -177,3 +177,19 @@ def test_leading_dimensions_and_nothing_past_the_output():
     buf = torch.full((30 * 129 + 64,), 7.0, dtype=BF16, device=device())
     fp8.fp8_linear_block(*d, out=buf[:30 * 129].view(30, 129))
     assert torch.equal(buf[:30 * 129].view(30, 129), flat) and (buf[30 * 129:] == 7).all()
+
+
+def test_most_rows():
+    # as many rows as the call takes: more tiles than a launch could number threads for
+    M, N, K = 2 ** 31 - 1, 3, 16
+    qx, qw, sx, sw, g = operands(64, N, K, False, 5)
+    rows = torch.cat((torch.arange(0, 8), torch.randint(8, M - 8, (48,), generator=g), torch.arange(M - 8, M)))
+    dqx = torch.zeros(M, K, dtype=torch.uint8, device=device())
+    dsx = torch.zeros(M, 1, device=device())
+    at = rows.to(device())
+    dqx[at], dsx[at] = qx.to(device()), sx.to(device())
+    y = fp8.fp8_linear_block(dqx, qw.to(device()), dsx, sw.to(device()))
+    y64, _, err, _ = ref.linear(qx, qw, sx, sw, False)
+    ref.check(y[at].cpu(), y64, err, "bf16")
+    y[at] = 0
+    assert not any(bool(part.any()) for part in y.split(2 ** 28))

@@ -198,3 +198,51 @@ def test_ranks_and_a_flat_gate():
     got = fp8.fp8_residual_norm_backward(dev(t3["x"]), r3, dev(t["w"]), rstd, dev(t3["h"]), gate=dev(t3["gate"]),
                                          post_weight=dev(t["post"]), post_rstd=prstd)
     assert got[0].shape == (2, 12, 264) and got[3].shape == (264,)
+
+
+def test_widest_rows():
+    # as many columns as the calls take.  In each result a value is off by a handful of FP32 roundings (at most 12, 16
+    # counted) of the magnitudes that are added for it; dx and r by their BF16 rounding besides.
+    H, rows, U, alpha = 2 ** 26, 2, 2.0 ** -24, 0.5
+    g = torch.Generator(device=device()).manual_seed(3)
+    r = lambda *s: torch.randn(*s, generator=g, device=device())  # noqa: E731
+    x, h, dy = (r(rows, H).to(BF16) for _ in range(3))
+    w, gate, post = (1 + 0.1 * r(H) for _ in range(3))
+
+    def close(got, want, size, half=0.0):
+        for a, b, c in zip(got.view(-1, H), want.view(-1, H), size.view(-1, H)):
+            assert ((a.double() - b).abs() <= 16 * U * c + half * b.abs()).all()
+
+    y, got_r, rstd, prstd = fp8.fp8_residual_norm(x, w, h, gate=gate, post_weight=post, alpha=alpha, out_kind=fp8.OUT_F32,
+                                                  stats=True)
+    f = alpha * gate.double() * post.double()
+    rms = lambda t: (t * t).mean(-1, keepdim=True).add(1e-6).rsqrt()  # noqa: E731
+    prs = rms(h.double())
+    v = h.double() * prs * f
+    r64 = x.double() + v
+    rs = rms(r64)
+    size = x.double().abs() + v.abs()
+    assert ((prstd.double() * prs.reciprocal().view(-1) - 1).abs() <= 16 * U).all()
+    assert ((rstd.double() * rs.reciprocal().view(-1) - 1).abs() <= 16 * U).all()
+    close(y, r64 * rs * w, size * rs * w.abs())
+    close(got_r, r64, size, 2.0 ** -8)
+    del y, v, r64, size
+    dx, dh, dw, dgate, dpost = fp8.fp8_residual_norm_backward(dy, got_r, w, rstd, h, gate=gate, post_weight=post,
+                                                              post_rstd=prstd, alpha=alpha)
+    n = got_r.double() * rstd.double().view(-1, 1)
+    gw = dy.double() * w.double()
+    c = (gw * n).mean(-1, keepdim=True)
+    rs = rstd.double().view(-1, 1)
+    # (c is off by some 2^-24 of the mean magnitude, about 1)
+    dx64, size = rs * (gw - n * c), rs * (gw.abs() + n.abs())
+    close(dx, dx64, size, 2.0 ** -8)
+    close(dw, (dy.double() * n).sum(0), (dy.double() * n).abs().sum(0))
+    del gw, n
+    z = h.double() * prstd.double().view(-1, 1)
+    zx, zs = (dx64 * z).sum(0), (size * z.abs()).sum(0)
+    close(dgate, alpha * post.double() * zx, alpha * post.double().abs() * zs)
+    close(dpost, alpha * gate.double() * zx, alpha * gate.double().abs() * zs)
+    p = dx64 * f
+    c2 = (p * z).mean(-1, keepdim=True)
+    prs = prstd.double().view(-1, 1)
+    close(dh, prs * (p - z * c2), prs * (size * f.abs() + z.abs()), 2.0 ** -8)
