@@ -113,3 +113,32 @@ def test_silu_of_infinities():
     q, s = fp8.silu_mul_2in_block(a.to(device()), b.to(device()))
     assert torch.isinf(s[0, 0]) and torch.isnan(s[1, 0]) and torch.isnan(s[2, 0])   # -Inf / (1 + Inf) is NaN
     assert q[0, 5] == 0x7F and (q[0, :5] == 0).all() and (q[1] == 0x7F).all() and (q[2] == 0x7F).all()
+
+
+@pytest.mark.parametrize("tile", [False, True])
+@pytest.mark.parametrize("transpose", [False, True])
+def test_more_elements_than_32_bits_count(tile, transpose):
+    # the last rows, 128 of which are a block: as if they were alone
+    M, K, last = 256 * 131 + 40, 65537, 128 + 40
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device=device())
+    x[-last:] = torch.randn(last, K, generator=torch.Generator(device=device()).manual_seed(1), device=device())
+    part = x[-last:].clone()
+    q, s = fp8.fp8_quant_block(x, tile=tile, transpose=transpose)
+    qp, sp = fp8.fp8_quant_block(part, tile=tile, transpose=transpose)
+    if transpose:
+        assert torch.equal(q[:, M - last:], qp) and torch.equal(s[:, -2:], sp)
+        assert not any(bool(c[:, :M - last].any()) for c in q.split(2 ** 13))
+    else:
+        blocks = 2 if tile else last
+        assert torch.equal(q[-last:], qp) and torch.equal(s[-blocks:], sp)
+        assert not any(bool(c.any()) for c in q[:-last].split(2 ** 13))
+
+
+def test_swiglu_of_more_elements_than_32_bits_count():
+    M, K, last = 33000, 65536, 50
+    g = torch.zeros(M, K, dtype=torch.bfloat16, device=device())
+    g[-last:] = torch.randn(last, K, generator=torch.Generator(device=device()).manual_seed(2), device=device())
+    u = g + 1
+    q, s = fp8.silu_mul_2in_block(g, u)
+    qp, sp = fp8.silu_mul_2in_block(g[-last:].clone(), u[-last:].clone())
+    assert torch.equal(q[-last:], qp) and torch.equal(s[-last:], sp) and not bool(s[:-last].any())
