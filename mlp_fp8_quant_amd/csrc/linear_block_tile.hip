@@ -309,9 +309,12 @@ __global__ __launch_bounds__(WM* WN * 64 * KSPL, 2) void linear_block_tile_kerne
     if (KT > 1) issue_stage(win, goff, kc, buf1, gstage(1));
   }
   if (KT > 0) {
-    // (two stages, scales and, where staged, the previous epilogue's accesses
-    // count together: wait for all of them)
-    __builtin_amdgcn_s_waitcnt(0x0F70);
+    // the first stage and the scales before it have landed; where staged the
+    // previous epilogue's accesses count too: wait for all (vmcnt alone: gfx9
+    // encoding)
+    static_assert(LPW < 64, "vmcnt has six bits");
+    if (!PERSIST && KT > 1) __builtin_amdgcn_s_waitcnt(0x0F70 | (LPW & 15) | ((LPW >> 4) << 14));
+    else __builtin_amdgcn_s_waitcnt(0x0F70);
     __syncthreads();
     rd(0, 0, 0);
   }
