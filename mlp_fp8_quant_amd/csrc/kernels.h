@@ -152,7 +152,7 @@ hipError_t launch_linear_tile(const LinearActArgs& g, const LinearPlan& p, int a
 // (fp8_linear_block): a.sx [M, KB], a.sw [N, KB] with a.row_scales, else
 // [ceil(N / 128), KB]; KB = ceil(K / 128).
 hipError_t launch_linear_block(const LinearActArgs& g, int num_cus, hipStream_t stream);
-// The tiled kernels, tile one of LinearTile's 256x128, 128x128, 128x128K2.
+// The tiled kernels, tile one of LinearTile's from kTile256x128 on.
 hipError_t launch_linear_block_tile(const LinearActArgs& g, int tile, int num_cus, hipStream_t stream);
 
 // Codes and scales of x [M, K] with a scale for each block of 128 (fp8_quant_block).
