@@ -245,10 +245,11 @@ hipError_t launch_rows(const LinearActArgs& g, hipStream_t stream) {
 }
 
 // How a shape runs (MI355X, 256 CUs; us measured).  Few outputs: the smallest
-// tile whose grid gives no CU more than one workgroup: 1x4096x4096 5.3 with one block (with two 5.6), 64x4096x4096
-// 7.6 with 32x32 (64x32 10.1, 32x16 10.6), 256x4096x4096 15.6 with 64x64 (128x64 18.0), 86x5351x1520 8.6 with 64x64 (64x32, two
-// to some CUs, 11.3);
-// and up to 64 rows 64x64 in pairs: 40x20000x4096 24.7 (128x64 35.8).
+// tile whose grid gives no CU more than one workgroup: 1x4096x4096 5.3 with one
+// block (with two 5.6), 64x4096x4096 7.6 with 32x32 (64x32 10.1, 32x16 10.6),
+// 86x5351x1520 8.6 with 64x64 (64x32, two to some CUs, 11.3), 256x4096x4096 15.6 with
+// 64x64 (128x64 18.0); and up to 64 rows 64x64 in pairs: 40x20000x4096 24.7 (128x64
+// 35.8).
 //
 // More outputs: the least of the estimates below, rounds of workgroups times (rate
 // * K + what a tile costs besides), the rate less where a round leaves CUs idle.
