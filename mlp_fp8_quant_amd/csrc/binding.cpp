@@ -15,6 +15,8 @@
 
 #include <ATen/ATen.h>
 #include <ATen/hip/EmptyTensor.h>
+#include <ATen/record_function.h>
+#include <c10/core/impl/LocalDispatchKeySet.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "../../include/fp8mot.h"
@@ -27,10 +29,19 @@ PyObject* g_get_device = nullptr;    // torch._C._cuda_getDevice
 
 struct Skip {};   // not the common case
 
-// A new tensor on `like`'s device, straight from its allocator: at::empty's way
-// through the dispatcher takes longer than that (0.9 us instead of 0.4), and the
-// inputs of the common case are tensors that no mode wraps.
+// Whether anything would see, or change, what at::empty does: a dispatch mode or
+// a transform of this thread, a profiler, deterministic algorithms (which fill
+// new tensors).
+bool watched() {
+  return !(c10::impl::tls_local_dispatch_key_set().included_ - c10::default_included_set).empty() ||
+         at::hasCallbacks() || at::globalContext().deterministicAlgorithms();
+}
+
+// A new tensor on `like`'s device.  Where nothing watches, straight from its
+// allocator: at::empty's way through the dispatcher takes longer than that (0.9 us
+// instead of 0.4).
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) {
+  if (watched()) return at::empty(shape, like.options().dtype(type));
   return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
 }
 
