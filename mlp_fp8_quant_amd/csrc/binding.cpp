@@ -37,17 +37,18 @@ bool watched() {
          at::hasCallbacks() || at::globalContext().deterministicAlgorithms();
 }
 
-// A new tensor on `like`'s device.  Where nothing watches, straight from its
-// allocator: at::empty's way through the dispatcher takes longer than that (0.9 us
-// instead of 0.4).
-at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) {
-  if (watched()) return at::empty(shape, like.options().dtype(type));
-  return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
-}
-
 // A plain tensor (or parameter) of the call's device.
 struct Call {
   int dev = -1;
+  const bool seen = watched();
+
+  // A new tensor on `like`'s device.  Where nothing watches, straight from its
+  // allocator: at::empty's way through the dispatcher takes longer than that (0.9
+  // us instead of 0.4).
+  at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) const {
+    if (seen) return at::empty(shape, like.options().dtype(type));
+    return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
+  }
 
   const at::Tensor& plain(PyObject* o) {
     if (!THPVariable_CheckExact(o) && (PyObject*)Py_TYPE(o) != g_parameter) throw Skip();
@@ -183,7 +184,7 @@ PyObject* linear_act(PyObject*, PyObject* const* a, Py_ssize_t n) {
     shape.back() = N;
     const at::Tensor out = c.output(a[11], shape, type, qx);
     at::Tensor pre;
-    if (a[10] == Py_True) pre = fresh(shape, at::kBFloat16, qx);
+    if (a[10] == Py_True) pre = c.fresh(shape, at::kBFloat16, qx);
     else if (a[10] != Py_False && a[10] != Py_None) pre = c.of(a[10], at::kBFloat16, M * N);
     const at::Tensor ws = c.scratch(a[13], fp8_linear_act_workspace(M, N, K), qx);
     const hipStream_t stream = c.stream();
@@ -242,8 +243,8 @@ PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor out = c.output(a[7], x.sizes(), type, x);
     at::Tensor mean, rstd;
     if (flag(a[6])) {
-      mean = fresh(x.sizes().slice(0, x.dim() - 1), at::kFloat, x);
-      rstd = fresh(x.sizes().slice(0, x.dim() - 1), at::kFloat, x);
+      mean = c.fresh(x.sizes().slice(0, x.dim() - 1), at::kFloat, x);
+      rstd = c.fresh(x.sizes().slice(0, x.dim() - 1), at::kFloat, x);
     }
     const float eps = (float)PyFloat_AS_DOUBLE(a[3]);
     const hipStream_t stream = c.stream();
@@ -373,7 +374,7 @@ PyObject* linear_block(PyObject*, PyObject* const* a, Py_ssize_t n) {
     shape.back() = N;
     const at::Tensor out = c.output(a[10], shape, type, qx);
     at::Tensor pre;
-    if (a[9] == Py_True) pre = fresh(shape, at::kBFloat16, qx);
+    if (a[9] == Py_True) pre = c.fresh(shape, at::kBFloat16, qx);
     else if (a[9] != Py_False && a[9] != Py_None) pre = c.of(a[9], at::kBFloat16, M * N);
     const hipStream_t stream = c.stream();
     const int st = without_gil([&] {
@@ -441,8 +442,8 @@ PyObject* residual_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (h != nullptr) r = c.output(a[11], x.sizes(), x.scalar_type(), x);
     const bool stats = flag(a[9]);
     if (stats) {
-      rstd = fresh(lead, at::kFloat, x);
-      if (post != nullptr) post_rstd = fresh(lead, at::kFloat, x);
+      rstd = c.fresh(lead, at::kFloat, x);
+      if (post != nullptr) post_rstd = c.fresh(lead, at::kFloat, x);
     }
     const hipStream_t stream = c.stream();
     const int st = without_gil([&] {
