@@ -506,14 +506,17 @@ int fp8_layer_norm_backward(const void* dy, int dy_elem, const void* x, int x_el
  * with its scale, and the norm before the next block with direct FP8 emission
  * for the projections that read it (root mean square norms):
  *   post_rstd = 1 / sqrt(sum_i hidden[i]^2 / H + eps)
- *   v    = hidden[i] * post_rstd * post_weight[i]  (hidden[i] without post_weight)
- *   r[i] = fma(alpha, v * gate[i], x[i])           the residual stream, x's type
+ *   z    = hidden[i] * post_rstd                   (hidden[i] without post_weight)
+ *   f    = (alpha * gate[i]) * post_weight[i]      (alpha times what there is)
+ *   r[i] = fma(z, f, x[i])                         the residual stream, x's type
  *   rstd = 1 / sqrt(sum_i r[i]^2 / H + eps)
  *   w    = r[i] * rstd * weight[i]
  *   y[i] = bf16_rne(w) | e4m3(w / *d_sy) (times fp32(1 / *d_sy)) | w, or with
  *          FP8MOT_OUT_FP8_BLOCK codes [rows, ld(H)] and d_scales [rows, nb(H)]
  *          as fp8_quant_block gives them of w
- * in FP32; rstd and w are taken from r before its rounding to x's type.
+ * each step one FP32 operation; rstd and w are taken from r before its rounding
+ * to x's type.  f is formed before hidden comes in: where alpha * gate leaves
+ * FP32's range f is infinite or 0, also where the whole product would be in it.
  *  - x, r: [rows, H] of x_elem; hidden: [rows, H] of h_elem, or NULL for the
  *    norm alone (r, gate and post_weight then have to be NULL: y of x).
  *  - gate: NULL, or [gates, H] of gate_elem, each row the gate of rows / gates
@@ -542,11 +545,12 @@ size_t fp8_residual_norm_backward_workspace(int64_t rows, int64_t H, int64_t gat
  * passes its gradient straight through) and dr, what reaches r past the norm:
  *   n = r * rstd,  g = dy * weight,  z = hidden * post_rstd (hidden without post_weight)
  *   dx = rstd * (g - n * sum_i(g * n) / H) + dr
- *   p  = dx * (alpha * gate * post_weight)
+ *   p  = dx * ((alpha * gate) * post_weight)
  *   dhidden = post_rstd * (p - z * sum_i(p * z) / H)  (p without post_weight)
  *   dweight = sum_rows dy * n,   dpost_weight = sum_rows alpha * gate * dx * z
  *   dgate   = alpha * post_weight * the sum of dx * z over the gate's rows
- * in FP32, dx not yet rounded where it is used again.  r, rstd, post_rstd:
+ * in FP32, dx not yet rounded where it is used again; of the last two, factors
+ * that rows share multiply those rows' sum.  r, rstd, post_rstd:
  * what fp8_residual_norm wrote (r as stored).  dy, hidden, dhidden: of h_elem;
  * r, dr, dx: of r_elem.  Without hidden gate, post_weight, dhidden, dgate and
  * dpost_weight have to be NULL; dr NULL: no such gradient.  dweight,

@@ -581,7 +581,8 @@ def fp8_residual_norm(x, weight=None, hidden=None, gate=None, post_weight=None, 
         r = x + alpha * gate * v
         y = r * rsqrt(mean(r^2) + eps) * weight
 
-    ``gate`` [H], or [gates, H] with a gate for each rows / gates rows.  Returns
+    with alpha * gate * post_weight formed first, as one FP32 factor of hidden's
+    norm.  ``gate`` [H], or [gates, H] with a gate for each rows / gates rows.  Returns
     (y, r): y BF16, FP32 or (at the scale ``sy``) E4M3 codes, or with
     OUT_FP8_BLOCK a pair (codes, scales) as fp8_quant_block gives; r has x's type
     and is written to ``stream_out`` (which may be x itself) where that is given.

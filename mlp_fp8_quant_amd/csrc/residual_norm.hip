@@ -2,11 +2,11 @@
 // scale, and their backward pass (declared in include/fp8mot.h as
 // fp8_residual_norm and fp8_residual_norm_backward).
 //
-//   forward   v = h rs_h pw (or h),  rs_h = 1 / sqrt(sum h^2 / H + eps)
-//             r = x + alpha gate v                    the residual stream
+//   forward   z = h rs_h (or h),  rs_h = 1 / sqrt(sum h^2 / H + eps)
+//             r = x + z (alpha gate pw)               the residual stream
 //             y = r rs w,  rs = 1 / sqrt(sum r^2 / H + eps)
 //   backward  g = dy w,  n = r rs,  z = h rs_h (or h)
-//             dx = rs (g - n sum(g n) / H) + dr,  p = alpha gate pw dx
+//             dx = rs (g - n sum(g n) / H) + dr,  p = dx (alpha gate pw)
 //             dh = rs_h (p - z sum(p z) / H)  (or p)
 //             dw = sum_rows dy n,  A = sum of dx z over a gate's rows:
 //             dgate = alpha pw A,  dpw = sum_gates alpha gate A
@@ -118,7 +118,8 @@ __device__ __forceinline__ void emit8(const ResidualNormArgs& g, int64_t r, int6
   }
 }
 
-// alpha gate pw of eight columns: what the block's output is multiplied by.
+// (alpha gate) pw of eight columns: what the block's output is multiplied by, as
+// one factor, which a walk over rows of one gate forms once.
 template <class Args>
 __device__ __forceinline__ void factor8(const Args& g, int64_t gate, int64_t i, float* f) {
   float pw[8];
