@@ -347,7 +347,8 @@ int fp8_quant_block(const void* x, int x_elem, uint8_t* q, float* d_scales, int6
 
 /* silu_mul_2in_fp8 with a scale for each 128 columns of a row, taken from the
  * values themselves instead of calibrated:
- *   v = g / (1 + exp(-g)) * u            (FP32, within about 2 ulp)
+ *   v = g / (1 + exp(-g)) * u            (FP32, within 9 * 2^-24 of its value;
+ *                                         zero where exp(-g) overflows)
  *   q, scales = fp8_quant_block of v [M, K]  (tile 0, transpose 0)
  * g, u: BF16 [M, K], 16-byte aligned like q [M, ld(K)]; limits as there. */
 int silu_mul_2in_block(const uint16_t* g, const uint16_t* u, uint8_t* q, float* d_scales,

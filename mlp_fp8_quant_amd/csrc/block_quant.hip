@@ -22,11 +22,13 @@ namespace {
 using namespace rows;
 using block::kBlock;
 
-// silu(g) u in FP32, to about 2 ulp: exp(-g) as 2^(hi + lo) with lo the part of
-// g log2(e) that hi rounds off (2^lo = 1 + lo ln 2), g times the reciprocal after
-// a Newton step.  (silu_mul's plain exponential is off by |g| 2^-24, which an
-// FP32 scale would show.)  Where the exponential is large or infinite, a division,
-// as the formula has it.
+// silu(g) u in FP32: exp(-g) as 2^(hi + lo) with lo the part of g log2(e) that hi
+// rounds off (2^lo = 1 + lo ln 2), g times the reciprocal after a Newton step.
+// (silu_mul's plain exponential is off by |g| 2^-24, which an FP32 scale would
+// show.)  Where the exponential is large or infinite, a division, as the formula
+// has it.  With w = 2^-24: the hardware's exponential is within 2 w, 1 + lo ln 2 and
+// their product round, d rounds (5 w so far), the refined reciprocal, its product
+// with g and that with u round: 8 w and terms of second order, 9 w as the bound.
 __device__ __forceinline__ float silu_mul_close(float g, float u) {
   const float c = __builtin_amdgcn_fmed3f(g, -128.0f, 128.0f);   // lo stays finite
   const float hi = __fmul_rn(c, -1.44269504f);
