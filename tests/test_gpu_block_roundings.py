@@ -1,0 +1,90 @@
+"""GPU: the product of block-scaled operands and the norms' sums over rows, held to
+the roundings that their kernels take (u = 2^-24, half a step of FP32)."""
+
+import pytest
+import torch
+
+import block_norm_ref as ref
+import mlp_fp8_quant_amd as fp8
+
+from block_tile_shapes import KERNEL_SHAPES
+from gpu_util import device
+from norm_linear_ref import U
+from test_gpu_linear_block import on, operands
+
+pytestmark = pytest.mark.gpu
+F32 = torch.float32
+
+
+def product(qx, qw, sx, sw, w_rows):
+    """(y, sum|terms|) in 64 bits, each block's scale one FP32 number."""
+    a, b = ref.decode(qx), ref.decode(qw)
+    (M, K), N = a.shape, b.shape[0]
+    sw = sw if w_rows else sw.repeat_interleave(128, dim=0)[:N]
+    y, terms = torch.zeros(M, N, dtype=torch.float64), torch.zeros(M, N, dtype=torch.float64)
+    for i in range((K + 127) // 128):
+        c = slice(128 * i, 128 * i + 128)
+        alpha = (sx[:, i:i + 1] * sw[:, i].view(1, -1)).double()
+        y += (a[:, c] @ b[:, c].t()) * alpha
+        terms += (a[:, c].abs() @ b[:, c].abs().t()) * alpha
+    return y, terms
+
+
+@pytest.mark.parametrize("w_rows", [False, True])
+@pytest.mark.parametrize("kernel,shape", [(k, s) for k, shapes in KERNEL_SHAPES.items() for s in shapes])
+def test_products(kernel, shape, w_rows):
+    # A block's 128 products are exact; the matrix core adds them eight at a time, a rounding within each eight and
+    # one as they join the sum (test_the_matrix_core_adds_eight_products): 17 u.  Then one FMA for each block and at
+    # most 16 additions of partial sums: (K / 128 + 34) u of sum|terms|, held to 36.
+    M, N, K = shape
+    qx, qw, sx, sw, _ = operands(M, N, K, w_rows, 3 * M + N)
+    r = torch.tensor(sorted({0, 1, 31, 32, 63, 64, 127, 128, 255, 256, M // 3, M // 2, M - 1} & set(range(M))))
+    y, terms = product(qx[r], qw, sx[r], sw, w_rows)
+    got = fp8.fp8_linear_block(*on(qx, qw, sx, sw), out_kind=fp8.OUT_F32)[r.to(device())].cpu().double()
+    worst = ((got - y).abs() / (((K + 127) // 128 + 36) * U * terms)).max().item()
+    assert worst <= 1.0, worst
+
+
+@pytest.mark.parametrize("N", [64, 20000])
+def test_the_matrix_core_adds_eight_products(N):
+    # beside a product of 2^16, whose step is 2^-7, two of 2^-8 are lost one by one (ties to even) and kept together
+    e = lambda v: int(torch.tensor(v).to(torch.float8_e4m3fn).view(torch.uint8))  # noqa: E731
+    qx = torch.zeros(128, 128, dtype=torch.uint8)
+    qw = torch.full((N, 128), e(2.0 ** -4), dtype=torch.uint8)
+    qx[:, 0], qw[:, 0] = e(256.0), e(256.0)
+    qx[:, 64] = e(2.0 ** -4)
+    for m in range(1, 128):
+        qx[m, m] = e(2.0 ** -4)                # (row 64: one product)
+    one = torch.ones(128, 1), torch.ones((N + 127) // 128, 1)
+    y = fp8.fp8_linear_block(*on(qx, qw, *one), out_kind=fp8.OUT_F32).cpu().double()
+    together = torch.zeros(128, dtype=torch.bool)
+    together[65:72] = True
+    assert torch.equal(y, torch.where(together, 65536.0 + 2.0 ** -7, 65536.0).double()[:, None].expand(128, N))
+
+
+# (rows, columns, gates): a few and many columns, slabs of a gate's rows, and gates that share a slab
+SUMS = [(16384, 64, 1), (16384, 520, 1), (16384, 1027, 8), (16384, 4096, 1), (16384, 64, 8), (16384, 64, 16384),
+        (65536, 40, 1), (4096, 8200, 1)]
+
+
+@pytest.mark.parametrize("rows,H,gates", SUMS)
+def test_sums_over_rows(rows, H, gates):
+    # Terms 1 + 2^-12 .. of which a serial FP32 sum loses a quarter of its step at every addition, always downwards:
+    # some 2^-13 of it at 16384 rows.  The kernels add at most 64 rows one after another here, the rows side by side
+    # in a tree, at most 64 slabs one after another and 16 runs of them: 160 u of the sum.
+    term = 1.0 + (1 + 2 * torch.arange(H, device=device()) % 5) * 2.0 ** -12
+    x = term.expand(rows, H).contiguous()
+    one = torch.ones(rows, H, device=device())
+    stat, ones = torch.ones(rows, device=device()), torch.ones(H, device=device())
+    # dy 1, n = r rstd = term
+    got = fp8.fp8_residual_norm_backward(one, x, ones, stat, alpha=0.5)
+    want = rows * term.double()
+    assert ((got[2].double() - want).abs() <= 160 * U * want).all(), "dweight"
+    # dy 0: dx = dr = term, z = hidden post_rstd = 1
+    gate = torch.full((gates, H), 0.5, device=device())
+    _, _, dw, dgate, dpost = fp8.fp8_residual_norm_backward(0 * one, x, ones, stat, one, gate=gate, post_weight=ones,
+                                                            post_rstd=stat, alpha=0.5, dr=x)
+    assert (dw == 0).all()
+    each = 0.5 * (rows // gates) * term.double()
+    assert ((dgate.double() - each).abs() <= 162 * U * each).all(), "dgate"
+    assert ((dpost.double() - 0.25 * want).abs() <= 162 * U * 0.25 * want).all(), "dpost_weight"
