@@ -532,7 +532,8 @@ int fp8_residual_norm(const void* x, int x_elem, const void* hidden, int h_elem,
     const Span st = {rstd, rows * 4}, su = {post_weight != nullptr ? post_rstd : nullptr, rows * 4};
     const Span scale = {out_kind == FP8MOT_OUT_FP8 ? d_sy : nullptr, 4};
     if (!same_or_apart(sr, sx) || !apart(sr, {sh, sg, sp, sw, sy, sc, st, su, scale}) ||
-        !(hidden == nullptr ? same_or_apart(sy, sx) : apart(sy, sx)) || !apart(sy, {sh, sg, sp, sw, sc, st, su, scale}) ||
+        // (codes are never x itself, though rows of 4 FP32 or 8 BF16 take the bytes of their padded codes)
+        !(hidden == nullptr && !block ? same_or_apart(sy, sx) : apart(sy, sx)) || !apart(sy, {sh, sg, sp, sw, sc, st, su, scale}) ||
         !apart(sc, {sx, sh, sg, sp, sw, st, su}) || !apart(st, {sx, sh, sg, sp, sw, su, scale}) ||
         !apart(su, {sx, sh, sg, sp, sw, scale}))
       return FP8MOT_ERR_INVALID_ARG;
