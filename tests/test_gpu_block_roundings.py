@@ -69,8 +69,8 @@ SUMS = [(16384, 64, 1), (16384, 520, 1), (16384, 1027, 8), (16384, 4096, 1), (16
 
 @pytest.mark.parametrize("rows,H,gates", SUMS)
 def test_sums_over_rows(rows, H, gates):
-    # Terms 1 + 2^-12 .. of which a serial FP32 sum loses a quarter of its step at every addition, always downwards:
-    # some 2^-13 of it at 16384 rows.  The kernels add at most 64 rows one after another here, the rows side by side
+    # Terms 1 + 2^-12 to 1 + 5 * 2^-12, which a long FP32 sum rounds the same way at every addition: one after another,
+    # most columns end some 3000 u off at 16384 rows.  The kernels add at most 64 rows one after another here, the rows side by side
     # in a tree, at most 64 slabs one after another and 16 runs of them: 160 u of the sum.
     term = 1.0 + (1 + 2 * torch.arange(H, device=device()) % 5) * 2.0 ** -12
     x = term.expand(rows, H).contiguous()
