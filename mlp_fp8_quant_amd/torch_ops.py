@@ -264,7 +264,8 @@ def residual_norm(x: torch.Tensor, hidden: torch.Tensor, weight: Optional[torch.
                   sy: Optional[torch.Tensor] = None
                   ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
     """(y, r, rstd, post_rstd) of a block's output and the stream it is added
-    to; post_rstd is empty without post_weight."""
+    to; post_rstd is empty without post_weight.  (Block codes: residual_norm_block.)"""
+    api._out_dtype(out_kind)
     y, r, rstd, post = api.fp8_residual_norm(x, weight, hidden, gate, post_weight, alpha, eps,
                                              out_kind, sy, stats=True)
     return y, r, rstd, rstd.new_empty(0) if post is None else post
