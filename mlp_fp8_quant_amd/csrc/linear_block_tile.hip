@@ -172,8 +172,8 @@ __global__ __launch_bounds__(WM* WN * 64 * KSPL, 2) void linear_block_tile_kerne
 #pragma unroll
       for (int c = 0; c < (W_COPIES + WAVES - 1) / WAVES; ++c) {
         const int d = c * WAVES + wave_id, s = d / (BN / 64), r = d % (BN / 64);
-        if (W_COPIES >= WAVES || d < W_COPIES) copy4_to_lds(w.ws, dst + XS + d * 256, h * kBatch + s < stages ? (r * 64 + ln) * stages * 4 : kOOB,
-                     h * 16 + s * 4);
+        const int off = h * kBatch + s < stages ? (r * 64 + ln) * stages * 4 : kOOB;
+        if (W_COPIES >= WAVES || d < W_COPIES) copy4_to_lds(w.ws, dst + XS + d * 256, off, h * 16 + s * 4);
       }
     } else {
       if (x) copy_to_lds(w.xs, dst + wave_id * 1024, (wave_id * 64 + ln) * stages * 4, h * 16);
