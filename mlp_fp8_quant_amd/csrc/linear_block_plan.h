@@ -22,6 +22,13 @@ namespace fp8mot {
 // 75, without groups 68, 256x128 84).  Without: 128x64, three to a CU, 300x16384x2048
 // 28.9 (128x128 32.0, with groups 36.8), 128x128, two, 5000x5000x4096 205 (128x64 218,
 // 256x128 220), 256x128 4096x12288x4096 347 (128x128 357).
+//
+// The times above and the estimates are of W's scales for tiles and BF16 outputs.
+// Of W's scales for rows, whose slots in LDS leave room for two workgroups of 128x64
+// to a CU, every tile takes some 10% longer, so that the same one stays the best or
+// within 4% of it: 4096x1536x2048 128x64 33.5 (256x128 34.2, 128x128 35.5; of tiles'
+// scales 30.6, 32.4, 32.8), 5120x2048x1536 41.7 (53.3, 43.6), FP32 added in place 46.5
+// (58.9, 48.2).
 inline int linear_block_plan(int64_t M, int64_t N, int64_t K) {
   constexpr int64_t kCus = 256;
   auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
