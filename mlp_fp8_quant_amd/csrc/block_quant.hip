@@ -43,8 +43,8 @@ __device__ __forceinline__ float silu_mul_close(float g, float u) {
 // Blocks of 128 columns.  Sixteen lanes take a block, eight columns each, R
 // blocks one after another with all their loads in flight.  FLAT: rows are
 // whole blocks, so that block i lies at element 128 i of x and of q and no
-// division finds its row.  16384x5120 BF16 42 us, 5.9 TB/s; SwiGLU 4096x12288 44
-// to 51 us, 5.1 to 5.9 TB/s.
+// division finds its row.  16384x5120 BF16 53 us, 4.8 TB/s (the same input again and
+// again, in part from the caches, 42); SwiGLU 4096x12288 49 to 56 us, 4.5 to 5.2 TB/s.
 template <bool F32, bool SILU, bool FLAT, int R>
 __global__ __launch_bounds__(256) void quant_rows_kernel(const void* __restrict__ x, const void* __restrict__ u,
                                                          uint8_t* __restrict__ q, float* __restrict__ scales,
@@ -94,7 +94,7 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const void* __restrict_
 }
 
 // 128 x 128 tiles of x with one scale each, a workgroup to a tile (25600x5120 BF16
-// 75 us, 5.3 TB/s; transposed 81): thread t takes
+// 72 to 75 us, 5.3 TB/s; transposed 79 to 81): thread t takes
 // columns 8 (t % 16) .. + 7 of rows 8 (t / 16) .. + 7.  TRANS: the codes of the
 // transposed tensor, turned through 16 KB of LDS (eight codes of one column, rows
 // 8 r .. 8 r + 7, lie at chunk r ^ (column / 8) of the column's 128 bytes, which

@@ -25,7 +25,7 @@ namespace fp8mot {
 //
 // The times above and the estimates are of W's scales for tiles and BF16 outputs.
 // Of W's scales for rows, whose slots in LDS leave room for two workgroups of 128x64
-// to a CU, every tile takes some 10% longer, so that the same one stays the best or
+// to a CU, the tiles take 6 to 19% longer, and the one chosen stays the best or
 // within 4% of it: 4096x1536x2048 128x64 33.5 (256x128 34.2, 128x128 35.5; of tiles'
 // scales 30.6, 32.4, 32.8), 5120x2048x1536 41.7 (53.3, 43.6), FP32 added in place 46.5
 // (58.9, 48.2).

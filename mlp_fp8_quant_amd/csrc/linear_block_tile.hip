@@ -19,14 +19,11 @@
 // bytes per lane and stage (column-major, for 16-byte reads).
 //
 // Many rows are bound by what issues beside the MFMAs and by power: at
-// 16384x25600x5120 (3475 to 3640 us, 1.18 to 1.24 PFLOP/s) the matrix cores work in
-// 62% of the cycles at 1.64 GHz, and decodes, FMAs and addresses issue in 53%.
-// Copies of the kernel that leave out a part (and so err) run 8% faster without the
-// block sums' FMAs, 7% with one decode for all fragments, 11% without the stages'
-// copies, 3% without the barrier, 0% without the wait for the copies.  A wave's
-// part of 64 x 32 decodes half as much again for each MFMA, but two K groups of
-// four such waves fill a CU's places where there are few tiles: 512x4096x12288 56
-// us against 67 with parts of 64 x 64, 0.92 PFLOP/s.
+// 16384x25600x5120 (3470 to 3670 us, 1.17 to 1.24 PFLOP/s) the matrix cores work in
+// 64% of the cycles at 1.67 GHz, and decodes, FMAs and addresses issue in 55%.  A
+// wave's part of 64 x 32 decodes half as much again for each MFMA, but two K groups
+// of four such waves fill a CU's places where there are few tiles: 512x4096x12288 56
+// to 60 us (on the card of the 56, 67 with parts of 64 x 64), 0.86 to 0.92 PFLOP/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -135,8 +135,8 @@ __device__ __forceinline__ void factor8(const Args& g, int64_t gate, int64_t i, 
 // seldom another one: the next row is on its way while this one is summed, and
 // the norms' weights and the gate stay in registers.  FULL: the groups are exactly
 // the row.  16384x5120 BF16 with 8 gates -> BF16 141 us, 4.8 TB/s, bound by memory;
-// -> block codes 139 us, 4.2 TB/s, also by what lies between a row's sums and its
-// codes.
+// -> block codes 137 us, 4.3 TB/s, also by what lies between a row's sums and its
+// codes; x alone -> BF16 67 us, 5.0 TB/s, -> codes 80.
 template <bool XF, bool HF, int TC, int U, int NT, bool FULL>
 __global__ __launch_bounds__(NT) void residual_norm_kernel(ResidualNormArgs g, int64_t walk) {
   __shared__ float red[32];
@@ -387,9 +387,10 @@ __device__ __forceinline__ RowRange rows_of_slab(const ResidualNormBwdArgs& g, c
 // side by side as the workgroup holds; or 0: the whole workgroup).  They walk
 // the rows of the workgroup's slab, which lies within one gate's rows, the next
 // row's loads on their way during this row's sums.  FULL: the threads' columns
-// are exactly the row.  16384x5120 BF16 with 8 gates and dr 202 us, 5.0 TB/s, bound
-// by memory; 512x4096 12, by four rows one after another.  MANY: gates share a slab, and rows side by side are those
-// of different gates, each T threads walking `together` gates of their own.
+// are exactly the row.  16384x5120 BF16 with 8 gates and dr 203 us, 4.95 TB/s (the
+// sums over slabs 6 more), bound by memory; 512x4096 12, by four rows one after
+// another.  MANY: gates share a slab, and rows side by side are those of different
+// gates, each T threads walking `together` gates of their own.
 template <bool XF, bool HF, int TC, int NT, bool FULL, bool MANY>
 __global__ __launch_bounds__(NT) void residual_norm_backward_kernel(ResidualNormBwdArgs g, Slabs sl) {
   __shared__ float red[32];
