@@ -360,6 +360,13 @@ def fp8_linear_act_backward(dy, pre, act=ACT_NONE, dz=None, dbias=None, workspac
     return dz, dbias
 
 
+def _nothing(*stats):
+    """The statistics of rows without a column, which the library leaves as they are: 0 / 0."""
+    for t in stats:
+        if t is not None:
+            t.fill_(math.nan)
+
+
 def fp8_layer_norm(x, weight=None, bias=None, eps=1e-5, out_kind=OUT_BF16, sy=None, stats=False,
                    out=None):
     """Layer norm over the last dimension of x [..., H] (BF16 or FP32):
@@ -375,7 +382,7 @@ def fp8_layer_norm(x, weight=None, bias=None, eps=1e-5, out_kind=OUT_BF16, sy=No
     xt = x.dtype
     n = x.numel()
     H = x.shape[-1]
-    rows = n // H if H else 0
+    rows = n // H if H else math.prod(x.shape[:-1])
     wb_elem = _fit_float(weight, "weight", dev, H, "H elements")
     b_elem = _fit_float(bias, "bias", dev, H, "H elements", None if weight is None else weight.dtype)
     dtype = _out_dtype(out_kind)
@@ -391,6 +398,8 @@ def fp8_layer_norm(x, weight=None, bias=None, eps=1e-5, out_kind=OUT_BF16, sy=No
     if stats:
         mean = x.new_empty(x.shape[:-1], dtype=_F32)
         rstd = torch.empty_like(mean)
+        if not H:
+            _nothing(mean, rstd)
     _lib.call("fp8_layer_norm", x.data_ptr(), 1 if xt is _F32 else 0, _ptr(weight), _ptr(bias),
               wb_elem if weight is not None else b_elem, out.data_ptr(), out_kind, sy_ptr, _ptr(mean),
               _ptr(rstd), rows, H, eps, _stream(x))
@@ -416,7 +425,7 @@ def fp8_layer_norm_backward(dy, x, weight, mean, rstd, dres=None, dx=None, dweig
     xt = x.dtype
     n = x.numel()
     H = x.shape[-1]
-    rows = n // H if H else 0
+    rows = n // H if H else math.prod(x.shape[:-1])
     if dy is None:
         raise ValueError("dy must be a tensor")
     dy_elem = _fit_float(dy, "dy", dev, n, "as many elements as x")
@@ -597,7 +606,7 @@ def fp8_residual_norm(x, weight=None, hidden=None, gate=None, post_weight=None, 
     dev = _on_gpu(x, "x")
     xt = x.dtype
     n, H = x.numel(), x.shape[-1]
-    rows = n // H if H else 0
+    rows = n // H if H else math.prod(x.shape[:-1])
     h_elem = _fit_float(hidden, "hidden", dev, n, "as many elements as x")
     w_elem = _fit_float(weight, "weight", dev, H, "H elements")
     p_elem = _fit_float(post_weight, "post_weight", dev, H, "H elements", None if weight is None else weight.dtype)
@@ -624,6 +633,8 @@ def fp8_residual_norm(x, weight=None, hidden=None, gate=None, post_weight=None, 
         rstd = x.new_empty(x.shape[:-1], dtype=_F32)
         if post_weight is not None:
             post_rstd = torch.empty_like(rstd)
+        if not H:
+            _nothing(rstd, post_rstd)
     _lib.call("fp8_residual_norm", x.data_ptr(), 1 if xt is _F32 else 0, _ptr(hidden), h_elem, _ptr(gate), g_elem,
               gates, _ptr(post_weight), _ptr(weight), w_elem if weight is not None else p_elem, _ptr(stream_out),
               out.data_ptr(), out_kind, sy_ptr, _ptr(scales), _ptr(rstd), _ptr(post_rstd), rows, H, alpha, eps,
@@ -655,7 +666,7 @@ def fp8_residual_norm_backward(dy, r, weight, rstd, hidden=None, gate=None, post
     dev = _on_gpu(r, "r")
     rt = r.dtype
     n, H = r.numel(), r.shape[-1]
-    rows = n // H if H else 0
+    rows = n // H if H else math.prod(r.shape[:-1])
     if dy is None:
         raise ValueError("dy must be a tensor")
     h_elem = _fit_float(dy, "dy", dev, n, "as many elements as r")
