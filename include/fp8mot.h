@@ -522,7 +522,8 @@ int fp8_layer_norm_backward(const void* dy, int dy_elem, const void* x, int x_el
  *    norm alone (r, gate and post_weight then have to be NULL: y of x).
  *  - gate: NULL, or [gates, H] of gate_elem, each row the gate of rows / gates
  *    rows one after another (one for all, one for each sample of a batch of
- *    equal lengths, one for each row); gates has to divide rows.
+ *    equal lengths, one for each row); gates, up to INT32_MAX, has to divide
+ *    rows.
  *  - post_weight, weight: [H] of w_elem; weight NULL: ones.  alpha finite.
  *  - rstd, post_rstd: FP32 [rows] for the backward pass, or NULL.
  *  - r may be x itself (the stream is then updated in place), and y x without

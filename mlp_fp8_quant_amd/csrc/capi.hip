@@ -115,6 +115,8 @@ constexpr int64_t kMaxColumns = int64_t(1) << 26;
 bool rows_ok(int64_t rows, int64_t cols) {
   return rows >= 0 && cols >= 0 && rows <= INT32_MAX && cols <= kMaxColumns;
 }
+// (no rows are divided by any number of gates: sizes and launches count them)
+bool gates_ok(int64_t rows, int64_t gates) { return gates >= 1 && gates <= INT32_MAX && rows % gates == 0; }
 int64_t elem_bytes(int e) { return e == FP8MOT_ELEM_F32 ? 4 : 2; }
 // Blocks of 128 that cover n, and the columns of a row of n codes with its padding.
 int64_t blocks128(int64_t n) { return (n + 127) / 128; }
@@ -515,7 +517,7 @@ int fp8_residual_norm(const void* x, int x_elem, const void* hidden, int h_elem,
   if (!rows_ok(rows, H) || !std::isfinite(eps) || eps < 0.0f || !std::isfinite(alpha)) return FP8MOT_ERR_INVALID_ARG;
   if (hidden == nullptr && rows > 0 && H > 0 && (gate != nullptr || post_weight != nullptr || r != nullptr))
     return FP8MOT_ERR_INVALID_ARG;
-  if (gate != nullptr && (gates < 1 || rows % gates != 0)) return FP8MOT_ERR_INVALID_ARG;
+  if (gate != nullptr && !gates_ok(rows, gates)) return FP8MOT_ERR_INVALID_ARG;
   if (rows == 0 || H == 0) return FP8MOT_OK;
   const bool block = out_kind == FP8MOT_OUT_FP8_BLOCK;
   if (x == nullptr || y == nullptr || (hidden != nullptr && r == nullptr) || (block && d_scales == nullptr))
@@ -554,7 +556,7 @@ int fp8_residual_norm(const void* x, int x_elem, const void* hidden, int h_elem,
 }
 
 size_t fp8_residual_norm_backward_workspace(int64_t rows, int64_t H, int64_t gates) {
-  if (!rows_ok(rows, H) || gates < 1 || rows % gates != 0) return 0;
+  if (!rows_ok(rows, H) || !gates_ok(rows, gates)) return 0;
   return (size_t)residual_norm_backward_floats(rows, H, gates) * sizeof(float);
 }
 
@@ -569,7 +571,7 @@ int fp8_residual_norm_backward(const void* dy, const void* r, int r_elem, const 
       !std::isfinite(alpha))
     return FP8MOT_ERR_INVALID_ARG;
   if (gate == nullptr) gates = 1;
-  if (gates < 1 || rows % gates != 0) return FP8MOT_ERR_INVALID_ARG;
+  if (!gates_ok(rows, gates)) return FP8MOT_ERR_INVALID_ARG;
   if (H == 0) return FP8MOT_OK;
   if ((dgate != nullptr && gate == nullptr) || (dpost_weight != nullptr && post_weight == nullptr))
     return FP8MOT_ERR_INVALID_ARG;
